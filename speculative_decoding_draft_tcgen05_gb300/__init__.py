@@ -1,8 +1,9 @@
 """DFlash 2 path selector on one GB300 GPU: Python binding of libdflash_select.
 
 The functions below have the names of the C entry points declared in
-``include/dflash_select.h`` and ``include/dflash_conv2.h`` and only marshal
-arguments: every step of the
+``include/dflash_select.h`` and ``include/dflash_conv2.h`` (those of
+``include/dflash_paged.h`` are in ``paged.py`` and available here too) and only
+marshal arguments: every step of the
 selector runs in the library's CUDA kernels. PyTorch supplies device memory
 and streams. If the library has not been built the calls raise; there is no
 fallback.
@@ -85,6 +86,7 @@ def lib() -> ctypes.CDLL:
             L.dflash_conv2_sync_status.argtypes = [P, P]
             L.dflash_conv2_destroy.argtypes = [P]
             L.dflash_last_error.restype = ctypes.c_char_p
+            paged.declare(L)
             for f in ("dflash_select_init", "dflash_select_run", "dflash_verify_prefix", "dflash_select_step_host",
                       "dflash_select_sync_status", "dflash_select_profile", "dflash_select_profile_read",
                       "dflash_select_destroy", "dflash_lmhead_topk_noalloc", "dflash_select_run_sampled",
@@ -519,3 +521,9 @@ def dflash_selftest_wait_timeout(device_status, stream=None):
     import torch
     _check(lib().dflash_selftest_wait_timeout(_ptr(device_status, torch.int32, "device_status"), _stream(stream)),
            "dflash_selftest_wait_timeout")
+
+
+from . import paged  # noqa: E402
+from .paged import (DFLASH_BF16, DFLASH_E4M3, DFLASH_FP16, PagedAttention, PagedBatch, PagedCache,  # noqa: E402,F401
+                    QkTransform, dflash_paged_append, dflash_paged_attend, dflash_paged_config, dflash_paged_destroy,
+                    dflash_paged_init, dflash_paged_sync_status, dflash_qk_norm_rope)

@@ -1,0 +1,79 @@
+// Launch interfaces of the paged-attention kernels (host side) and the launch
+// parameters that they share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dflash_paged.h"
+#include "kernels.h"
+
+namespace dfl {
+
+// Bit of the device error word beside those of kernels.h: a page id, a length
+// or a position outside its table.
+enum : int { DEV_ERR_PLACE = 4 };
+
+// ---- norm + rotation (+ cache append) ----
+struct PrepRows {  // [tokens, heads, head_dim] in and out; strides in elements
+    const void *in = nullptr;
+    void *out = nullptr;
+    int64_t in_ts = 0, in_hs = 0, out_ts = 0, out_hs = 0;
+    const void *weight = nullptr;
+    int heads = 0;
+};
+
+struct PrepParams {
+    PrepRows q, k, v;  // out of k and v unused where the cache takes them
+    int tokens = 0;
+    const float *table = nullptr;
+    int positions_n = 0, rotary = 0, interleaved = 0;
+    float eps = 0.f;
+    const int32_t *positions = nullptr;
+    // cache (append only)
+    int append = 0, fp8 = 0;
+    dflash_paged_cache cache = {};
+    dflash_paged_batch batch = {};
+    int page = 0;
+    int *err = nullptr;
+};
+cudaError_t launch_prep(const PrepParams &p, int head_dim, int dtype, cudaStream_t s);
+
+// ---- attention ----
+struct AttendParams {
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    const void *k, *v;
+    int64_t page_stride, slot_stride, head_stride;
+    const int32_t *cu, *lens, *table;
+    int64_t table_stride;
+    int table_cols, num_pages;
+    int B, tokens, kv_heads, group, page;  // group = query heads per key/value head
+    int causal, window;            // window 0: none
+    float scale_log2;              // score scale * log2(e) (* the keys' scale)
+    float v_scale;
+    // Workspace: CTA c's partial results in slots 2c (a piece that continues an
+    // earlier CTA's item) and 2c + 1 (one that a later CTA continues), and the
+    // merge's work list, entry c for the item that CTA c begins and CTA c + 1
+    // continues.
+    float *part_o;    // [2 * grid][rows][head_dim]
+    float2 *part_ml;  // [2 * grid][rows] running maximum (log2) and sum
+    int4 *merge;      // [2 * grid]
+    int *err;
+};
+
+// Rows of a work item and keys of a work unit of the two kernels.
+constexpr int kRowsUnit = 64;    // few rows: 16 or 32 rows, units of 64 keys
+constexpr int kTileRows = 256;   // many rows
+constexpr int kTileUnit = 128;
+
+cudaError_t prepare_attend_rows(int smem_optin);
+cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int num_sms,
+                               cudaStream_t s);
+// Joins the partial results of the split items (rows per item, `grid` CTAs of the attention launch).
+cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s);
+
+}  // namespace dfl

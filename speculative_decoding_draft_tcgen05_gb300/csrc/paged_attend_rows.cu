@@ -1,0 +1,592 @@
+// Attention of few rows (single tokens and draft blocks) over a paged cache,
+// and the merge of split items.
+#include "paged.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kRowsThreads = 128;  // 4 warps, 2 CTAs per SM
+constexpr int kRowsWarps = kRowsThreads / 32;
+constexpr int kRowsRing = 24 * 1024;  // ring bytes of one warp
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 values in the low 16 bits -> two fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t x)
+{
+    uint32_t y;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Shapes of one variant. CH: 16-byte chunks of a key's row; a stage of a
+// warp's ring holds 16 keys and their values.
+template <int D, bool FP8>
+struct RowsShape {
+    static constexpr int ROW = D * (FP8 ? 1 : 2);
+    static constexpr int CH = ROW / 16;
+    static constexpr int TILE = 16 * ROW;
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int STAGES = (kRowsRing / STAGE < 6) ? kRowsRing / STAGE : 6;
+    // Physical chunk of (row, chunk): 8 rows at one chunk (an ldmatrix phase)
+    // and the 16 of a half-row write fall into distinct banks.
+    __device__ static uint32_t at(int row, int c)
+    {
+        const int x = CH >= 8 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & (CH - 1)));
+        return static_cast<uint32_t>(row * ROW + x * 16);
+    }
+};
+
+template <int D, int MT>
+constexpr int rows_q_bytes()
+{
+    return MT * 16 * D * 2;
+}
+
+constexpr int kRowsPad = 8;  // floats between merge rows
+
+// ---------------------------------------------------------------------------
+// One CTA walks its even share of all (sequence, key/value head, row tile)
+// items' keys. Of every unit of 64 keys warp w takes keys 16 w .. 16 w + 15,
+// with its own ring of asynchronous copies, its own running maximum and sum
+// and its own accumulator over all MT * 16 rows: warps meet only at the end of
+// a piece, where their four results are joined in shared memory. What a CTA
+// does not finish goes to the workspace for the merge kernel.
+//
+// For every key the rows of a group (query heads that share it, times the
+// new tokens) use the same copy in shared memory, so the cache is read once.
+// The limit is HBM: 2 * D * 2 bytes per key against 4 * D * rows operations,
+// 32 op/byte at 32 rows, which mma.sync sustains; the tensor memory path would
+// leave 3/4 or more of its 128-row tiles empty here.
+// ---------------------------------------------------------------------------
+template <int D, int MT, typename QT, bool FP8>
+__global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
+{
+    using CT = typename std::conditional<FP8, __half, QT>::type;  // type of the matrix products
+    using SH = RowsShape<D, FP8>;
+    constexpr int R = MT * 16, S = SH::STAGES, CH = SH::CH;
+    constexpr int QCH = D * 2 / 16;  // chunks of a query row
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float q_undo[R];  // FP8: what a query row was scaled by, undone
+    __shared__ float2 row_ml[kRowsWarps][R];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t q_s = smem_u32(smem);
+    const uint32_t ring = q_s + rows_q_bytes<D, MT>() + warp * kRowsRing;
+    uint8_t *const ring_ptr = smem + rows_q_bytes<D, MT>();
+    auto q_at = [](int row, int c) { return static_cast<uint32_t>(row * (D * 2) + ((c ^ (row & 7)) * 16)); };
+
+    pdl_trigger();
+    pdl_wait();
+    const PagedPlan plan = paged_plan<kRowsThreads>(p, R, kRowsUnit);
+    PagedWalk walk;
+    walk.start(p, plan, R, kRowsUnit);
+    int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
+    if (walk.left > 0) {
+        for (;;) {
+            const PagedPiece &pc = walk.pc;
+            const PagedSeq &s = pc.s;
+            const int rows = min(R, s.n * p.group - pc.rt * R);  // real rows of this item
+            const int base = s.len - s.n;
+
+            // ---- queries to shared memory, whole 16-byte pieces; rows past the item's are zero
+            __syncthreads();
+            for (int i = tid; i < R * QCH; i += kRowsThreads) {
+                const int r = i / QCH, c = i % QCH;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) {
+                    const int rr = pc.rt * R + r, t = rr / p.group, g = rr % p.group;
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) +
+                                                         (s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c);
+                }
+                if constexpr (FP8) {
+                    // The products run in fp16: a power of two per row brings the row's largest
+                    // value to [2^8, 2^9), so bf16 queries of any size fit (and f16 ones stay exact).
+                    float f[8];
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 a = unpack2<QT>(u[k]);
+                        f[2 * k] = a.x;
+                        f[2 * k + 1] = a.y;
+                        top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+                    }
+#pragma unroll
+                    for (int o = QCH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal
+                    e = max(-100, min(100, e));
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+                    v = make_uint4(pack2<CT>(f[0] * up, f[1] * up), pack2<CT>(f[2] * up, f[3] * up),
+                                   pack2<CT>(f[4] * up, f[5] * up), pack2<CT>(f[6] * up, f[7] * up));
+                    if (c == 0) q_undo[r] = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
+                }
+                *reinterpret_cast<uint4 *>(smem + q_at(r, c)) = v;
+            }
+            __syncthreads();
+
+            // ---- limits of this thread's rows (8 h + lane / 4 of row tile mt): keys in (after, upto]
+            int upto[2 * MT], after[2 * MT];
+            float factor[2 * MT];
+            int most_after = -1, least_upto = 0x7FFFFFFF;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                const int place = base + (pc.rt * R + r) / p.group;
+                upto[i] = r < rows ? (p.causal ? min(place, s.len - 1) : s.len - 1) : -1;
+                after[i] = p.window > 0 ? place - p.window : -1;
+                if (r < rows) {
+                    least_upto = min(least_upto, upto[i]);
+                    most_after = max(most_after, after[i]);
+                }
+                factor[i] = p.scale_log2 * (FP8 ? q_undo[r] : 1.f);
+            }
+            least_upto = __reduce_min_sync(0xFFFFFFFFu, least_upto);
+            most_after = __reduce_max_sync(0xFFFFFFFFu, most_after);
+
+            // ---- the ring: unit j of the piece, this warp's 16 keys
+            const int n_units = pc.e - pc.a, first = pc.it.u0 + pc.a;
+            const int lo = pc.it.lo, hi = pc.it.hi;
+            const uint8_t *kb = static_cast<const uint8_t *>(p.k);
+            const uint8_t *vb = static_cast<const uint8_t *>(p.v);
+            constexpr int ES = FP8 ? 1 : 2;
+            int pages = -1;  // lane l: the page of unit pages_from + l
+            int pages_from = -(1 << 30);
+            auto issue = [&](int j) {
+                if (j < n_units) {
+                    if (j - pages_from >= 32) {
+                        pages_from = j;
+                        const int key = (first + j + lane) * kRowsUnit + 16 * warp;
+                        pages = -1;
+                        if (j + lane < n_units && key < hi && key + 16 > lo) {
+                            pages = __ldg(p.table + pc.b * p.table_stride + key / p.page);
+                            if (pages < 0 || pages >= p.num_pages) {
+                                pages = -1;
+                                atomicOr(p.err, DEV_ERR_PLACE);
+                            }
+                        }
+                    }
+                    const int page = __shfl_sync(0xFFFFFFFFu, pages, j - pages_from);
+                    const int key = (first + j) * kRowsUnit + 16 * warp;
+                    const int64_t at = page * p.page_stride + (key % p.page) * p.slot_stride + pc.kvh * p.head_stride;
+                    const uint32_t dst = ring + (j % S) * SH::STAGE;
+#pragma unroll
+                    for (int i = 0; i < 16 * CH / 32; ++i) {
+                        const int row = (32 * i + lane) / CH, c = (32 * i + lane) % CH;
+                        const bool ok = page >= 0 && key + row >= lo && key + row < hi;
+                        const int64_t o = ok ? (at + row * p.slot_stride) * ES + 16 * c : 0;
+                        cp_async16(dst + SH::at(row, c), kb + o, ok);
+                        cp_async16(dst + SH::TILE + SH::at(row, c), vb + o, ok);
+                    }
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int j = 0; j < S - 1; ++j) issue(j);
+
+            float o[MT][D / 8][4];
+            float m[2 * MT], l[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
+
+            for (int j = 0; j < n_units; ++j) {
+                cp_async_wait<S - 2>();
+                __syncwarp();
+                issue(j + S - 1);
+                const uint32_t ks = ring + (j % S) * SH::STAGE, vs = ks + SH::TILE;
+                const int key0 = (first + j) * kRowsUnit + 16 * warp;
+                if (key0 >= hi || key0 + 16 <= lo) continue;  // no row sees these keys
+
+                // ---- scores
+                float sc[MT][2][4];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sc[i][n][k] = 0.f;
+#pragma unroll
+                for (int c2 = 0; c2 < (FP8 ? D / 32 : D / 16); ++c2) {
+                    uint32_t kf[4];
+                    if constexpr (FP8) {
+                        // matrices: keys 0-7 and 8-15 of chunks 2 c2 and 2 c2 + 1. A thread gets 4
+                        // consecutive values of a key; they stand for k = 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+                        // of the product (the queries below are read in the same order).
+                        ldsm4(ks + SH::at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c2 + (lane >> 4)), kf);
+#pragma unroll
+                        for (int hc = 0; hc < 2; ++hc) {
+                            const uint32_t b00 = e4m3x2_to_h2(kf[2 * hc]), b01 = e4m3x2_to_h2(kf[2 * hc] >> 16);
+                            const uint32_t b10 = e4m3x2_to_h2(kf[2 * hc + 1]), b11 = e4m3x2_to_h2(kf[2 * hc + 1] >> 16);
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                uint32_t a[4];
+                                const int r = 16 * i + (lane >> 2);
+                                // values 16 (2 c2 + hc) + 4 (lane % 4) .. + 3 of rows r and r + 8
+                                const int c = 2 * (2 * c2 + hc) + ((lane & 3) >> 1);
+                                const uint2 x = *reinterpret_cast<const uint2 *>(smem + q_at(r, c) + 8 * (lane & 1));
+                                const uint2 y = *reinterpret_cast<const uint2 *>(smem + q_at(r + 8, c) + 8 * (lane & 1));
+                                a[0] = x.x;
+                                a[1] = y.x;
+                                a[2] = x.y;
+                                a[3] = y.y;
+                                mma16816<CT>(sc[i][0], a, b00, b01);
+                                mma16816<CT>(sc[i][1], a, b10, b11);
+                            }
+                        }
+                    } else {
+                        ldsm4(ks + SH::at((lane & 7) + (lane >> 4) * 8, 2 * c2 + ((lane >> 3) & 1)), kf);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            uint32_t a[4];
+                            ldsm4(q_s + q_at(16 * i + (lane & 15), 2 * c2 + (lane >> 4)), a);
+                            mma16816<CT>(sc[i][0], a, kf[0], kf[1]);
+                            mma16816<CT>(sc[i][1], a, kf[2], kf[3]);
+                        }
+                    }
+                }
+
+                // ---- scale, mask, running maximum
+                const bool whole = key0 > most_after && key0 + 15 <= least_upto;
+                float top[2 * MT];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    top[i] = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float &x = sc[i >> 1][n][2 * (i & 1) + k];
+                            x *= factor[i];
+                            if (!whole) {
+                                const int key = key0 + 8 * n + 2 * (lane & 3) + k;
+                                if (key > upto[i] || key <= after[i]) x = -INFINITY;
+                            }
+                            top[i] = fmaxf(top[i], x);
+                        }
+                }
+                // A row's maximum moves only when it grew by more than 2^8 (fp32 sums and the 16-bit
+                // weights stand a stale one: the weights are at most 256): the accumulator is then
+                // hardly ever rescaled. The first unit sets it.
+                bool grew = false;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+                    grew |= top[i] > m[i] + 8.f;
+                }
+                if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i) {
+                        const float now = fmaxf(m[i], top[i]);
+                        const float f = now == -INFINITY ? 1.f : ex2(m[i] - now);
+                        m[i] = now;
+                        l[i] *= f;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[i >> 1][n][2 * (i & 1)] *= f;
+                            o[i >> 1][n][2 * (i & 1) + 1] *= f;
+                        }
+                    }
+                }
+
+                // ---- weights, rounded to the values' 16-bit type for the product; the sum takes them unrounded
+                uint32_t pf[MT][4];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const float mm = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float a = ex2(sc[i >> 1][n][2 * (i & 1)] - mm);
+                        const float b = ex2(sc[i >> 1][n][2 * (i & 1) + 1] - mm);
+                        l[i] += a + b;
+                        pf[i >> 1][2 * n + (i & 1)] = pack2<CT>(a, b);
+                    }
+                }
+
+                // ---- values
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t vf[4];  // keys 0-7 and 8-15 of chunks c and c + 1
+                    ldsm4_t(vs + SH::at((lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), vf);
+                    if constexpr (FP8) {
+                        // a thread holds values 2 (lane / 4), + 1 of keys 2 j, 2 j + 1: the even values of a
+                        // chunk make one 8-column tile, the odd ones the next
+#pragma unroll
+                        for (int hc = 0; hc < 2; ++hc) {
+                            const uint32_t x = vf[2 * hc], y = vf[2 * hc + 1];
+                            const uint32_t e0 = e4m3x2_to_h2(__byte_perm(x, 0, 0x4420)), e1 = e4m3x2_to_h2(__byte_perm(y, 0, 0x4420));
+                            const uint32_t d0 = e4m3x2_to_h2(__byte_perm(x, 0, 0x4431)), d1 = e4m3x2_to_h2(__byte_perm(y, 0, 0x4431));
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                mma16816<CT>(o[i][2 * (c + hc)], pf[i], e0, e1);
+                                mma16816<CT>(o[i][2 * (c + hc) + 1], pf[i], d0, d1);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            mma16816<CT>(o[i][c], pf[i], vf[0], vf[1]);
+                            mma16816<CT>(o[i][c + 1], pf[i], vf[2], vf[3]);
+                        }
+                    }
+                }
+            }
+
+            // ---- join the four warps: each leaves its accumulator in its own ring
+            cp_async_wait<0>();
+            __syncwarp();
+            constexpr int OS = D + kRowsPad;
+            float *mine = reinterpret_cast<float *>(ring_ptr + warp * kRowsRing);
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+                const int r = 8 * i + (lane >> 2);
+                if ((lane & 3) == 0) row_ml[warp][r] = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    const float2 v = make_float2(o[i >> 1][n][2 * (i & 1)], o[i >> 1][n][2 * (i & 1) + 1]);
+                    if constexpr (FP8) {  // tile 2 c + h holds values 16 c + 2 col + h
+                        mine[r * OS + 16 * (n >> 1) + 4 * (lane & 3) + (n & 1)] = v.x;
+                        mine[r * OS + 16 * (n >> 1) + 4 * (lane & 3) + 2 + (n & 1)] = v.y;
+                    } else {
+                        *reinterpret_cast<float2 *>(mine + r * OS + 8 * n + 2 * (lane & 3)) = v;
+                    }
+                }
+            }
+            __syncthreads();
+            const bool begins = pc.a == 0, ends = pc.e == pc.it.units;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0);
+            for (int i = tid; i < rows * (D / 8); i += kRowsThreads) {
+                const int r = i / (D / 8), c = i % (D / 8);
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, row_ml[w][r].x);
+                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kRowsWarps; ++w) {
+                    const float2 ml = row_ml[w][r];
+                    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                    L += f * ml.y;
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        reinterpret_cast<const float *>(ring_ptr + w * kRowsRing) + r * OS + 8 * c);
+                    const float4 x = src[0], y = src[1];
+                    acc[0] = fmaf(f, x.x, acc[0]);
+                    acc[1] = fmaf(f, x.y, acc[1]);
+                    acc[2] = fmaf(f, x.z, acc[2]);
+                    acc[3] = fmaf(f, x.w, acc[3]);
+                    acc[4] = fmaf(f, y.x, acc[4]);
+                    acc[5] = fmaf(f, y.y, acc[5]);
+                    acc[6] = fmaf(f, y.z, acc[6]);
+                    acc[7] = fmaf(f, y.w, acc[7]);
+                }
+                if (begins && ends) {
+                    const int rr = pc.rt * R + r, t = s.t0 + rr / p.group, hd = pc.kvh * p.group + rr % p.group;
+                    const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
+                    uint4 v = make_uint4(pack2<QT>(acc[0] * inv, acc[1] * inv), pack2<QT>(acc[2] * inv, acc[3] * inv),
+                                         pack2<QT>(acc[4] * inv, acc[5] * inv), pack2<QT>(acc[6] * inv, acc[7] * inv));
+                    *reinterpret_cast<uint4 *>(static_cast<QT *>(p.out) + t * p.o_ts + hd * p.o_hs + 8 * c) = v;
+                    if (c == 0 && p.lse)
+                        p.lse[static_cast<int64_t>(t) * p.kv_heads * p.group + hd] =
+                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + (slot * R + r) * D + 8 * c);
+                    dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    if (c == 0) p.part_ml[slot * R + r] = make_float2(M, L);
+                }
+            }
+            if (begins && !ends) {  // this CTA's last piece
+                const int64_t last = plan.end - walk.left - pc.a + pc.it.units - 1;
+                merge0 = make_int4(s.t0, pc.rt * R, rows, pc.kvh);
+                merge1 = make_int4(paged_owner(last, plan.total, plan.ctas) - static_cast<int>(blockIdx.x) + 1, 0, 0, 0);
+            }
+            if (!walk.next(p, R, kRowsUnit)) break;
+        }
+    }
+    if (tid == 0) {
+        p.merge[2 * blockIdx.x] = merge0;
+        p.merge[2 * blockIdx.x + 1] = merge1;
+    }
+}
+
+// Joins the partial results of the item that CTA blockIdx.x began and its
+// successors finished, one row per warp, in CTA order (so always the same sum).
+constexpr int kMergeWarps = 4;
+
+template <int D, typename QT>
+__global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * kMergeWarps + warp;
+    const int64_t c0 = blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    const int parts = p.merge[2 * c0 + 1].x;
+    if (parts == 0) return;
+    const int4 item = p.merge[2 * c0];  // first token row, first row, rows, key/value head
+    if (r >= item.z) return;
+    // slot of part i: 2 c0 + 1 for the beginning, 2 (c0 + i) after it
+    float M = -INFINITY;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[(2 * (c0 + i) + (i == 0)) * R + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    float L = 0.f, acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const int64_t row = (2 * (c0 + i) + (i == 0)) * R + r;
+        const float2 ml = p.part_ml[row];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        L = fmaf(f, ml.y, L);
+        const float *src = p.part_o + row * D + V * lane;
+        if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(src);
+            acc[0] = fmaf(f, x.x, acc[0]);
+            acc[1] = fmaf(f, x.y, acc[1]);
+            acc[2] = fmaf(f, x.z, acc[2]);
+            acc[3] = fmaf(f, x.w, acc[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(src);
+            acc[0] = fmaf(f, x.x, acc[0]);
+            acc[1] = fmaf(f, x.y, acc[1]);
+        }
+    }
+    const int rr = item.y + r, t = item.x + rr / p.group, hd = item.w * p.group + rr % p.group;
+    const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
+    QT *dst = static_cast<QT *>(p.out) + t * p.o_ts + hd * p.o_hs + V * lane;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack2<QT>(acc[0] * inv, acc[1] * inv), pack2<QT>(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack2<QT>(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse)
+        p.lse[static_cast<int64_t>(t) * p.kv_heads * p.group + hd] =
+            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+}
+
+template <int D, int MT>
+constexpr size_t rows_smem()
+{
+    return rows_q_bytes<D, MT>() + kRowsWarps * kRowsRing;
+}
+
+// Calls f with the kernel of a variant and its shared memory.
+template <typename F>
+cudaError_t rows_variant(int head_dim, int dtype, int fp8, int rows, F &&f)
+{
+    using B = __nv_bfloat16;
+    using H = __half;
+#define DFL_ROWS(D, MT)                                                                                            \
+    if (head_dim == D && rows == 16 * MT) {                                                                        \
+        if (dtype == DFLASH_BF16 && !fp8) return f(attend_rows_kernel<D, MT, B, false>, rows_smem<D, MT>());       \
+        if (dtype == DFLASH_BF16) return f(attend_rows_kernel<D, MT, B, true>, rows_smem<D, MT>());                \
+        if (!fp8) return f(attend_rows_kernel<D, MT, H, false>, rows_smem<D, MT>());                               \
+        return f(attend_rows_kernel<D, MT, H, true>, rows_smem<D, MT>());                                          \
+    }
+    DFL_ROWS(128, 1)
+    DFL_ROWS(128, 2)
+    DFL_ROWS(64, 1)
+    DFL_ROWS(64, 2)
+#undef DFL_ROWS
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t prepare_attend_rows(int smem_optin)
+{
+    for (int d : {64, 128})
+        for (int dt : {DFLASH_BF16, DFLASH_FP16})
+            for (int fp8 : {0, 1})
+                for (int rows : {16, 32}) {
+                    const cudaError_t e = rows_variant(d, dt, fp8, rows, [&](auto kern, size_t) {
+                        return set_max_dynamic_smem(kern, smem_optin);
+                    });
+                    if (e != cudaSuccess) return e;
+                }
+    return cudaSuccess;
+}
+
+cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int num_sms,
+                               cudaStream_t s)
+{
+    return rows_variant(head_dim, dtype, fp8, rows, [&](auto kern, size_t smem) {
+        return launch_ex(kern, dim3(2 * num_sms), dim3(kRowsThreads), smem, s, 1, p);
+    });
+}
+
+cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s)
+{
+    const dim3 g(grid, (rows + kMergeWarps - 1) / kMergeWarps), b(kMergeWarps * 32);
+    if (head_dim == 128)
+        return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<128, __nv_bfloat16>, g, b, 0, s, 1, p, rows)
+                                    : launch_ex(attend_merge_kernel<128, __half>, g, b, 0, s, 1, p, rows);
+    return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<64, __nv_bfloat16>, g, b, 0, s, 1, p, rows)
+                                : launch_ex(attend_merge_kernel<64, __half>, g, b, 0, s, 1, p, rows);
+}
+
+}  // namespace dfl
