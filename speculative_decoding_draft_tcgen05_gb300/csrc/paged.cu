@@ -9,6 +9,9 @@
 
 namespace dfl {
 dflash_status host_fail(dflash_status st, const char *msg);
+dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, bool bf16, int head_dim, int slots, int heads,
+                                   int64_t pages, int64_t slot_stride, int64_t head_stride, int64_t page_stride,
+                                   int box_rows);
 }
 
 struct dflash_paged_ctx {
@@ -169,11 +172,13 @@ extern "C" dflash_status dflash_paged_init(const dflash_paged_config *cfg, void 
         return paged_fail(DFLASH_ERR_UNSUPPORTED, "built for sm_103 (GB300); device is sm_%lld%lld", major, minor);
     }
     // Partial results: two slots per CTA of the larger of the two kernels' grids.
-    const size_t rows = 2 * static_cast<size_t>(c->num_sms) * 2 * 32;
+    const size_t rows = 2 * static_cast<size_t>(c->num_sms) * dfl::kTileRows;
+    static_assert(dfl::kTileRows >= 2 * 32, "two CTAs of up to 32 rows per SM, or one of kTileRows");
     const size_t o_bytes = rows * cfg->head_dim * sizeof(float), ml_bytes = rows * sizeof(float2);
     const size_t merge_bytes = 2 * static_cast<size_t>(c->num_sms) * 2 * sizeof(int4);
     const size_t total = o_bytes + ml_bytes + merge_bytes + 256;
-    if (dfl::prepare_attend_rows(smem_optin) != cudaSuccess || cudaMalloc(&c->block, total) != cudaSuccess) {
+    if (dfl::prepare_attend_rows(smem_optin) != cudaSuccess || dfl::prepare_attend_tile(smem_optin) != cudaSuccess ||
+        cudaMalloc(&c->block, total) != cudaSuccess) {
         delete c;
         cudaGetLastError();
         return paged_fail(DFLASH_ERR_CUDA, "setting up paged attention failed (workspace of %lld bytes)", total);
@@ -274,9 +279,28 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     p.merge = h->merge;
     p.err = h->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int rows = static_cast<int64_t>(batch->max_tokens) * p.group <= 16 ? 16 : 32;
-    cudaError_t e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, h->num_sms, s);
-    if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, 2 * h->num_sms, s);
+    const int64_t most_rows = static_cast<int64_t>(batch->max_tokens) * p.group;
+    cudaError_t e;
+    int rows, grid;
+    if (most_rows > 32 && !fp8) {
+        CUtensorMap tm_k, tm_v;
+        const int box = dfl::tile_box_rows(p.page);
+        const bool bf16 = h->cfg.dtype == DFLASH_BF16;
+        dflash_status st2 = dfl::host_make_tmap_pages(&tm_k, p.k, bf16, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
+                                                      p.slot_stride, p.head_stride, p.page_stride, box);
+        if (st2 == DFLASH_OK)
+            st2 = dfl::host_make_tmap_pages(&tm_v, p.v, bf16, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
+                                            p.slot_stride, p.head_stride, p.page_stride, box);
+        if (st2 != DFLASH_OK) return st2;
+        rows = dfl::kTileRows;
+        grid = h->num_sms;
+        e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, grid, s);
+    } else {
+        rows = most_rows <= 16 ? 16 : 32;
+        grid = 2 * h->num_sms;
+        e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, grid, s);
+    }
+    if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, s);
     if (e != cudaSuccess) return paged_fail(DFLASH_ERR_CUDA, "attention: a launch failed (error %lld)", e);
     return DFLASH_OK;
 }

@@ -71,8 +71,14 @@ constexpr int kTileRows = 256;   // many rows
 constexpr int kTileUnit = 128;
 
 cudaError_t prepare_attend_rows(int smem_optin);
-cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int num_sms,
+cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int grid,
                                cudaStream_t s);
+cudaError_t prepare_attend_tile(int smem_optin);
+// Rows of one box of a page's tensor map: the most that divide a page and a tile.
+int tile_box_rows(int page);
+// tm_k, tm_v: host_make_tmap_pages() with boxes of tile_box_rows() slots.
+cudaError_t launch_attend_tile(const AttendParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int head_dim,
+                               int dtype, int grid, cudaStream_t s);
 // Joins the partial results of the split items (rows per item, `grid` CTAs of the attention launch).
 cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s);
 

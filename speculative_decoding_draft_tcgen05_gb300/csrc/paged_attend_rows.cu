@@ -571,11 +571,11 @@ cudaError_t prepare_attend_rows(int smem_optin)
     return cudaSuccess;
 }
 
-cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int num_sms,
+cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int grid,
                                cudaStream_t s)
 {
     return rows_variant(head_dim, dtype, fp8, rows, [&](auto kern, size_t smem) {
-        return launch_ex(kern, dim3(2 * num_sms), dim3(kRowsThreads), smem, s, 1, p);
+        return launch_ex(kern, dim3(grid), dim3(kRowsThreads), smem, s, 1, p);
     });
 }
 
