@@ -14,12 +14,17 @@ dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, bool bf16, 
                                    int box_rows);
 }
 
+#ifndef DFL_TILE_MIN_ROWS
+#define DFL_TILE_MIN_ROWS 32
+#endif
+
 struct dflash_paged_ctx {
     dflash_paged_config cfg;
     int dev = 0, num_sms = 0;
     float *part_o = nullptr;
     float2 *part_ml = nullptr;
     int4 *merge = nullptr;
+    unsigned *ticket = nullptr;
     int *err = nullptr;
     void *block = nullptr;  // the one allocation
 };
@@ -176,7 +181,8 @@ extern "C" dflash_status dflash_paged_init(const dflash_paged_config *cfg, void 
     static_assert(dfl::kTileRows >= 2 * 32, "two CTAs of up to 32 rows per SM, or one of kTileRows");
     const size_t o_bytes = rows * cfg->head_dim * sizeof(float), ml_bytes = rows * sizeof(float2);
     const size_t merge_bytes = 2 * static_cast<size_t>(c->num_sms) * 2 * sizeof(int4);
-    const size_t total = o_bytes + ml_bytes + merge_bytes + 256;
+    const size_t ticket_bytes = 2 * static_cast<size_t>(c->num_sms) * dfl::kTicketWarps * sizeof(unsigned);
+    const size_t total = o_bytes + ml_bytes + merge_bytes + ticket_bytes + 256;
     if (dfl::prepare_attend_rows(smem_optin) != cudaSuccess || dfl::prepare_attend_tile(smem_optin) != cudaSuccess ||
         cudaMalloc(&c->block, total) != cudaSuccess) {
         delete c;
@@ -187,11 +193,12 @@ extern "C" dflash_status dflash_paged_init(const dflash_paged_config *cfg, void 
     c->part_o = reinterpret_cast<float *>(at);
     c->part_ml = reinterpret_cast<float2 *>(at + o_bytes);
     c->merge = reinterpret_cast<int4 *>(at + o_bytes + ml_bytes);
-    c->err = reinterpret_cast<int *>(at + o_bytes + ml_bytes + merge_bytes);
-    if (cudaMemsetAsync(c->err, 0, sizeof(int), static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    c->ticket = reinterpret_cast<unsigned *>(at + o_bytes + ml_bytes + merge_bytes);
+    c->err = reinterpret_cast<int *>(at + o_bytes + ml_bytes + merge_bytes + ticket_bytes);
+    if (cudaMemsetAsync(c->ticket, 0, ticket_bytes + 256, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaFree(c->block);
         delete c;
-        return paged_fail(DFLASH_ERR_CUDA, "clearing the device error word failed");
+        return paged_fail(DFLASH_ERR_CUDA, "clearing the workspace failed");
     }
     *out = c;
     return DFLASH_OK;
@@ -270,6 +277,8 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     p.kv_heads = h->cfg.kv_heads;
     p.group = h->cfg.heads / h->cfg.kv_heads;
     p.page = h->cfg.page_size;
+    p.by_group = dfl::FastDiv(p.group);
+    p.by_page = dfl::FastDiv(p.page);
     p.causal = causal;
     p.window = window;
     p.scale_log2 = scale * 1.44269504088896341f * (fp8 ? cache->k_scale : 1.f);
@@ -277,12 +286,13 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     p.merge = h->merge;
+    p.ticket = h->ticket;
     p.err = h->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t most_rows = static_cast<int64_t>(batch->max_tokens) * p.group;
     cudaError_t e;
     int rows, grid;
-    if (most_rows > 32 && !fp8) {
+    if (most_rows > DFL_TILE_MIN_ROWS && !fp8) {
         CUtensorMap tm_k, tm_v;
         const int box = dfl::tile_box_rows(p.page);
         const bool bf16 = h->cfg.dtype == DFLASH_BF16;

@@ -63,7 +63,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const AttendParams &p, int b)
     PagedSeq s;
     s.t0 = min(max(__ldg(p.cu + b), 0), p.tokens);
     s.n = min(max(__ldg(p.cu + b + 1), s.t0), p.tokens) - s.t0;
-    const int64_t cap = static_cast<int64_t>(p.table_cols) * p.page;
+    // (tiles may run past the end, so places stay clear of 2^31)
+    const int64_t cap = min(static_cast<int64_t>(p.table_cols) * p.page, (int64_t(1) << 31) - 4096);
     const int len = __ldg(p.lens + b);
     s.len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
     return s;
@@ -81,7 +82,7 @@ struct PagedItem {
 __device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const PagedSeq &s, int rt, int R, int U)
 {
     const int r0 = rt * R, r1 = min(s.n * p.group, r0 + R);
-    const int ta = r0 / p.group, tb = (r1 - 1) / p.group;
+    const int ta = p.by_group.div(r0), tb = p.by_group.div(r1 - 1);
     const int base = s.len - s.n;
     PagedItem it;
     it.hi = p.causal ? min(s.len, max(0, base + tb + 1)) : s.len;
@@ -106,34 +107,70 @@ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const Page
 struct PagedPlan {
     int64_t total, begin, end;
     int64_t ctas;  // G
-    int b;        // sequence of unit `begin`
-    int64_t off;  // its offset within that sequence's units
+    int b;         // sequence of unit `begin`
+    int per_head;  // its units per key/value head
+    int64_t off;   // the offset of `begin` within that sequence's units
 };
 
+constexpr int kPlanSeqs = 512;  // sequences whose units are kept in shared memory
+
+// Units per key/value head of a sequence, by one thread or by a whole warp.
+__device__ __forceinline__ int paged_units(const AttendParams &p, const PagedSeq &s, int R, int U)
+{
+    const int nrt = paged_row_tiles(p, s, R);
+    int u = 0;
+    for (int rt = 0; rt < nrt; ++rt) u += paged_item(p, s, rt, R, U).units;
+    return u;
+}
+
+__device__ __forceinline__ int paged_units_warp(const AttendParams &p, const PagedSeq &s, int R, int U, int lane)
+{
+    const int nrt = paged_row_tiles(p, s, R);
+    int u = 0;
+    for (int rt = lane; rt < nrt; rt += 32) u += paged_item(p, s, rt, R, U).units;
+    return __reduce_add_sync(0xFFFFFFFFu, u);
+}
+
+// units: kPlanSeqs ints of shared memory that are free until the plan is made.
 template <int NT>
-__device__ PagedPlan paged_plan(const AttendParams &p, int R, int U)
+__device__ PagedPlan paged_plan(const AttendParams &p, int R, int U, int *units)
 {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ PagedPlan plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + NT - 1) / NT;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    auto seq_units = [&](int b) {
-        const PagedSeq s = paged_seq(p, b);
-        const int nrt = paged_row_tiles(p, s, R);
-        int64_t u = 0;
-        for (int rt = 0; rt < nrt; ++rt) u += paged_item(p, s, rt, R, U).units;
-        return u * p.kv_heads;
-    };
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        mine += seq_units(b);
+    const bool kept = p.B <= kPlanSeqs;
+
+    // Sequences of a few row tiles by a thread each, longer ones by a warp each.
+    bool many = false;
+    for (int b = tid; b < p.B; b += NT) {
+        if (kept) {
+            const PagedSeq s = paged_seq(p, b);
+            const bool by_warp = paged_row_tiles(p, s, R) > 2;
+            units[b] = by_warp ? -1 : paged_units(p, s, R, U);
+            many |= by_warp;
+        }
         if (blockIdx.x == 0) {  // what paged_seq() had to clamp
             const int len = __ldg(p.lens + b), t0 = __ldg(p.cu + b), t1 = __ldg(p.cu + b + 1);
             if (len < 0 || len > static_cast<int64_t>(p.table_cols) * p.page || t0 < 0 || t1 < t0 || t1 > p.tokens)
                 atomicOr(p.err, DEV_ERR_PLACE);
         }
     }
+    if (__syncthreads_or(many)) {
+        for (int b = warp; b < p.B; b += NT / 32)
+            if (units[b] < 0) {
+                const int u = paged_units_warp(p, paged_seq(p, b), R, U, lane);
+                __syncwarp();
+                if (lane == 0) units[b] = u;
+            }
+        __syncthreads();
+    }
+    auto seq_units = [&](int b) {
+        return static_cast<int64_t>(kept ? units[b] : paged_units(p, paged_seq(p, b), R, U)) * p.kv_heads;
+    };
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_units(b);
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -150,24 +187,21 @@ __device__ PagedPlan paged_plan(const AttendParams &p, int R, int U)
     }
     const int64_t G = min(static_cast<int64_t>(gridDim.x), total), c = blockIdx.x;
     const int64_t begin = c < G ? total * c / G : 0, end = c < G ? total * (c + 1) / G : 0;
-    if (tid == 0) {
+    if (begin < end ? (before <= begin && begin < before + mine) : tid == 0) {
+        int64_t off = begin - before, u = 1;
+        int b = b0;
+        if (begin < end)
+            for (; b < b1; ++b) {
+                u = seq_units(b);
+                if (off < u) break;
+                off -= u;
+            }
         plan.total = total;
         plan.begin = begin;
         plan.end = end;
         plan.ctas = G;
-        plan.b = 0;
-        plan.off = 0;
-    }
-    __syncthreads();
-    if (begin < end && before <= begin && begin < before + mine) {
-        int64_t off = begin - before;
-        int b = b0;
-        for (; b < b1; ++b) {
-            const int64_t u = seq_units(b);
-            if (off < u) break;
-            off -= u;
-        }
         plan.b = b;
+        plan.per_head = static_cast<int>(u / p.kv_heads);
         plan.off = off;
     }
     __syncthreads();
@@ -188,25 +222,35 @@ struct PagedWalk {
     int64_t left;
     int nrt, off;
 
+    // Whole warps call it.
     __device__ void start(const AttendParams &p, const PagedPlan &plan, int R, int U)
     {
         left = plan.end - plan.begin;
         if (left <= 0) return;
+        const int lane = threadIdx.x & 31;
         pc.b = plan.b;
         pc.s = paged_seq(p, pc.b);
         nrt = paged_row_tiles(p, pc.s, R);
-        int64_t per_head = 0;
-        for (int rt = 0; rt < nrt; ++rt) per_head += paged_item(p, pc.s, rt, R, U).units;
-        pc.kvh = static_cast<int>(plan.off / per_head);
-        int64_t rem = plan.off % per_head;
-        pc.rt = 0;
-        for (;;) {
-            pc.it = paged_item(p, pc.s, pc.rt, R, U);
-            if (rem < pc.it.units) break;
-            rem -= pc.it.units;
-            ++pc.rt;
+        pc.kvh = static_cast<int>(plan.off / plan.per_head);
+        int rem = static_cast<int>(plan.off - static_cast<int64_t>(pc.kvh) * plan.per_head);
+        for (int from = 0;; from += 32) {  // the row tile that holds unit `rem` of the head, 32 at a time
+            const int u = from + lane < nrt ? paged_item(p, pc.s, from + lane, R, U).units : 0;
+            int upto = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            if (rem < all) {
+                const int k = __ffs(__ballot_sync(0xFFFFFFFFu, rem < upto)) - 1;
+                off = rem - __shfl_sync(0xFFFFFFFFu, upto - u, k);
+                pc.rt = from + k;
+                break;
+            }
+            rem -= all;
         }
-        off = static_cast<int>(rem);
+        pc.it = paged_item(p, pc.s, pc.rt, R, U);
         cut();
     }
     __device__ void cut()
@@ -241,6 +285,36 @@ struct PagedWalk {
 __device__ __forceinline__ int paged_owner(int64_t u, int64_t total, int64_t G)
 {
     return static_cast<int>(((u + 1) * G - 1) / total);
+}
+
+// The CTAs that share the current piece's item: the first, and how many.
+__device__ __forceinline__ int2 paged_sharers(const PagedPlan &plan, const PagedWalk &w)
+{
+    const int64_t first = plan.end - w.left - w.pc.a;
+    const int c0 = paged_owner(first, plan.total, plan.ctas);
+    return make_int2(c0, paged_owner(first + w.pc.it.units - 1, plan.total, plan.ctas) - c0 + 1);
+}
+
+// Slot of part i of the item that CTA c0 begins.
+__device__ __forceinline__ int64_t paged_slot(int c0, int i)
+{
+    return 2 * static_cast<int64_t>(c0 + i) + (i == 0);
+}
+
+// A warp has written its rows of a part: true if it is the last of `parts` to
+// do so, and may read the others'.
+__device__ __forceinline__ bool paged_last(unsigned *ticket, int parts, int lane)
+{
+    __threadfence();
+    __syncwarp();
+    unsigned got = 0;
+    if (lane == 0) {
+        got = atomicAdd(ticket, 1u);
+        if (got == static_cast<unsigned>(parts) - 1) *ticket = 0;  // for the next call
+    }
+    got = __shfl_sync(0xFFFFFFFFu, got, 0);
+    __threadfence();
+    return got == static_cast<unsigned>(parts) - 1;
 }
 
 }  // namespace dfl

@@ -41,6 +41,24 @@ struct PrepParams {
 cudaError_t launch_prep(const PrepParams &p, int head_dim, int dtype, cudaStream_t s);
 
 // ---- attention ----
+// Division of 0 <= n < 2^31 by a constant of the launch.
+struct FastDiv {
+    uint32_t d = 1, mul = 1, shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by)
+    {
+        while ((uint64_t(1) << shift) < by) ++shift;  // ceil(log2 by)
+        mul = static_cast<uint32_t>((((uint64_t(1) << shift) - by) << 32) / by + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int n) const
+    {
+        const uint32_t u = static_cast<uint32_t>(n);
+        return static_cast<int>((__umulhi(u, mul) + u) >> shift);
+    }
+#endif
+};
+
 struct AttendParams {
     const void *q;
     void *out;
@@ -52,16 +70,20 @@ struct AttendParams {
     int64_t table_stride;
     int table_cols, num_pages;
     int B, tokens, kv_heads, group, page;  // group = query heads per key/value head
+    FastDiv by_group, by_page;
     int causal, window;            // window 0: none
     float scale_log2;              // score scale * log2(e) (* the keys' scale)
     float v_scale;
     // Workspace: CTA c's partial results in slots 2c (a piece that continues an
-    // earlier CTA's item) and 2c + 1 (one that a later CTA continues), and the
-    // merge's work list, entry c for the item that CTA c begins and CTA c + 1
-    // continues.
-    float *part_o;    // [2 * grid][rows][head_dim]
-    float2 *part_ml;  // [2 * grid][rows] running maximum (log2) and sum
-    int4 *merge;      // [2 * grid]
+    // earlier CTA's item) and 2c + 1 (one that a later CTA continues). An item
+    // split over at most kTicketParts CTAs is joined by whichever finishes last
+    // (a counter per warp's rows, at the CTA that begins the item, zero between
+    // calls); one over more CTAs by the merge kernel, whose list has entry c
+    // for the item that CTA c begins.
+    float *part_o;     // [2 * grid][rows][head_dim]
+    float2 *part_ml;   // [2 * grid][rows] running maximum (log2) and sum
+    int4 *merge;       // [2 * grid]: first token row, first row, rows, key/value head | CTAs (0: nothing to do)
+    unsigned *ticket;  // [grid][kTicketWarps]
     int *err;
 };
 
@@ -69,6 +91,7 @@ struct AttendParams {
 constexpr int kRowsUnit = 64;    // few rows: 16 or 32 rows, units of 64 keys
 constexpr int kTileRows = 256;   // many rows
 constexpr int kTileUnit = 128;
+constexpr int kTicketParts = 4, kTicketWarps = 8;
 
 cudaError_t prepare_attend_rows(int smem_optin);
 cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int grid,

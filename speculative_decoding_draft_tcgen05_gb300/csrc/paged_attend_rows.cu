@@ -1,5 +1,7 @@
 // Attention of few rows (single tokens and draft blocks) over a paged cache,
 // and the merge of split items.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace dfl {
@@ -90,6 +92,18 @@ struct RowsShape {
     }
 };
 
+__device__ __forceinline__ void add8(float (&acc)[8], float f, const float4 &x, const float4 &y)
+{
+    acc[0] = fmaf(f, x.x, acc[0]);
+    acc[1] = fmaf(f, x.y, acc[1]);
+    acc[2] = fmaf(f, x.z, acc[2]);
+    acc[3] = fmaf(f, x.w, acc[3]);
+    acc[4] = fmaf(f, y.x, acc[4]);
+    acc[5] = fmaf(f, y.y, acc[5]);
+    acc[6] = fmaf(f, y.z, acc[6]);
+    acc[7] = fmaf(f, y.w, acc[7]);
+}
+
 template <int D, int MT>
 constexpr int rows_q_bytes()
 {
@@ -130,7 +144,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
 
     pdl_trigger();
     pdl_wait();
-    const PagedPlan plan = paged_plan<kRowsThreads>(p, R, kRowsUnit);
+    const PagedPlan plan = paged_plan<kRowsThreads>(p, R, kRowsUnit, reinterpret_cast<int *>(smem));
     PagedWalk walk;
     walk.start(p, plan, R, kRowsUnit);
     int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
@@ -147,7 +161,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                 const int r = i / QCH, c = i % QCH;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (r < rows) {
-                    const int rr = pc.rt * R + r, t = rr / p.group, g = rr % p.group;
+                    const int rr = pc.rt * R + r, t = p.by_group.div(rr), g = rr - t * p.group;
                     v = *reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) +
                                                          (s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c);
                 }
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
                 const int r = 8 * i + (lane >> 2);
-                const int place = base + (pc.rt * R + r) / p.group;
+                const int place = base + p.by_group.div(pc.rt * R + r);
                 upto[i] = r < rows ? (p.causal ? min(place, s.len - 1) : s.len - 1) : -1;
                 after[i] = p.window > 0 ? place - p.window : -1;
                 if (r < rows) {
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                         const int key = (first + j + lane) * kRowsUnit + 16 * warp;
                         pages = -1;
                         if (j + lane < n_units && key < hi && key + 16 > lo) {
-                            pages = __ldg(p.table + pc.b * p.table_stride + key / p.page);
+                            pages = __ldg(p.table + pc.b * p.table_stride + p.by_page.div(key));
                             if (pages < 0 || pages >= p.num_pages) {
                                 pages = -1;
                                 atomicOr(p.err, DEV_ERR_PLACE);
@@ -220,7 +234,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                     }
                     const int page = __shfl_sync(0xFFFFFFFFu, pages, j - pages_from);
                     const int key = (first + j) * kRowsUnit + 16 * warp;
-                    const int64_t at = page * p.page_stride + (key % p.page) * p.slot_stride + pc.kvh * p.head_stride;
+                    const int slot = key - p.by_page.div(key) * p.page;
+                    const int64_t at = page * p.page_stride + slot * p.slot_stride + pc.kvh * p.head_stride;
                     const uint32_t dst = ring + (j % S) * SH::STAGE;
 #pragma unroll
                     for (int i = 0; i < 16 * CH / 32; ++i) {
@@ -416,8 +431,20 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                 }
             }
             __syncthreads();
-            const bool begins = pc.a == 0, ends = pc.e == pc.it.units;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0);
+            const bool begins = pc.a == 0, split = !begins || pc.e < pc.it.units;
+            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
+            const int64_t mine_slot = paged_slot(share.x, static_cast<int>(blockIdx.x) - share.x);
+            auto finish = [&](int r, int c, const float(&acc)[8], float M, float L) {
+                const int rr = pc.rt * R + r, t = p.by_group.div(rr), hd = pc.kvh * p.group + rr - t * p.group;
+                const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
+                *reinterpret_cast<uint4 *>(static_cast<QT *>(p.out) + (s.t0 + t) * p.o_ts + hd * p.o_hs + 8 * c) =
+                    make_uint4(pack2<QT>(acc[0] * inv, acc[1] * inv), pack2<QT>(acc[2] * inv, acc[3] * inv),
+                               pack2<QT>(acc[4] * inv, acc[5] * inv), pack2<QT>(acc[6] * inv, acc[7] * inv));
+                if (c == 0 && p.lse)
+                    p.lse[static_cast<int64_t>(s.t0 + t) * p.kv_heads * p.group + hd] =
+                        M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+            };
+            // a warp always takes the same rows, so the CTAs that share an item join them warp by warp
             for (int i = tid; i < rows * (D / 8); i += kRowsThreads) {
                 const int r = i / (D / 8), c = i % (D / 8);
                 float M = -INFINITY, L = 0.f;
@@ -431,36 +458,45 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                     L += f * ml.y;
                     const float4 *src = reinterpret_cast<const float4 *>(
                         reinterpret_cast<const float *>(ring_ptr + w * kRowsRing) + r * OS + 8 * c);
-                    const float4 x = src[0], y = src[1];
-                    acc[0] = fmaf(f, x.x, acc[0]);
-                    acc[1] = fmaf(f, x.y, acc[1]);
-                    acc[2] = fmaf(f, x.z, acc[2]);
-                    acc[3] = fmaf(f, x.w, acc[3]);
-                    acc[4] = fmaf(f, y.x, acc[4]);
-                    acc[5] = fmaf(f, y.y, acc[5]);
-                    acc[6] = fmaf(f, y.z, acc[6]);
-                    acc[7] = fmaf(f, y.w, acc[7]);
+                    add8(acc, f, src[0], src[1]);
                 }
-                if (begins && ends) {
-                    const int rr = pc.rt * R + r, t = s.t0 + rr / p.group, hd = pc.kvh * p.group + rr % p.group;
-                    const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
-                    uint4 v = make_uint4(pack2<QT>(acc[0] * inv, acc[1] * inv), pack2<QT>(acc[2] * inv, acc[3] * inv),
-                                         pack2<QT>(acc[4] * inv, acc[5] * inv), pack2<QT>(acc[6] * inv, acc[7] * inv));
-                    *reinterpret_cast<uint4 *>(static_cast<QT *>(p.out) + t * p.o_ts + hd * p.o_hs + 8 * c) = v;
-                    if (c == 0 && p.lse)
-                        p.lse[static_cast<int64_t>(t) * p.kv_heads * p.group + hd] =
-                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                if (!split) {
+                    finish(r, c, acc, M, L);
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + (slot * R + r) * D + 8 * c);
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + (mine_slot * R + r) * D + 8 * c);
                     dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                    if (c == 0) p.part_ml[slot * R + r] = make_float2(M, L);
+                    if (c == 0) p.part_ml[mine_slot * R + r] = make_float2(M, L);
                 }
             }
-            if (begins && !ends) {  // this CTA's last piece
-                const int64_t last = plan.end - walk.left - pc.a + pc.it.units - 1;
+            if (split && share.y <= kTicketParts) {
+                __syncwarp();
+                if (paged_last(p.ticket + share.x * kTicketWarps + warp, share.y, lane))
+                    for (int i = tid; i < rows * (D / 8); i += kRowsThreads) {
+                        const int r = i / (D / 8), c = i % (D / 8);
+                        float2 ml[kTicketParts];
+                        float M = -INFINITY, L = 0.f;
+#pragma unroll
+                        for (int k = 0; k < kTicketParts; ++k) {
+                            ml[k] = k < share.y ? __ldcg(p.part_ml + paged_slot(share.x, k) * R + r) : make_float2(-INFINITY, 0.f);
+                            M = fmaxf(M, ml[k].x);
+                        }
+                        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < kTicketParts; ++k)
+                            if (k < share.y) {
+                                const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                                L += f * ml[k].y;
+                                const float4 *src = reinterpret_cast<const float4 *>(
+                                    p.part_o + (paged_slot(share.x, k) * R + r) * D + 8 * c);
+                                add8(acc, f, __ldcg(src), __ldcg(src + 1));
+                            }
+                        finish(r, c, acc, M, L);
+                    }
+            }
+            if (begins && share.y > kTicketParts) {  // this CTA's last piece
                 merge0 = make_int4(s.t0, pc.rt * R, rows, pc.kvh);
-                merge1 = make_int4(paged_owner(last, plan.total, plan.ctas) - static_cast<int>(blockIdx.x) + 1, 0, 0, 0);
+                merge1 = make_int4(share.y, 0, 0, 0);
             }
             if (!walk.next(p, R, kRowsUnit)) break;
         }
@@ -471,61 +507,109 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
     }
 }
 
-// Joins the partial results of the item that CTA blockIdx.x began and its
-// successors finished, one row per warp, in CTA order (so always the same sum).
-constexpr int kMergeWarps = 4;
+// Joins the items that were split over more than kTicketParts CTAs. Every
+// block reads the whole list (an entry per CTA) and takes quads of rows in
+// turn; its warps take a quad's parts in turn (always the same ones, so the
+// sum does not depend on the order in which anything finished), four rows of
+// loads in flight each, and the warps' sums are added in shared memory.
+constexpr int kMergeWarps = 8, kMergeQuad = 4, kMergeMost = 1024;
 
 template <int D, typename QT>
-__global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R)
+__global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R, int G)
 {
     constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.y * kMergeWarps + warp;
-    const int64_t c0 = blockIdx.x;
+    using F = typename std::conditional<V == 4, float4, float2>::type;
+    __shared__ int list[kMergeMost], listed;
+    __shared__ float top[kMergeWarps], sums[kMergeWarps][kMergeQuad];
+    __shared__ __align__(16) float part[kMergeWarps][kMergeQuad][D];  // (read and written in pieces of F)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    const int parts = p.merge[2 * c0 + 1].x;
-    if (parts == 0) return;
-    const int4 item = p.merge[2 * c0];  // first token row, first row, rows, key/value head
-    if (r >= item.z) return;
-    // slot of part i: 2 c0 + 1 for the beginning, 2 (c0 + i) after it
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[(2 * (c0 + i) + (i == 0)) * R + r].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    float L = 0.f, acc[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    if (warp == 0) {
+        int n = 0;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const int64_t row = (2 * (c0 + i) + (i == 0)) * R + r;
-        const float2 ml = p.part_ml[row];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        L = fmaf(f, ml.y, L);
-        const float *src = p.part_o + row * D + V * lane;
-        if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(src);
-            acc[0] = fmaf(f, x.x, acc[0]);
-            acc[1] = fmaf(f, x.y, acc[1]);
-            acc[2] = fmaf(f, x.z, acc[2]);
-            acc[3] = fmaf(f, x.w, acc[3]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2 *>(src);
-            acc[0] = fmaf(f, x.x, acc[0]);
-            acc[1] = fmaf(f, x.y, acc[1]);
+        for (int c = lane; c < (G + 31) / 32 * 32; c += 32) {
+            const bool has = c < G && p.merge[2 * c + 1].x > 0;
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
+            if (has) list[n + __popc(m & ((1u << lane) - 1u))] = c;
+            n += __popc(m);
         }
+        if (lane == 0) listed = n;
     }
-    const int rr = item.y + r, t = item.x + rr / p.group, hd = item.w * p.group + rr % p.group;
-    const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
-    QT *dst = static_cast<QT *>(p.out) + t * p.o_ts + hd * p.o_hs + V * lane;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack2<QT>(acc[0] * inv, acc[1] * inv), pack2<QT>(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack2<QT>(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse)
-        p.lse[static_cast<int64_t>(t) * p.kv_heads * p.group + hd] =
-            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+    __syncthreads();
+    const int entries = listed;
+    for (int64_t k = blockIdx.x; k < static_cast<int64_t>(entries) * (R / kMergeQuad); k += gridDim.x) {
+        const int c0 = list[k % entries], r0 = static_cast<int>(k / entries) * kMergeQuad;
+        const int4 item = p.merge[2 * c0];
+        const int parts = p.merge[2 * c0 + 1].x, rows = min(kMergeQuad, item.z - r0);
+        if (rows <= 0) continue;  // (the whole block)
+        // the rows' maxima: two warps a row
+        float m = -INFINITY;
+        if (warp / 2 < rows)
+            for (int i = (warp & 1) * 32 + lane; i < parts; i += 64) m = fmaxf(m, p.part_ml[paged_slot(c0, i) * R + r0 + warp / 2].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane == 0) top[warp] = m;
+        __syncthreads();
+        float M[kMergeQuad], L[kMergeQuad], acc[kMergeQuad][V];
+#pragma unroll
+        for (int q = 0; q < kMergeQuad; ++q) {
+            M[q] = fmaxf(top[2 * q], top[2 * q + 1]);
+            L[q] = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[q][v] = 0.f;
+        }
+#pragma unroll 2
+        for (int i = warp; i < parts; i += kMergeWarps) {
+            const int64_t row = paged_slot(c0, i) * R + r0;
+            F x[kMergeQuad];
+            float2 ml[kMergeQuad];
+#pragma unroll
+            for (int q = 0; q < kMergeQuad; ++q) {
+                const int64_t at = row + (q < rows ? q : 0);
+                ml[q] = p.part_ml[at];
+                x[q] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
+            }
+#pragma unroll
+            for (int q = 0; q < kMergeQuad; ++q) {
+                const float f = ml[q].x == -INFINITY ? 0.f : ex2(ml[q].x - M[q]);
+                L[q] = fmaf(f, ml[q].y, L[q]);
+                const float *xs = reinterpret_cast<const float *>(&x[q]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[q][v] = fmaf(f, xs[v], acc[q][v]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kMergeQuad; ++q) {
+            F x;
+            float *xs = reinterpret_cast<float *>(&x);
+#pragma unroll
+            for (int v = 0; v < V; ++v) xs[v] = acc[q][v];
+            *reinterpret_cast<F *>(&part[warp][q][V * lane]) = x;
+            if (lane == 0) sums[warp][q] = L[q];
+        }
+        __syncthreads();
+        const int q = tid / 64, d = tid % 64 * 2;
+        if (q < rows && d < D) {
+            float total = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) {
+                total += sums[w][q];
+                a += part[w][q][d];
+                b += part[w][q][d + 1];
+            }
+            const int rr = item.y + r0 + q, t = p.by_group.div(rr), hd = item.w * p.group + rr - t * p.group;
+            const float inv = total > 0.f || total != total ? p.v_scale / total : 0.f;
+            *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + (item.x + t) * p.o_ts + hd * p.o_hs + d) =
+                pack2<QT>(a * inv, b * inv);
+            if (d == 0 && p.lse) {
+                const float mm = fmaxf(top[2 * q], top[2 * q + 1]);
+                p.lse[static_cast<int64_t>(item.x + t) * p.kv_heads * p.group + hd] =
+                    mm == -INFINITY ? -INFINITY : (mm + lg2(total)) * 0.69314718055994531f;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 template <int D, int MT>
@@ -581,12 +665,13 @@ cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, i
 
 cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s)
 {
-    const dim3 g(grid, (rows + kMergeWarps - 1) / kMergeWarps), b(kMergeWarps * 32);
+    if (grid > kMergeMost) return cudaErrorInvalidValue;
+    const dim3 g(grid), b(kMergeWarps * 32);
     if (head_dim == 128)
-        return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<128, __nv_bfloat16>, g, b, 0, s, 1, p, rows)
-                                    : launch_ex(attend_merge_kernel<128, __half>, g, b, 0, s, 1, p, rows);
-    return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<64, __nv_bfloat16>, g, b, 0, s, 1, p, rows)
-                                : launch_ex(attend_merge_kernel<64, __half>, g, b, 0, s, 1, p, rows);
+        return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<128, __nv_bfloat16>, g, b, 0, s, 1, p, rows, grid)
+                                    : launch_ex(attend_merge_kernel<128, __half>, g, b, 0, s, 1, p, rows, grid);
+    return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<64, __nv_bfloat16>, g, b, 0, s, 1, p, rows, grid)
+                                : launch_ex(attend_merge_kernel<64, __half>, g, b, 0, s, 1, p, rows, grid);
 }
 
 }  // namespace dfl

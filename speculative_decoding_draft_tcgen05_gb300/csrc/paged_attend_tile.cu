@@ -25,6 +25,7 @@ struct TileShape {
     static constexpr uint32_t TILE = BOXES * BOX;       // 128 rows of queries, keys or values
     static constexpr int STAGES = D == 128 ? 5 : 10;    // tiles of keys or values in flight
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static_assert(SMEM + 2048 <= 227 * 1024, "with the static shared memory, what a block can have");
     static constexpr uint32_t O_COL = 256;              // TMEM: scores 0-127 | 128-255, results from 256
 };
 
@@ -47,6 +48,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm,
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
+}
+
+// Adds to the bytes that a barrier's phase waits for (an arrival of its own still has to follow).
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void fence_async_proxy()
@@ -133,6 +140,13 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
         : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ void tmem_store_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -171,10 +185,10 @@ __device__ __forceinline__ int stream_steps(int n, bool alt, int i)
 // previous product is complete when the scores after it are (products of one
 // thread finish in order), so no other role takes part.
 //
-// Tiles whose keys are all on pages in use come by TMA (boxes of
-// gcd(page, 128) rows x 64 values, 128-byte swizzle); a tile that reaches past
-// the sequence's end or before its window is copied by the load warps, with
-// zeros in the place of what must not be read.
+// Keys and values come by TMA in boxes of gcd(page, 128) rows x 64 values
+// (128-byte swizzle); a box that reaches past the sequence's end, or lies on a
+// page before the window, is written by the load warps, with zeros in the
+// place of what must not be read.
 // ---------------------------------------------------------------------------
 struct TileParams {
     AttendParams a;
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
-    const PagedPlan plan = paged_plan<kTileThreads>(p, R, U);  // holds block barriers
+    const PagedPlan plan = paged_plan<kTileThreads>(p, R, U, reinterpret_cast<int *>(smem));  // holds block barriers
     tc_fence_after_sync();
     const uint32_t tmem = bars.tmem;
     int *const ab = &bars.abort_flag;
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             const int n = pc.e - pc.a, steps = stream_steps(n, alt, i);
             const int r = alt ? row : 128 * i + row;  // row of the item
             const bool real = r < rows;
-            const int rr = pc.rt * R + r, tok = rr / p.group, head = pc.kvh * p.group + rr % p.group;
+            const int rr = pc.rt * R + r, tok = p.by_group.div(rr), head = pc.kvh * p.group + rr - tok * p.group;
 
             // ---- this stream's queries (of a short item, stream 0's serve both)
             if (!(alt && i == 1)) {
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 for (int c = 0; c < 128; c += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1])));
+                        top[k] = max3(top[k], __uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1]));
                 const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
                 if (t == 0) {
                     m = now;
@@ -308,22 +322,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 }
                 // weights, rounded to 16 bits for the product; the sum takes them unrounded
                 const float off = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 by = make_float2(factor, factor), less = make_float2(-off, -off);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        const float a = ex2(fmaf(__uint_as_float(sr[64 * h + 2 * c]), factor, -off));
-                        const float b = ex2(fmaf(__uint_as_float(sr[64 * h + 2 * c + 1]), factor, -off));
-                        sum[c & 1] += a;
-                        sum[2 + (c & 1)] += b;
-                        w[c] = pack2<T>(a, b);
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[64 * h + 2 * c]), __uint_as_float(sr[64 * h + 2 * c + 1])),
+                                              by, less);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[c & 1] = __fadd2_rn(sum[c & 1], x);
+                        w[c] = pack2<T>(x.x, x.y);
                     }
                     tmem_store32(s_col + 32 * h, w);
                 }
                 tmem_store_wait();
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 both = __fadd2_rn(sum[0], sum[1]);
+                l += both.x + both.y;
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars.p_full[i]));
             }
@@ -366,15 +383,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 x_phase ^= 1;
             }
 
-            const bool begins = pc.a == 0, ends = pc.e == pc.it.units;
+            const bool begins = pc.a == 0, split = !begins || pc.e < pc.it.units;
+            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
             if (!(alt && i == 1)) {
-                const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0);
+                T *const dst = static_cast<T *>(p.out) + (s.t0 + tok) * p.o_ts + head * p.o_hs;
+                float *const part = p.part_o + (paged_slot(share.x, static_cast<int>(blockIdx.x) - share.x) * R + r) * D;
                 const bool joined = alt && n > 1;
-                if (alt && !joined) add = 0.f;
-                const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;
-                const float f = (begins && ends) ? keep * inv : keep, g = (begins && ends) ? add * inv : add;
-                T *dst = static_cast<T *>(p.out) + (s.t0 + tok) * p.o_ts + head * p.o_hs;
-                float *part = p.part_o + (slot * R + r) * D;
+                auto store = [&](int c, const float(&v)[32]) {  // 32 finished values of the row
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4 *>(dst + c + k) =
+                            make_uint4(pack2<T>(v[k], v[k + 1]), pack2<T>(v[k + 2], v[k + 3]), pack2<T>(v[k + 4], v[k + 5]),
+                                       pack2<T>(v[k + 6], v[k + 7]));
+                };
+                auto store_lse = [&](float M, float L) {
+                    if (p.lse)
+                        p.lse[static_cast<int64_t>(s.t0 + tok) * p.kv_heads * p.group + head] =
+                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                };
+                const float inv = split ? 1.f : (l > 0.f || l != l ? p.v_scale / l : 0.f);
+                const float f = keep * inv, g = add * inv;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -392,36 +420,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                             v[k + 3] = fmaf(x.w, g, v[k + 3]);
                         }
                     }
-                    if (real) {
-                        if (begins && ends) {
+                    if (real && !split) store(c, v);
+                    if (real && split) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-                                *reinterpret_cast<uint4 *>(dst + c + k) =
-                                    make_uint4(pack2<T>(v[k], v[k + 1]), pack2<T>(v[k + 2], v[k + 3]),
-                                               pack2<T>(v[k + 4], v[k + 5]), pack2<T>(v[k + 6], v[k + 7]));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<float4 *>(part + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                        }
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(part + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                 }
                 tc_fence_before_sync();
-                if (real) {
-                    if (begins && ends) {
-                        if (p.lse)
-                            p.lse[static_cast<int64_t>(s.t0 + tok) * p.kv_heads * p.group + head] =
-                                m == -INFINITY ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
-                    } else {
-                        p.part_ml[slot * R + r] = make_float2(m, l);
-                    }
-                }
                 if (alt) mbar_arrive(smem_u32(&bars.x_taken));
+                if (real && !split) store_lse(m, l);
+                if (real && split) p.part_ml[(part - p.part_o) / D] = make_float2(m, l);
+                if (split && share.y <= kTicketParts &&
+                    paged_last(p.ticket + share.x * kTicketWarps + warp, share.y, lane) && real) {
+                    float2 ml[kTicketParts];
+                    float M = -INFINITY, L = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kTicketParts; ++k) {
+                        ml[k] = k < share.y ? __ldcg(p.part_ml + paged_slot(share.x, k) * R + r) : make_float2(-INFINITY, 0.f);
+                        M = fmaxf(M, ml[k].x);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kTicketParts; ++k) {
+                        ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                        L += ml[k].x * ml[k].y;
+                    }
+                    const float done = L > 0.f || L != L ? p.v_scale / L : 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll 1
+                        for (int k = 0; k < share.y; ++k) {
+                            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (paged_slot(share.x, k) * R + r) * D + c);
+                            const float w = (k == 0 ? ml[0].x : k == 1 ? ml[1].x : k == 2 ? ml[2].x : ml[3].x) * done;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 x = __ldcg(src + e);
+                                v[4 * e] = fmaf(x.x, w, v[4 * e]);
+                                v[4 * e + 1] = fmaf(x.y, w, v[4 * e + 1]);
+                                v[4 * e + 2] = fmaf(x.z, w, v[4 * e + 2]);
+                                v[4 * e + 3] = fmaf(x.w, w, v[4 * e + 3]);
+                            }
+                        }
+                        store(c, v);
+                    }
+                    store_lse(M, L);
+                }
+                __syncwarp();
             }
-            if (begins && !ends) {  // this CTA's last piece
-                const int64_t last = plan.end - walk.left - pc.a + pc.it.units - 1;
+            if (begins && share.y > kTicketParts) {  // this CTA's last piece
                 merge0 = make_int4(s.t0, pc.rt * R, rows, pc.kvh);
-                merge1 = make_int4(paged_owner(last, plan.total, plan.ctas) - static_cast<int>(blockIdx.x) + 1, 0, 0, 0);
+                merge1 = make_int4(share.y, 0, 0, 0);
             }
             walk.next(p, R, U);
         }
@@ -435,6 +486,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             // -------------------------------------------------- matrix products
             if (lane == 0) {
                 constexpr uint32_t id_s = idesc_16<T>(128, 128, false), id_o = idesc_16<T>(128, D, true);
+                // (a descriptor's low bits are the address in units of 16 bytes: stepping it is an addition)
+                const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_mn(ring, SH::BOX);
                 uint32_t seq = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
                 bool ok = true;
                 auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -451,11 +504,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         const uint32_t k = seq + 2u * (alt ? 2 * t + i : t), st = k % S;
                         if (!wait(&bars.full[st], (k / S) & 1)) return;
                         tc_fence_after_sync();
-                        const uint32_t qa = q_s + (alt ? 0 : i) * SH::TILE, ka = ring + st * SH::TILE;
+                        const uint64_t qa = q_desc + (alt ? 0u : i * (SH::TILE >> 4)), ka = k_desc + st * (SH::TILE >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t o = (kk >> 2) * SH::BOX + (kk & 3) * 32;
-                            umma_bf16(tmem + 128u * i, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), id_s, kk > 0);
+                            const uint32_t o = ((kk >> 2) * SH::BOX + (kk & 3) * 32) >> 4;
+                            umma_bf16(tmem + 128u * i, qa + o, ka + o, id_s, kk > 0);
                         }
                         umma_commit(smem_u32(&bars.s_full[i]));
                         if (alt || i == 1) umma_commit(smem_u32(&bars.empty[st]));
@@ -465,11 +518,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         if (!wait(&bars.full[st], (k / S) & 1) || !wait(&bars.p_full[i], p_phase[i])) return;
                         p_phase[i] ^= 1;
                         tc_fence_after_sync();
-                        const uint32_t va = ring + st * SH::TILE;
+                        const uint64_t va = v_desc + st * (SH::TILE >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            umma_ts(tmem + SH::O_COL + D * i, tmem + 128u * i + 8u * kk, smem_desc_mn(va + kk * 2048, SH::BOX), id_o,
-                                    t > 0 || kk > 0);
+                            umma_ts(tmem + SH::O_COL + D * i, tmem + 128u * i + 8u * kk, va + kk * (2048 >> 4), id_o, t > 0 || kk > 0);
                         if (alt || i == 1) umma_commit(smem_u32(&bars.empty[st]));
                         if (t + 1 == steps[i]) umma_commit(smem_u32(&bars.o_full[i]));
                     };
@@ -498,81 +550,73 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         } else {
             // -------------------------------------------------- keys and values
             const int lw = warp - 9, ltid = tid - 9 * 32;
-            const int groups = U / tp.box_rows;  // row groups of a tile: 1, 2, 4 or 8
+            const int br = tp.box_rows, groups = U / br;  // row groups of a tile: 1, 2, 4 or 8
             uint32_t seq = 0, last_tma = 0;
             bool ok = true, any_tma = false;
             while (ok && walk.left > 0) {
                 const PagedPiece &pc = walk.pc;
                 const int n = pc.e - pc.a, len = pc.s.len, lo = pc.it.lo, hi = pc.it.hi;
-                const int from = lo / p.page * p.page;  // first place of a page in use
+                const int from = p.by_page.div(lo) * p.page;  // the first page that is used
+                const int32_t *const pages = p.table + pc.b * p.table_stride;
+                // lane g: the page of row group g of a tile (-1: no key of it is used)
+                auto page_of = [&](int j) {
+                    const int key = (pc.it.u0 + pc.a + j) * U + lane * br;
+                    return lane < groups && key >= from && key < hi ? __ldg(pages + p.by_page.div(key)) : -1;
+                };
+                int ahead = page_of(0);
                 for (int j = 0; j < n && ok; ++j) {
-                    const int key0 = (pc.it.u0 + pc.a + j) * U;
-                    // lane g: the page of row group g
-                    int page = -1, slot = 0;
-                    const int key = key0 + (lane & 7) * tp.box_rows;
-                    if (lane < groups && key + tp.box_rows > lo && key < hi) {
-                        const int col = key / p.page;
-                        slot = key - col * p.page;
-                        page = __ldg(p.table + pc.b * p.table_stride + col);
-                        if (page < 0 || page >= p.num_pages) {
-                            page = -1;
-                            atomicOr(p.err, DEV_ERR_PLACE);
-                        }
+                    const int key0 = (pc.it.u0 + pc.a + j) * U, key = key0 + lane * br;
+                    int page = ahead;
+                    if (j + 1 < n) ahead = page_of(j + 1);
+                    if (lane < groups && key >= from && key < hi && (page < 0 || page >= p.num_pages)) {
+                        page = -1;
+                        atomicOr(p.err, DEV_ERR_PLACE);
                     }
-                    const bool whole = key0 >= from && key0 + U <= len &&
-                                       __all_sync(0xFFFFFFFFu, lane >= groups || page >= 0 || key >= hi);
-                    // a whole tile may reach past the last key that a row sees (causal): those pages are read too
-                    bool tma = whole;
-                    if (whole && lane < groups && key >= hi) {
-                        const int col = key / p.page;
-                        slot = key - col * p.page;
-                        page = __ldg(p.table + pc.b * p.table_stride + col);
-                    }
-                    if (whole) tma = __all_sync(0xFFFFFFFFu, lane >= groups || (page >= 0 && page < p.num_pages));
+                    const int slot = key - p.by_page.div(key) * p.page;
+                    // groups that TMA brings whole, and those that hold places past the end (or no key in use)
+                    const unsigned tma = __ballot_sync(0xFFFFFFFFu, page >= 0 && key + br <= len);
+                    const int soft = groups - __popc(tma);
 #pragma unroll 1
                     for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
                         const uint32_t st = seq % S, bar = smem_u32(&bars.full[st]);
                         if (!(ok = warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab))) break;
                         const uint32_t dst = ring + st * SH::TILE;
-                        if (tma) {
-                            if (lw == 0) {
-                                if (lane == 0) mbar_arrive_expect_tx(bar, SH::TILE);
-                                __syncwarp();
-                                const int g = lane & 7, box = lane >> 3;
-                                const int pg = __shfl_sync(0xFFFFFFFFu, page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
-                                if (g < groups && box < SH::BOXES)
-                                    tma_load_4d(dst + box * SH::BOX + g * tp.box_rows * 128, kv ? &tp.tm_v : &tp.tm_k, 64 * box,
-                                                sl, pc.kvh, pg, bar);
-                                any_tma = true;
-                                last_tma = seq;
-                            } else if (lane == 0) {
-                                mbar_arrive(bar);
-                            }
-                        } else {
+                        if (lw == 0 && tma) {
+                            if (lane == 0) mbar_expect_tx(bar, __popc(tma) * br * SH::BOXES * 128u);
+                            __syncwarp();
+                            const int g = lane & 7, box = lane >> 3;
+                            const int pg = __shfl_sync(0xFFFFFFFFu, page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
+                            if (box < SH::BOXES && (tma >> g & 1))
+                                tma_load_4d(dst + box * SH::BOX + g * br * 128, kv ? &tp.tm_v : &tp.tm_k, 64 * box, sl, pc.kvh,
+                                            pg, bar);
+                            any_tma = true;
+                            last_tma = seq;
+                        }
+                        if (soft) {
                             const uint8_t *base = static_cast<const uint8_t *>(kv ? p.v : p.k);
                             constexpr int CH = D / 8;  // 16-byte pieces of a row
-                            constexpr int kPieces = (U * CH + 32 * kLoadWarps - 1) / (32 * kLoadWarps) * (32 * kLoadWarps);
-#pragma unroll 1
-                            for (int x = ltid; x < kPieces; x += 32 * kLoadWarps) {
-                                const int row = x / CH, c = x % CH, k = key0 + row;
-                                const int g = min(row / tp.box_rows, 7);
+                            for (int g = 0; g < groups; ++g) {
+                                if (tma >> g & 1) continue;
                                 const int pg = __shfl_sync(0xFFFFFFFFu, page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
-                                if (row >= U) continue;
-                                const bool in = pg >= 0 && k >= lo && k < hi;
-                                const int64_t at = in ? pg * p.page_stride + (sl + row % tp.box_rows) * p.slot_stride +
-                                                            pc.kvh * p.head_stride + 8 * c
-                                                      : 0;
-                                const int bytes = in ? 16 : 0;  // 0: zeros
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                                 dst + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16)),
-                                             "l"(base + 2 * at), "r"(bytes)
-                                             : "memory");
+                                const int64_t at = pg * p.page_stride + sl * p.slot_stride + pc.kvh * p.head_stride;
+#pragma unroll 4
+                                for (int x = ltid; x < br * CH; x += 32 * kLoadWarps) {
+                                    const int row = x / CH, c = x % CH, k = key0 + g * br + row;
+                                    const bool in = pg >= 0 && k < len;
+                                    const int64_t o = in ? at + row * p.slot_stride + 8 * c : 0;
+                                    const int bytes = in ? 16 : 0;  // 0: zeros
+                                    const int rw = g * br + row;
+                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                                     dst + (c >> 3) * SH::BOX + rw * 128 + (((c & 7) ^ (rw & 7)) * 16)),
+                                                 "l"(base + 2 * o), "r"(bytes)
+                                                 : "memory");
+                                }
                             }
                             asm volatile("cp.async.wait_all;" ::: "memory");
                             fence_async_proxy();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(bar);
                         }
+                        if (lane == 0) mbar_arrive(bar);
                     }
                 }
                 walk.next(p, R, U);
