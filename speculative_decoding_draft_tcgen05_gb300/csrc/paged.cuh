@@ -317,4 +317,19 @@ __device__ __forceinline__ bool paged_last(unsigned *ticket, int parts, int lane
     return got == static_cast<unsigned>(parts) - 1;
 }
 
+// True (and the counter is cleared) if all parts but this warp's are written
+// already: then it need not write its own.
+__device__ __forceinline__ bool paged_all_others(unsigned *ticket, int parts, int lane)
+{
+    unsigned got = 0;
+    if (lane == 0) {
+        got = atomicAdd(ticket, 0u);
+        if (got == static_cast<unsigned>(parts) - 1) *ticket = 0;
+    }
+    got = __shfl_sync(0xFFFFFFFFu, got, 0);
+    if (got != static_cast<unsigned>(parts) - 1) return false;
+    __threadfence();
+    return true;
+}
+
 }  // namespace dfl

@@ -31,7 +31,7 @@ struct TileShape {
 
 struct TileBars {
     uint64_t full[10], empty[10];  // ring of tiles
-    uint64_t q_full[2];            // a stream's queries are in shared memory
+    uint64_t q_full[2];            // (one arrival per warp, here and below) a stream's queries are in shared memory
     uint64_t s_full[2];            // its scores are in TMEM
     uint64_t p_full[2];            // its weights are in TMEM
     uint64_t o_full[2];            // its results are complete
@@ -85,14 +85,42 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t box)
     return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], A's rows in the TMEM lanes, two 16-bit K values a column.
-__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+// The products and commits below are issued by the lane that `who` is true
+// in, by predicating the instruction alone: the code around it stays
+// warp-uniform and its operands in uniform registers (inside a divergent
+// branch an issue took about 80 cycles, more than the product itself).
+// D[tmem] (+)= A[smem] * B[smem]^T.
+__device__ __forceinline__ void umma_ss(uint32_t who, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(acc)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(who)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], A's rows in the TMEM lanes, two 16-bit K values a column.
+__device__ __forceinline__ void umma_ts(uint32_t who, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(who)
+        : "memory");
+}
+
+// Arrives once on `bar` when every product issued so far by this lane is done.
+__device__ __forceinline__ void umma_commit_if(uint32_t who, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+        "r"(who)
         : "memory");
 }
 
@@ -152,10 +180,25 @@ __device__ __forceinline__ void tmem_store_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+    return is != 0;
+}
+
 // Bounded wait of a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag)
 {
     return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, abort_flag));
+}
+
+// One arrival of a whole warp, after what its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane)
+{
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
 }
 
 // The steps of one stream in a piece of n tiles: with rows for both streams
@@ -217,13 +260,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             mbar_init(smem_u32(&bars.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.q_full[i]), 128);
+            mbar_init(smem_u32(&bars.q_full[i]), 4);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
-            mbar_init(smem_u32(&bars.p_full[i]), 128);
+            mbar_init(smem_u32(&bars.p_full[i]), 4);
             mbar_init(smem_u32(&bars.o_full[i]), 1);
         }
-        mbar_init(smem_u32(&bars.x_given), 128);
-        mbar_init(smem_u32(&bars.x_taken), 128);
+        mbar_init(smem_u32(&bars.x_given), 4);
+        mbar_init(smem_u32(&bars.x_taken), 4);
         mbar_init(smem_u32(&bars.done), 1);
         bars.abort_flag = 0;
         fence_mbar_init();
@@ -250,58 +293,75 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const uint32_t s_col = tmem + lane_base + 128u * i, o_col = tmem + lane_base + SH::O_COL + D * i;
         uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
         int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
-        bool ok = true;
-        while (ok && walk.left > 0) {
-            const PagedPiece &pc = walk.pc;
-            const PagedSeq &s = pc.s;
-            const int rows = min(R, s.n * p.group - pc.rt * R);
-            const bool alt = rows <= 128;
-            const int n = pc.e - pc.a, steps = stream_steps(n, alt, i);
-            const int r = alt ? row : 128 * i + row;  // row of the item
-            const bool real = r < rows;
-            const int rr = pc.rt * R + r, tok = p.by_group.div(rr), head = pc.kvh * p.group + rr - tok * p.group;
+        const float factor = p.scale_log2;
 
-            // ---- this stream's queries (of a short item, stream 0's serve both)
-            if (!(alt && i == 1)) {
-                const T *src = static_cast<const T *>(p.q) + (s.t0 + tok) * p.q_ts + head * p.q_hs;
-                uint8_t *dst = smem + i * SH::TILE + row * 128;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = real ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * SH::BOX + (((c & 7) ^ (row & 7)) * 16)) = v;
-                }
-                fence_async_proxy();
-                mbar_arrive(smem_u32(&bars.q_full[i]));
-            }
+        // This thread's row of a piece.
+        struct Row {
+            int r, tok, head;   // row of the item; row of the call and query head
+            int upto, after;    // keys that it sees: (after, upto]
+            int key0, steps;    // first key of the piece, steps of this stream
+            bool real, alt;     // a row past the item's is not; a short item's tiles alternate
+        };
+        auto row_of = [&](const PagedPiece &pc) {
+            Row c;
+            const int rows = min(R, pc.s.n * p.group - pc.rt * R);
+            c.alt = rows <= 128;
+            c.r = c.alt ? row : 128 * i + row;
+            c.real = c.r < rows;
+            const int rr = pc.rt * R + c.r, t = p.by_group.div(rr), place = pc.s.len - pc.s.n + t;
+            c.tok = pc.s.t0 + t;
+            c.head = pc.kvh * p.group + rr - t * p.group;
+            c.upto = c.real ? (p.causal ? min(place, pc.s.len - 1) : pc.s.len - 1) : -1;
+            c.after = p.window > 0 ? place - p.window : -1;
+            c.key0 = (pc.it.u0 + pc.a) * U;
+            c.steps = stream_steps(pc.e - pc.a, c.alt, i);
+            return c;
+        };
+        // Its query to shared memory (of a short item, stream 0's rows serve both).
+        auto load_q = [&](const Row &c) {
+            if (c.alt && i == 1) return;
+            const T *src = static_cast<const T *>(p.q) + c.tok * p.q_ts + c.head * p.q_hs;
+            uint8_t *dst = smem + i * SH::TILE + row * 128;
+            uint4 v[D / 8];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                v[k] = c.real ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                *reinterpret_cast<uint4 *>(dst + (k >> 3) * SH::BOX + (((k & 7) ^ (row & 7)) * 16)) = v[k];
+            fence_async_proxy();
+            warp_arrive(&bars.q_full[i], lane);
+        };
 
-            // ---- keys that this row sees: (after, upto]
-            const int place = s.len - s.n + tok;
-            const int upto = real ? (p.causal ? min(place, s.len - 1) : s.len - 1) : -1;
-            const int after = p.window > 0 ? place - p.window : -1;
-            const int least_upto = __reduce_min_sync(0xFFFFFFFFu, real ? upto : 0x7FFFFFFF);
-            const int most_after = __reduce_max_sync(0xFFFFFFFFu, real ? after : -1);
-            const float factor = p.scale_log2;
+        bool ok = true, more = walk.left > 0;
+        Row c = {};
+        if (more) {
+            c = row_of(walk.pc);
+            load_q(c);
+        }
+        while (more) {
+            const int least_upto = __reduce_min_sync(0xFFFFFFFFu, c.real ? c.upto : 0x7FFFFFFF);
+            const int most_after = __reduce_max_sync(0xFFFFFFFFu, c.real ? c.after : -1);
             float m = -INFINITY, l = 0.f;
-
-            for (int t = 0; t < steps; ++t) {
-                const int key0 = (pc.it.u0 + pc.a + (alt ? 2 * t + i : t)) * U;
+            for (int t = 0; t < c.steps; ++t) {
+                const int key0 = c.key0 + (c.alt ? 2 * t + i : t) * U;
                 if (!(ok = warp_wait(&bars.s_full[i], s_phase, ab))) break;
                 s_phase ^= 1;
                 tc_fence_after_sync();
                 uint32_t sr[128];
                 tmem_load128(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
-                    const int hi = upto - key0, lo = after - key0;
+                    const int hi = c.upto - key0, lo = c.after - key0;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > hi || c <= lo) sr[c] = __float_as_uint(-INFINITY);
+                    for (int k = 0; k < 128; ++k)
+                        if (k > hi || k <= lo) sr[k] = __float_as_uint(-INFINITY);
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c += 8)
+                for (int k = 0; k < 128; k += 8)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top[k] = max3(top[k], __uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1]));
+                    for (int e = 0; e < 4; ++e)
+                        top[e] = max3(top[e], __uint_as_float(sr[k + 2 * e]), __uint_as_float(sr[k + 2 * e + 1]));
                 const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
                 if (t == 0) {
                     m = now;
@@ -311,12 +371,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                     m = to;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
+                    for (int k = 0; k < D; k += 32) {
                         uint32_t o[32];
-                        tmem_load32(o_col + c, o);
+                        tmem_load32(o_col + k, o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_store32(o_col + c, o);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_store32(o_col + k, o);
                     }
                     tmem_store_wait();
                 }
@@ -328,24 +388,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[32];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[64 * h + 2 * c]), __uint_as_float(sr[64 * h + 2 * c + 1])),
+                    for (int k = 0; k < 32; ++k) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[64 * h + 2 * k]), __uint_as_float(sr[64 * h + 2 * k + 1])),
                                               by, less);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
-                        sum[c & 1] = __fadd2_rn(sum[c & 1], x);
-                        w[c] = pack2<T>(x.x, x.y);
+                        sum[k & 1] = __fadd2_rn(sum[k & 1], x);
+                        w[k] = pack2<T>(x.x, x.y);
                     }
                     tmem_store32(s_col + 32 * h, w);
                 }
                 tmem_store_wait();
+                tc_fence_before_sync();
+                warp_arrive(&bars.p_full[i], lane);
                 const float2 both = __fadd2_rn(sum[0], sum[1]);
                 l += both.x + both.y;
-                tc_fence_before_sync();
-                mbar_arrive(smem_u32(&bars.p_full[i]));
             }
             if (!ok) break;
-            if (steps > 0) {
+
+            // ---- the next piece's queries are on their way before this one's result is complete. (A short
+            // item's join uses the queries' place: there they wait.)
+            const Row e = c;
+            const bool begins = walk.pc.a == 0, split = !begins || walk.pc.e < walk.pc.it.units, joined = e.alt && walk.pc.e - walk.pc.a > 1;
+            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
+            if (begins && share.y > kTicketParts) {  // (the CTA's last piece)
+                merge0 = make_int4(walk.pc.s.t0, walk.pc.rt * R, min(R, walk.pc.s.n * p.group - walk.pc.rt * R), walk.pc.kvh);
+                merge1 = make_int4(share.y, 0, 0, 0);
+            }
+            more = walk.next(p, R, U);
+            if (more) c = row_of(walk.pc);
+            if (more && !e.alt) load_q(c);
+            if (e.steps > 0) {
                 if (!(ok = warp_wait(&bars.o_full[i], o_phase, ab))) break;
                 o_phase ^= 1;
                 tc_fence_after_sync();
@@ -354,23 +427,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             // ---- a short item: stream 1 leaves its result where the queries were, stream 0 adds it to its own
             float *const xbuf = reinterpret_cast<float *>(smem);
             float keep = 1.f, add = 0.f;
-            if (alt) {
+            if (e.alt) {
                 if (i == 1) {
-                    if (steps > 0) {
+                    if (e.steps > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
+                        for (int k = 0; k < D; k += 32) {
                             uint32_t o[32];
-                            tmem_load32(o_col + c, o);
+                            tmem_load32(o_col + k, o);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)  // swizzled: a thread's row, conflict-free 16-byte pieces
-                                *reinterpret_cast<uint4 *>(xbuf + row * D + (((c + k) / 4) ^ (row & 7)) * 4) =
-                                    make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            for (int b = 0; b < 32; b += 4)  // swizzled: a thread's row, conflict-free 16-byte pieces
+                                *reinterpret_cast<uint4 *>(xbuf + row * D + (((k + b) / 4) ^ (row & 7)) * 4) =
+                                    make_uint4(o[b], o[b + 1], o[b + 2], o[b + 3]);
                         }
                     }
                     x_ml[row] = make_float2(m, l);
                     tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&bars.x_given));
-                    if (!(ok = warp_wait(&bars.x_taken, x_phase, ab))) break;
+                    warp_arrive(&bars.x_given, lane);
                 } else {
                     if (!(ok = warp_wait(&bars.x_given, x_phase, ab))) break;
                     const float2 other = x_ml[row];
@@ -380,101 +452,122 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                     m = to;
                     l = l * keep + other.y * add;
                 }
-                x_phase ^= 1;
             }
 
-            const bool begins = pc.a == 0, split = !begins || pc.e < pc.it.units;
-            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
-            if (!(alt && i == 1)) {
-                T *const dst = static_cast<T *>(p.out) + (s.t0 + tok) * p.o_ts + head * p.o_hs;
-                float *const part = p.part_o + (paged_slot(share.x, static_cast<int>(blockIdx.x) - share.x) * R + r) * D;
-                const bool joined = alt && n > 1;
-                auto store = [&](int c, const float(&v)[32]) {  // 32 finished values of the row
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4 *>(dst + c + k) =
-                            make_uint4(pack2<T>(v[k], v[k + 1]), pack2<T>(v[k + 2], v[k + 3]), pack2<T>(v[k + 4], v[k + 5]),
-                                       pack2<T>(v[k + 6], v[k + 7]));
-                };
-                auto store_lse = [&](float M, float L) {
-                    if (p.lse)
-                        p.lse[static_cast<int64_t>(s.t0 + tok) * p.kv_heads * p.group + head] =
-                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
-                };
-                const float inv = split ? 1.f : (l > 0.f || l != l ? p.v_scale / l : 0.f);
-                const float f = keep * inv, g = add * inv;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+            if (!(e.alt && i == 1)) {
+                T *const dst = static_cast<T *>(p.out) + e.tok * p.o_ts + e.head * p.o_hs;
+                const int mine = static_cast<int>(blockIdx.x) - share.x;  // this CTA's part of a split item
+                auto own = [&](int k, float (&v)[32]) {  // 32 values of this row's result
                     uint32_t o[32];
-                    tmem_load32(o_col + c, o);
-                    float v[32];
+                    tmem_load32(o_col + k, o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * f;
+                    for (int b = 0; b < 32; ++b) v[b] = __uint_as_float(o[b]) * keep;
                     if (joined) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(xbuf + row * D + (((c + k) / 4) ^ (row & 7)) * 4);
-                            v[k] = fmaf(x.x, g, v[k]);
-                            v[k + 1] = fmaf(x.y, g, v[k + 1]);
-                            v[k + 2] = fmaf(x.z, g, v[k + 2]);
-                            v[k + 3] = fmaf(x.w, g, v[k + 3]);
+                        for (int b = 0; b < 32; b += 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(xbuf + row * D + (((k + b) / 4) ^ (row & 7)) * 4);
+                            v[b] = fmaf(x.x, add, v[b]);
+                            v[b + 1] = fmaf(x.y, add, v[b + 1]);
+                            v[b + 2] = fmaf(x.z, add, v[b + 2]);
+                            v[b + 3] = fmaf(x.w, add, v[b + 3]);
                         }
                     }
-                    if (real && !split) store(c, v);
-                    if (real && split) {
+                };
+                auto store = [&](int k, const float (&v)[32], float by) {
+                    if (e.real) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(part + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        for (int b = 0; b < 32; b += 8)
+                            *reinterpret_cast<uint4 *>(dst + k + b) =
+                                make_uint4(pack2<T>(v[b] * by, v[b + 1] * by), pack2<T>(v[b + 2] * by, v[b + 3] * by),
+                                           pack2<T>(v[b + 4] * by, v[b + 5] * by), pack2<T>(v[b + 6] * by, v[b + 7] * by));
+                    }
+                };
+                auto store_lse = [&](float M, float L) {
+                    if (e.real && p.lse)
+                        p.lse[static_cast<int64_t>(e.tok) * p.kv_heads * p.group + e.head] =
+                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                };
+                bool last = false;
+                unsigned *const ticket = p.ticket + share.x * kTicketWarps + warp;
+                const bool by_ticket = split && share.y <= kTicketParts;
+                if (!split) {
+                    const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        float v[32];
+                        own(k, v);
+                        store(k, v, inv);
+                    }
+                    store_lse(m, l);
+                } else {
+                    // the last to finish need not write its part down
+                    if (by_ticket) last = paged_all_others(ticket, share.y, lane);
+                    if (!last) {
+                        const int64_t at = paged_slot(share.x, mine) * R + e.r;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            float v[32];
+                            own(k, v);
+                            if (e.real) {
+#pragma unroll
+                                for (int b = 0; b < 32; b += 4)
+                                    *reinterpret_cast<float4 *>(p.part_o + at * D + k + b) = make_float4(v[b], v[b + 1], v[b + 2], v[b + 3]);
+                            }
+                        }
+                        if (e.real) p.part_ml[at] = make_float2(m, l);
+                        if (by_ticket) last = paged_last(ticket, share.y, lane);
                     }
                 }
-                tc_fence_before_sync();
-                if (alt) mbar_arrive(smem_u32(&bars.x_taken));
-                if (real && !split) store_lse(m, l);
-                if (real && split) p.part_ml[(part - p.part_o) / D] = make_float2(m, l);
-                if (split && share.y <= kTicketParts &&
-                    paged_last(p.ticket + share.x * kTicketWarps + warp, share.y, lane) && real) {
+                if (last) {  // joins the parts, in their order whoever does it
                     float2 ml[kTicketParts];
                     float M = -INFINITY, L = 0.f;
 #pragma unroll
                     for (int k = 0; k < kTicketParts; ++k) {
-                        ml[k] = k < share.y ? __ldcg(p.part_ml + paged_slot(share.x, k) * R + r) : make_float2(-INFINITY, 0.f);
+                        ml[k] = make_float2(-INFINITY, 0.f);
+                        if (k == mine) ml[k] = make_float2(m, l);
+                        else if (k < share.y && e.real) ml[k] = __ldcg(p.part_ml + paged_slot(share.x, k) * R + e.r);
                         M = fmaxf(M, ml[k].x);
                     }
 #pragma unroll
                     for (int k = 0; k < kTicketParts; ++k) {
                         ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
-                        L += ml[k].x * ml[k].y;
+                        L = fmaf(ml[k].x, ml[k].y, L);
                     }
-                    const float done = L > 0.f || L != L ? p.v_scale / L : 0.f;
+                    const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
+                    for (int k = 0; k < D; k += 32) {
+                        float v[32], x[32];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                        for (int b = 0; b < 32; ++b) v[b] = 0.f;
 #pragma unroll 1
-                        for (int k = 0; k < share.y; ++k) {
-                            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (paged_slot(share.x, k) * R + r) * D + c);
-                            const float w = (k == 0 ? ml[0].x : k == 1 ? ml[1].x : k == 2 ? ml[2].x : ml[3].x) * done;
+                        for (int part = 0; part < share.y; ++part) {
+                            const float w = part == 0 ? ml[0].x : part == 1 ? ml[1].x : part == 2 ? ml[2].x : ml[3].x;
+                            if (part == mine) {
+                                own(k, x);
+                            } else {
+                                const float4 *src = reinterpret_cast<const float4 *>(
+                                    p.part_o + (paged_slot(share.x, part) * R + e.r) * D + k);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 x = __ldcg(src + e);
-                                v[4 * e] = fmaf(x.x, w, v[4 * e]);
-                                v[4 * e + 1] = fmaf(x.y, w, v[4 * e + 1]);
-                                v[4 * e + 2] = fmaf(x.z, w, v[4 * e + 2]);
-                                v[4 * e + 3] = fmaf(x.w, w, v[4 * e + 3]);
+                                for (int b = 0; b < 8; ++b) {
+                                    const float4 y = e.real ? __ldcg(src + b) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    x[4 * b] = y.x, x[4 * b + 1] = y.y, x[4 * b + 2] = y.z, x[4 * b + 3] = y.w;
+                                }
                             }
+#pragma unroll
+                            for (int b = 0; b < 32; ++b) v[b] = fmaf(x[b], w, v[b]);
                         }
-                        store(c, v);
+                        store(k, v, inv);
                     }
                     store_lse(M, L);
                 }
-                __syncwarp();
+                tc_fence_before_sync();
             }
-            if (begins && share.y > kTicketParts) {  // this CTA's last piece
-                merge0 = make_int4(s.t0, pc.rt * R, rows, pc.kvh);
-                merge1 = make_int4(share.y, 0, 0, 0);
+            if (e.alt) {
+                if (i == 0) warp_arrive(&bars.x_taken, lane);
+                if (!(ok = warp_wait(&bars.x_taken, x_phase, ab))) break;
+                x_phase ^= 1;
+                if (more) load_q(c);
             }
-            walk.next(p, R, U);
         }
         if (tid == 0) {
             p.merge[2 * blockIdx.x] = merge0;
@@ -484,67 +577,73 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) {
             // -------------------------------------------------- matrix products
-            if (lane == 0) {
-                constexpr uint32_t id_s = idesc_16<T>(128, 128, false), id_o = idesc_16<T>(128, D, true);
-                // (a descriptor's low bits are the address in units of 16 bytes: stepping it is an addition)
-                const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_mn(ring, SH::BOX);
-                uint32_t seq = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-                bool ok = true;
-                auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    ok = ok && mbar_wait(smem_u32(bar), parity, ab);
-                    return ok;
-                };
-                while (ok && walk.left > 0) {
-                    const PagedPiece &pc = walk.pc;
-                    const bool alt = pc.s.n * p.group - pc.rt * R <= 128;
-                    const int n = pc.e - pc.a;
-                    const int steps[2] = {stream_steps(n, alt, 0), stream_steps(n, alt, 1)};
-                    // tile j of the piece: keys in stage (seq + 2 j) % S, values in the next
-                    auto scores = [&](int i, int t) {
-                        const uint32_t k = seq + 2u * (alt ? 2 * t + i : t), st = k % S;
-                        if (!wait(&bars.full[st], (k / S) & 1)) return;
+            // (the whole warp runs this role, one lane issues)
+            const uint32_t who = elect_one();
+            constexpr uint32_t id_s = idesc_16<T>(128, 128, false), id_o = idesc_16<T>(128, D, true);
+            // a descriptor's low bits are the address in units of 16 bytes: stepping it is an addition
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_mn(ring, SH::BOX);
+            uint32_t seq = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            while (ok && walk.left > 0) {
+                const PagedPiece &pc = walk.pc;
+                const bool alt = pc.s.n * p.group - pc.rt * R <= 128;
+                const int n = pc.e - pc.a;
+                const int steps[2] = {stream_steps(n, alt, 0), stream_steps(n, alt, 1)};
+                // tile j of the piece: keys in stage (seq + 2 j) % S, values in the next. Where both streams use a
+                // tile, stream 0 waits for it and stream 1 releases it.
+                auto scores = [&](int i, int t) {
+                    const uint32_t k = seq + 2u * (alt ? 2 * t + i : t), st = __shfl_sync(0xFFFFFFFFu, k % S, 0);
+                    if (alt || i == 0) {
+                        ok = warp_wait(&bars.full[st], (k / S) & 1, ab);
+                        if (!ok) return;
                         tc_fence_after_sync();
-                        const uint64_t qa = q_desc + (alt ? 0u : i * (SH::TILE >> 4)), ka = k_desc + st * (SH::TILE >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t o = ((kk >> 2) * SH::BOX + (kk & 3) * 32) >> 4;
-                            umma_bf16(tmem + 128u * i, qa + o, ka + o, id_s, kk > 0);
-                        }
-                        umma_commit(smem_u32(&bars.s_full[i]));
-                        if (alt || i == 1) umma_commit(smem_u32(&bars.empty[st]));
-                    };
-                    auto results = [&](int i, int t) {
-                        const uint32_t k = seq + 2u * (alt ? 2 * t + i : t) + 1, st = k % S;
-                        if (!wait(&bars.full[st], (k / S) & 1) || !wait(&bars.p_full[i], p_phase[i])) return;
-                        p_phase[i] ^= 1;
-                        tc_fence_after_sync();
-                        const uint64_t va = v_desc + st * (SH::TILE >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_ts(tmem + SH::O_COL + D * i, tmem + 128u * i + 8u * kk, va + kk * (2048 >> 4), id_o, t > 0 || kk > 0);
-                        if (alt || i == 1) umma_commit(smem_u32(&bars.empty[st]));
-                        if (t + 1 == steps[i]) umma_commit(smem_u32(&bars.o_full[i]));
-                    };
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        if (!(alt && i == 1)) {
-                            if (!wait(&bars.q_full[i], q_phase[i])) break;
-                            q_phase[i] ^= 1;
-                        }
-                        if (steps[i] > 0) scores(i, 0);
                     }
-                    for (int t = 0; t < steps[0] && ok; ++t)
-                        for (int i = 0; i < 2 && ok; ++i)
-                            if (t < steps[i]) {
-                                results(i, t);
-                                if (ok && t + 1 < steps[i]) scores(i, t + 1);
-                            }
-                    seq += 2u * n;
-                    walk.next(p, R, U);
+                    const uint64_t qa = q_desc + (alt ? 0u : i * (SH::TILE >> 4)), ka = k_desc + st * (SH::TILE >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t o = ((kk >> 2) * SH::BOX + (kk & 3) * 32) >> 4;
+                        umma_ss(who, tm + 128u * i, qa + o, ka + o, id_s, kk > 0);
+                    }
+                    umma_commit_if(who, &bars.s_full[i]);
+                    if (alt || i == 1) umma_commit_if(who, &bars.empty[st]);
+                };
+                auto results = [&](int i, int t) {
+                    const uint32_t k = seq + 2u * (alt ? 2 * t + i : t) + 1, st = __shfl_sync(0xFFFFFFFFu, k % S, 0);
+                    if (alt || i == 0) ok = warp_wait(&bars.full[st], (k / S) & 1, ab);
+                    ok = ok && warp_wait(&bars.p_full[i], p_phase[i], ab);
+                    if (!ok) return;
+                    p_phase[i] ^= 1;
+                    tc_fence_after_sync();
+                    const uint64_t va = v_desc + st * (SH::TILE >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(who, tm + SH::O_COL + D * i, tm + 128u * i + 8u * kk, va + kk * (2048 >> 4), id_o, t > 0 || kk > 0);
+                    if (alt || i == 1) umma_commit_if(who, &bars.empty[st]);
+                    if (t + 1 == steps[i]) umma_commit_if(who, &bars.o_full[i]);
+                };
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (ok && !(alt && i == 1)) {
+                        ok = warp_wait(&bars.q_full[i], q_phase[i], ab);
+                        q_phase[i] ^= 1;
+                        tc_fence_after_sync();
+                    }
+                    if (ok && steps[i] > 0) scores(i, 0);
                 }
-                if (!ok) {  // products in flight still write TMEM: see them off before it is freed
-                    umma_commit(smem_u32(&bars.done));
-                    mbar_wait(smem_u32(&bars.done), 0, ab, false);
-                }
+                for (int t = 0; t < steps[0] && ok; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (ok && t < steps[i]) {
+                            results(i, t);
+                            if (ok && t + 1 < steps[i]) scores(i, t + 1);
+                        }
+                seq += 2u * n;
+                walk.next(p, R, U);
+            }
+            if (!ok) {  // products in flight still write TMEM: see them off before it is freed
+                umma_commit_if(who, &bars.done);
+                mbar_wait(smem_u32(&bars.done), 0, ab, false);
             }
             __syncwarp();
         } else {
