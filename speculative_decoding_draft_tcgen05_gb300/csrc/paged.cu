@@ -180,8 +180,8 @@ extern "C" dflash_status dflash_paged_init(const dflash_paged_config *cfg, void 
     const size_t rows = 2 * static_cast<size_t>(c->num_sms) * dfl::kTileRows;
     static_assert(dfl::kTileRows >= 2 * 32, "two CTAs of up to 32 rows per SM, or one of kTileRows");
     const size_t o_bytes = rows * cfg->head_dim * sizeof(float), ml_bytes = rows * sizeof(float2);
-    const size_t merge_bytes = 2 * static_cast<size_t>(c->num_sms) * 2 * sizeof(int4);
-    const size_t ticket_bytes = 2 * static_cast<size_t>(c->num_sms) * dfl::kTicketWarps * sizeof(unsigned);
+    const size_t merge_bytes = 2 * static_cast<size_t>(c->num_sms) * 3 * sizeof(int4);
+    const size_t ticket_bytes = 3 * static_cast<size_t>(c->num_sms) * dfl::kTicketWarps * sizeof(unsigned);
     const size_t total = o_bytes + ml_bytes + merge_bytes + ticket_bytes + 256;
     if (dfl::prepare_attend_rows(smem_optin) != cudaSuccess || dfl::prepare_attend_tile(smem_optin) != cudaSuccess ||
         cudaMalloc(&c->block, total) != cudaSuccess) {
@@ -307,7 +307,7 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
         e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, grid, s);
     } else {
         rows = most_rows <= 16 ? 16 : 32;
-        grid = 2 * h->num_sms;
+        grid = (rows == 16 ? 3 : 2) * h->num_sms;
         e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, grid, s);
     }
     if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, s);

@@ -70,26 +70,32 @@ __device__ __forceinline__ PagedSeq paged_seq(const AttendParams &p, int b)
     return s;
 }
 
-// A work item is (sequence, key/value head, R consecutive rows); row r of a
-// sequence's n * group rows is query head kvh * group + r % group of its new
-// token r / group, so the heads that share keys share a tile. [lo, hi): keys
-// that some row of the item sees (empty: lo = hi). A unit is U keys on a
-// multiple of U; an item without keys still has one unit, which writes zeros.
+// How a kernel cuts the work. A work item is (sequence, key/value head, R
+// consecutive rows); row r of a sequence's n * group rows is query head
+// kvh * group + r % group of its new token r / group, so the heads that share
+// keys share a tile. A unit is U keys on a multiple of U. Starting and
+// finishing an item costs about as much as C units.
+struct PagedCut {
+    int R, U, C;
+};
+
+// [lo, hi): keys that some row of the item sees (empty: lo = hi). An item
+// without keys still has one unit, which writes zeros.
 struct PagedItem {
     int lo, hi, u0, units;
 };
 
-__device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const PagedSeq &s, int rt, int R, int U)
+__device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const PagedSeq &s, int rt, PagedCut k)
 {
-    const int r0 = rt * R, r1 = min(s.n * p.group, r0 + R);
+    const int r0 = rt * k.R, r1 = min(s.n * p.group, r0 + k.R);
     const int ta = p.by_group.div(r0), tb = p.by_group.div(r1 - 1);
     const int base = s.len - s.n;
     PagedItem it;
     it.hi = p.causal ? min(s.len, max(0, base + tb + 1)) : s.len;
     it.lo = p.window > 0 ? max(0, base + ta - p.window + 1) : 0;
     if (it.lo >= it.hi) it.lo = it.hi = 0;
-    it.u0 = it.lo / U;
-    it.units = max(1, (it.hi + U - 1) / U - it.u0);
+    it.u0 = it.lo / k.U;
+    it.units = max(1, (it.hi + k.U - 1) / k.U - it.u0);
     return it;
 }
 
@@ -98,42 +104,48 @@ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const Page
     return (s.n * p.group + R - 1) / R;
 }
 
-// The units of all items in order (sequence, head, row tile), split evenly:
-// CTA c of G takes units [total * c / G, total * (c + 1) / G), with G the grid,
-// or `total` where that is less: every one of the G CTAs has a unit, so the
-// CTAs that share an item are consecutive. Every CTA works
-// this out for itself from the lengths on the device: the launch needs
-// nothing from the host, and a captured graph stays valid when they change.
+// The items' costs (units + C) in order (sequence, head, row tile) are split
+// evenly: boundary c of G lies at total * c / G, moved to the item's start
+// where it falls into the C, and CTA c takes what is between boundaries c and
+// c + 1. G is the grid, or less where the CTAs would get less than `least`
+// each. Every CTA works this out for itself from the lengths on the device:
+// the launch needs nothing from the host, and a captured graph stays valid
+// when they change.
 struct PagedPlan {
     int64_t total, begin, end;
-    int64_t ctas;  // G
-    int b;         // sequence of unit `begin`
-    int per_head;  // its units per key/value head
-    int64_t off;   // the offset of `begin` within that sequence's units
+    int ctas;      // G
+    int b;         // sequence of `begin`
+    int kvh, off;  // the head that it falls into, and the offset within the head
 };
 
-constexpr int kPlanSeqs = 512;  // sequences whose units are kept in shared memory
-
-// Units per key/value head of a sequence, by one thread or by a whole warp.
-__device__ __forceinline__ int paged_units(const AttendParams &p, const PagedSeq &s, int R, int U)
+// n / d, which the 64-bit division (some hundred cycles) is only needed for when n does not fit 32 bits.
+__device__ __forceinline__ int64_t paged_div(int64_t n, int d)
 {
-    const int nrt = paged_row_tiles(p, s, R);
+    return n >> 32 ? n / d : static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+}
+
+constexpr int kPlanSeqs = 512;  // sequences whose costs are kept in shared memory
+
+// Cost per key/value head of a sequence, by one thread or by a whole warp.
+__device__ __forceinline__ int paged_cost(const AttendParams &p, const PagedSeq &s, PagedCut k)
+{
+    const int nrt = paged_row_tiles(p, s, k.R);
     int u = 0;
-    for (int rt = 0; rt < nrt; ++rt) u += paged_item(p, s, rt, R, U).units;
+    for (int rt = 0; rt < nrt; ++rt) u += paged_item(p, s, rt, k).units + k.C;
     return u;
 }
 
-__device__ __forceinline__ int paged_units_warp(const AttendParams &p, const PagedSeq &s, int R, int U, int lane)
+__device__ __forceinline__ int paged_cost_warp(const AttendParams &p, const PagedSeq &s, PagedCut k, int lane)
 {
-    const int nrt = paged_row_tiles(p, s, R);
+    const int nrt = paged_row_tiles(p, s, k.R);
     int u = 0;
-    for (int rt = lane; rt < nrt; rt += 32) u += paged_item(p, s, rt, R, U).units;
+    for (int rt = lane; rt < nrt; rt += 32) u += paged_item(p, s, rt, k).units + k.C;
     return __reduce_add_sync(0xFFFFFFFFu, u);
 }
 
-// units: kPlanSeqs ints of shared memory that are free until the plan is made.
+// cost: kPlanSeqs ints of shared memory that are free until the plan is made.
 template <int NT>
-__device__ PagedPlan paged_plan(const AttendParams &p, int R, int U, int *units)
+__device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, int *cost)
 {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ PagedPlan plan;
@@ -147,8 +159,8 @@ __device__ PagedPlan paged_plan(const AttendParams &p, int R, int U, int *units)
     for (int b = tid; b < p.B; b += NT) {
         if (kept) {
             const PagedSeq s = paged_seq(p, b);
-            const bool by_warp = paged_row_tiles(p, s, R) > 2;
-            units[b] = by_warp ? -1 : paged_units(p, s, R, U);
+            const bool by_warp = paged_row_tiles(p, s, cut.R) > 2;
+            cost[b] = by_warp ? -1 : paged_cost(p, s, cut);
             many |= by_warp;
         }
         if (blockIdx.x == 0) {  // what paged_seq() had to clamp
@@ -159,23 +171,25 @@ __device__ PagedPlan paged_plan(const AttendParams &p, int R, int U, int *units)
     }
     if (__syncthreads_or(many)) {
         for (int b = warp; b < p.B; b += NT / 32)
-            if (units[b] < 0) {
-                const int u = paged_units_warp(p, paged_seq(p, b), R, U, lane);
+            if (cost[b] < 0) {
+                const int u = paged_cost_warp(p, paged_seq(p, b), cut, lane);
                 __syncwarp();
-                if (lane == 0) units[b] = u;
+                if (lane == 0) cost[b] = u;
             }
         __syncthreads();
     }
-    auto seq_units = [&](int b) {
-        return static_cast<int64_t>(kept ? units[b] : paged_units(p, paged_seq(p, b), R, U)) * p.kv_heads;
-    };
+    auto head_cost = [&](int b) { return kept ? cost[b] : paged_cost(p, paged_seq(p, b), cut); };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_units(b);
+    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(head_cost(b)) * p.kv_heads;
     int64_t scan = mine;
+    if (p.B > 1) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-        if (lane >= o) scan += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+            if (lane >= o) scan += v;
+        }
+    } else {
+        scan = __shfl_sync(0xFFFFFFFFu, mine, 0);
     }
     if (lane == 31) warp_sum[warp] = scan;
     __syncthreads();
@@ -185,56 +199,70 @@ __device__ PagedPlan paged_plan(const AttendParams &p, int R, int U, int *units)
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const int64_t G = min(static_cast<int64_t>(gridDim.x), total), c = blockIdx.x;
-    const int64_t begin = c < G ? total * c / G : 0, end = c < G ? total * (c + 1) / G : 0;
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), paged_div(total + least - 1, least)));
+    const int c = blockIdx.x;
+    int64_t begin = 0, end = 0;
+    if (c < G) {  // total * c / G, in parts that fit
+        const int64_t q = paged_div(total, G);
+        const int rest = static_cast<int>(total - q * G);
+        begin = q * c + static_cast<uint32_t>(rest * c) / static_cast<uint32_t>(G);
+        end = q * (c + 1) + static_cast<uint32_t>(rest * (c + 1)) / static_cast<uint32_t>(G);
+    }
     if (begin < end ? (before <= begin && begin < before + mine) : tid == 0) {
-        int64_t off = begin - before, u = 1;
-        int b = b0;
+        int64_t off = begin - before;
+        int b = b0, per_head = 1;
         if (begin < end)
             for (; b < b1; ++b) {
-                u = seq_units(b);
-                if (off < u) break;
-                off -= u;
+                per_head = head_cost(b);
+                if (off < static_cast<int64_t>(per_head) * p.kv_heads) break;
+                off -= static_cast<int64_t>(per_head) * p.kv_heads;
             }
         plan.total = total;
         plan.begin = begin;
         plan.end = end;
         plan.ctas = G;
         plan.b = b;
-        plan.per_head = static_cast<int>(u / p.kv_heads);
-        plan.off = off;
+        plan.kvh = begin < end ? static_cast<int>(paged_div(off, per_head)) : 0;
+        plan.off = static_cast<int>(off - static_cast<int64_t>(plan.kvh) * per_head);
     }
     __syncthreads();
     return plan;
 }
 
-// The CTA's pieces one after the other: (sequence, head, row tile) and the
-// units [a, e) of it, with whether the item begins before or goes on after.
+// The CTA's pieces one after the other: units [a, e) of an item.
 struct PagedPiece {
     PagedSeq s;
     PagedItem it;
     int b, kvh, rt;
-    int a, e;  // unit range within the item
+    int a, e;
 };
 
 struct PagedWalk {
     PagedPiece pc;
-    int64_t left;
-    int nrt, off;
+    int64_t at, end;  // where the item starts in the sum of costs; the CTA's end
+    int nrt;
+    bool more;        // pc is a piece of this CTA
 
-    // Whole warps call it.
-    __device__ void start(const AttendParams &p, const PagedPlan &plan, int R, int U)
+    // Unit of the item that a boundary (an offset from `at`) stands for.
+    __device__ __forceinline__ int unit_at(int64_t off, PagedCut k) const
     {
-        left = plan.end - plan.begin;
-        if (left <= 0) return;
+        return static_cast<int>(max(int64_t(0), min(off - k.C, static_cast<int64_t>(pc.it.units))));
+    }
+    // Whole warps call it.
+    __device__ void start(const AttendParams &p, const PagedPlan &plan, PagedCut k)
+    {
+        end = plan.end;
+        more = plan.begin < plan.end;
+        if (!more) return;
         const int lane = threadIdx.x & 31;
         pc.b = plan.b;
         pc.s = paged_seq(p, pc.b);
-        nrt = paged_row_tiles(p, pc.s, R);
-        pc.kvh = static_cast<int>(plan.off / plan.per_head);
-        int rem = static_cast<int>(plan.off - static_cast<int64_t>(pc.kvh) * plan.per_head);
-        for (int from = 0;; from += 32) {  // the row tile that holds unit `rem` of the head, 32 at a time
-            const int u = from + lane < nrt ? paged_item(p, pc.s, from + lane, R, U).units : 0;
+        nrt = paged_row_tiles(p, pc.s, k.R);
+        pc.kvh = plan.kvh;
+        pc.rt = 0;
+        int rem = plan.off;
+        for (int from = 0; nrt > 1; from += 32) {  // the row tile that holds cost `rem` of the head, 32 at a time
+            const int u = from + lane < nrt ? paged_item(p, pc.s, from + lane, k).units + k.C : 0;
             int upto = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -243,27 +271,26 @@ struct PagedWalk {
             }
             const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
             if (rem < all) {
-                const int k = __ffs(__ballot_sync(0xFFFFFFFFu, rem < upto)) - 1;
-                off = rem - __shfl_sync(0xFFFFFFFFu, upto - u, k);
-                pc.rt = from + k;
+                const int l = __ffs(__ballot_sync(0xFFFFFFFFu, rem < upto)) - 1;
+                rem -= __shfl_sync(0xFFFFFFFFu, upto - u, l);
+                pc.rt = from + l;
                 break;
             }
             rem -= all;
         }
-        pc.it = paged_item(p, pc.s, pc.rt, R, U);
-        cut();
+        at = plan.begin - rem;
+        pc.it = paged_item(p, pc.s, pc.rt, k);
+        pc.a = unit_at(rem, k);
+        pc.e = unit_at(end - at, k);
+        more = pc.e > pc.a;
+        // (rem < units + C, so pc.a < units; a share that ends where it begins has no piece)
     }
-    __device__ void cut()
+    // On to the next piece, if the CTA's share has one.
+    __device__ bool next(const AttendParams &p, PagedCut k)
     {
-        pc.a = off;
-        pc.e = static_cast<int>(min(static_cast<int64_t>(pc.it.units), off + left));
-    }
-    // On to the next piece; false when the CTA's share is done.
-    __device__ bool next(const AttendParams &p, int R, int U)
-    {
-        left -= pc.e - pc.a;
-        if (left <= 0) return false;
-        off = 0;
+        at += pc.it.units + k.C;
+        more = at + k.C < end;
+        if (!more) return false;
         if (++pc.rt == nrt) {
             pc.rt = 0;
             if (++pc.kvh == p.kv_heads) {
@@ -271,28 +298,33 @@ struct PagedWalk {
                 do {
                     ++pc.b;
                     pc.s = paged_seq(p, pc.b);
-                    nrt = paged_row_tiles(p, pc.s, R);
-                } while (nrt == 0);  // ends: there are units left
+                    nrt = paged_row_tiles(p, pc.s, k.R);
+                } while (nrt == 0);  // ends: there are items left
             }
         }
-        pc.it = paged_item(p, pc.s, pc.rt, R, U);
-        cut();
+        pc.it = paged_item(p, pc.s, pc.rt, k);
+        pc.a = 0;
+        pc.e = unit_at(end - at, k);
         return true;
     }
+    // Whether another CTA has a part of the piece's item.
+    __device__ __forceinline__ bool split() const { return pc.a > 0 || pc.e < pc.it.units; }
 };
 
-// CTA that holds unit u of `total` over G CTAs.
-__device__ __forceinline__ int paged_owner(int64_t u, int64_t total, int64_t G)
+__device__ __forceinline__ int64_t paged_quot(int64_t n, int64_t d)
 {
-    return static_cast<int>(((u + 1) * G - 1) / total);
+    return (n | d) >> 32 ? n / d : static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
 }
 
-// The CTAs that share the current piece's item: the first, and how many.
-__device__ __forceinline__ int2 paged_sharers(const PagedPlan &plan, const PagedWalk &w)
+// The CTAs that share the piece's item: the first, and how many. Boundary c
+// lies inside the item (after its first unit, before its last one's end) if
+// at + C < total * c / G rounded down < at + C + units.
+__device__ __forceinline__ int2 paged_sharers(const PagedPlan &plan, const PagedWalk &w, PagedCut k)
 {
-    const int64_t first = plan.end - w.left - w.pc.a;
-    const int c0 = paged_owner(first, plan.total, plan.ctas);
-    return make_int2(c0, paged_owner(first + w.pc.it.units - 1, plan.total, plan.ctas) - c0 + 1);
+    const int64_t low = w.at + k.C + 1, high = w.at + k.C + w.pc.it.units;  // low <= boundary < high
+    const int64_t first = paged_quot(low * plan.ctas + plan.total - 1, plan.total);  // smallest c with total * c / G >= low
+    const int64_t end = paged_quot(high * plan.ctas + plan.total - 1, plan.total);   // smallest c with total * c / G >= high
+    return make_int2(static_cast<int>(first - 1), static_cast<int>(end - first + 1));
 }
 
 // Slot of part i of the item that CTA c0 begins.

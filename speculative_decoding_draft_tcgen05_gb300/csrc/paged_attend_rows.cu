@@ -8,9 +8,16 @@ namespace dfl {
 
 namespace {
 
-constexpr int kRowsThreads = 128;  // 4 warps, 2 CTAs per SM
+constexpr int kRowsThreads = 128;  // 4 warps
+#ifndef DFL_ROWS_COST
+#define DFL_ROWS_COST 5
+#endif
+#ifndef DFL_ROWS_LEAST
+#define DFL_ROWS_LEAST 1
+#endif
+constexpr int kRowsCost = DFL_ROWS_COST, kRowsLeast = DFL_ROWS_LEAST;
 constexpr int kRowsWarps = kRowsThreads / 32;
-constexpr int kRowsRing = 24 * 1024;  // ring bytes of one warp
+template <int MT> constexpr int rows_ring() { return MT == 1 ? 16 * 1024 : 24 * 1024; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -76,13 +83,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t x)
 
 // Shapes of one variant. CH: 16-byte chunks of a key's row; a stage of a
 // warp's ring holds 16 keys and their values.
-template <int D, bool FP8>
+template <int D, int MT, bool FP8>
 struct RowsShape {
     static constexpr int ROW = D * (FP8 ? 1 : 2);
     static constexpr int CH = ROW / 16;
     static constexpr int TILE = 16 * ROW;
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int STAGES = (kRowsRing / STAGE < 6) ? kRowsRing / STAGE : 6;
+    static constexpr int STAGES = (rows_ring<MT>() / STAGE < 6) ? rows_ring<MT>() / STAGE : 6;
     // Physical chunk of (row, chunk): 8 rows at one chunk (an ldmatrix phase)
     // and the 16 of a half-row write fall into distinct banks.
     __device__ static uint32_t at(int row, int c)
@@ -127,10 +134,11 @@ constexpr int kRowsPad = 8;  // floats between merge rows
 // leave 3/4 or more of its 128-row tiles empty here.
 // ---------------------------------------------------------------------------
 template <int D, int MT, typename QT, bool FP8>
-__global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
+__global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
 {
     using CT = typename std::conditional<FP8, __half, QT>::type;  // type of the matrix products
-    using SH = RowsShape<D, FP8>;
+    using SH = RowsShape<D, MT, FP8>;
+    constexpr int kRowsRing = rows_ring<MT>();
     constexpr int R = MT * 16, S = SH::STAGES, CH = SH::CH;
     constexpr int QCH = D * 2 / 16;  // chunks of a query row
     extern __shared__ __align__(128) uint8_t smem[];
@@ -144,19 +152,60 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
 
     pdl_trigger();
     pdl_wait();
-    const PagedPlan plan = paged_plan<kRowsThreads>(p, R, kRowsUnit, reinterpret_cast<int *>(smem));
+    constexpr PagedCut cut = {R, kRowsUnit, kRowsCost};
+    const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, kRowsLeast, reinterpret_cast<int *>(smem));
     PagedWalk walk;
-    walk.start(p, plan, R, kRowsUnit);
+    walk.start(p, plan, cut);
     int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
-    if (walk.left > 0) {
+    if (walk.more) {
         for (;;) {
             const PagedPiece &pc = walk.pc;
             const PagedSeq &s = pc.s;
             const int rows = min(R, s.n * p.group - pc.rt * R);  // real rows of this item
             const int base = s.len - s.n;
 
+            // ---- the ring: unit j of the piece, this warp's 16 keys
+            const int n_units = pc.e - pc.a, first = pc.it.u0 + pc.a;
+            const int lo = pc.it.lo, hi = pc.it.hi;
+            const uint8_t *kb = static_cast<const uint8_t *>(p.k);
+            const uint8_t *vb = static_cast<const uint8_t *>(p.v);
+            constexpr int ES = FP8 ? 1 : 2;
+            int pages = -1;  // lane l: the page of unit pages_from + l
+            int pages_from = -(1 << 30);
+            auto issue = [&](int j) {
+                if (j < n_units) {
+                    if (j - pages_from >= 32) {
+                        pages_from = j;
+                        const int key = (first + j + lane) * kRowsUnit + 16 * warp;
+                        pages = -1;
+                        if (j + lane < n_units && key < hi && key + 16 > lo) {
+                            pages = __ldg(p.table + pc.b * p.table_stride + p.by_page.div(key));
+                            if (pages < 0 || pages >= p.num_pages) {
+                                pages = -1;
+                                atomicOr(p.err, DEV_ERR_PLACE);
+                            }
+                        }
+                    }
+                    const int page = __shfl_sync(0xFFFFFFFFu, pages, j - pages_from);
+                    const int key = (first + j) * kRowsUnit + 16 * warp;
+                    const int slot = key - p.by_page.div(key) * p.page;
+                    const int64_t at = page * p.page_stride + slot * p.slot_stride + pc.kvh * p.head_stride;
+                    const uint32_t dst = ring + (j % S) * SH::STAGE;
+#pragma unroll
+                    for (int i = 0; i < 16 * CH / 32; ++i) {
+                        const int row = (32 * i + lane) / CH, c = (32 * i + lane) % CH;
+                        const bool ok = page >= 0 && key + row >= lo && key + row < hi;
+                        const int64_t o = ok ? (at + row * p.slot_stride) * ES + 16 * c : 0;
+                        cp_async16(dst + SH::at(row, c), kb + o, ok);
+                        cp_async16(dst + SH::TILE + SH::at(row, c), vb + o, ok);
+                    }
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int j = 0; j < S - 1; ++j) issue(j);
+
             // ---- queries to shared memory, whole 16-byte pieces; rows past the item's are zero
-            __syncthreads();
             for (int i = tid; i < R * QCH; i += kRowsThreads) {
                 const int r = i / QCH, c = i % QCH;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -209,47 +258,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
             }
             least_upto = __reduce_min_sync(0xFFFFFFFFu, least_upto);
             most_after = __reduce_max_sync(0xFFFFFFFFu, most_after);
-
-            // ---- the ring: unit j of the piece, this warp's 16 keys
-            const int n_units = pc.e - pc.a, first = pc.it.u0 + pc.a;
-            const int lo = pc.it.lo, hi = pc.it.hi;
-            const uint8_t *kb = static_cast<const uint8_t *>(p.k);
-            const uint8_t *vb = static_cast<const uint8_t *>(p.v);
-            constexpr int ES = FP8 ? 1 : 2;
-            int pages = -1;  // lane l: the page of unit pages_from + l
-            int pages_from = -(1 << 30);
-            auto issue = [&](int j) {
-                if (j < n_units) {
-                    if (j - pages_from >= 32) {
-                        pages_from = j;
-                        const int key = (first + j + lane) * kRowsUnit + 16 * warp;
-                        pages = -1;
-                        if (j + lane < n_units && key < hi && key + 16 > lo) {
-                            pages = __ldg(p.table + pc.b * p.table_stride + p.by_page.div(key));
-                            if (pages < 0 || pages >= p.num_pages) {
-                                pages = -1;
-                                atomicOr(p.err, DEV_ERR_PLACE);
-                            }
-                        }
-                    }
-                    const int page = __shfl_sync(0xFFFFFFFFu, pages, j - pages_from);
-                    const int key = (first + j) * kRowsUnit + 16 * warp;
-                    const int slot = key - p.by_page.div(key) * p.page;
-                    const int64_t at = page * p.page_stride + slot * p.slot_stride + pc.kvh * p.head_stride;
-                    const uint32_t dst = ring + (j % S) * SH::STAGE;
-#pragma unroll
-                    for (int i = 0; i < 16 * CH / 32; ++i) {
-                        const int row = (32 * i + lane) / CH, c = (32 * i + lane) % CH;
-                        const bool ok = page >= 0 && key + row >= lo && key + row < hi;
-                        const int64_t o = ok ? (at + row * p.slot_stride) * ES + 16 * c : 0;
-                        cp_async16(dst + SH::at(row, c), kb + o, ok);
-                        cp_async16(dst + SH::TILE + SH::at(row, c), vb + o, ok);
-                    }
-                }
-                cp_async_commit();
-            };
-#pragma unroll
-            for (int j = 0; j < S - 1; ++j) issue(j);
 
             float o[MT][D / 8][4];
             float m[2 * MT], l[2 * MT];
@@ -431,8 +439,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                 }
             }
             __syncthreads();
-            const bool begins = pc.a == 0, split = !begins || pc.e < pc.it.units;
-            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
+            const bool begins = pc.a == 0, split = walk.split();
+            const int2 share = split ? paged_sharers(plan, walk, cut) : make_int2(0, 1);
             const int64_t mine_slot = paged_slot(share.x, static_cast<int>(blockIdx.x) - share.x);
             auto finish = [&](int r, int c, const float(&acc)[8], float M, float L) {
                 const int rr = pc.rt * R + r, t = p.by_group.div(rr), hd = pc.kvh * p.group + rr - t * p.group;
@@ -498,7 +506,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
                 merge0 = make_int4(s.t0, pc.rt * R, rows, pc.kvh);
                 merge1 = make_int4(share.y, 0, 0, 0);
             }
-            if (!walk.next(p, R, kRowsUnit)) break;
+            if (!walk.next(p, cut)) break;
+            __syncthreads();  // the rings and the queries' place are free again
         }
     }
     if (tid == 0) {
@@ -508,105 +517,102 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attend_rows_kernel(const __gr
 }
 
 // Joins the items that were split over more than kTicketParts CTAs. Every
-// block reads the whole list (an entry per CTA) and takes quads of rows in
-// turn; its warps take a quad's parts in turn (always the same ones, so the
-// sum does not depend on the order in which anything finished), four rows of
-// loads in flight each, and the warps' sums are added in shared memory.
-constexpr int kMergeWarps = 8, kMergeQuad = 4, kMergeMost = 1024;
+// block reads the whole list (an entry per CTA of the attention launch) and
+// takes the listed items' rows in turn, a row at a time: its warps take the
+// row's parts in turn, several in flight, and their sums are added in shared
+// memory. Which warp adds which parts is fixed, so the result does not depend
+// on the order in which anything finished. A call with few rows is all
+// latency here: three dependent reads (list; maxima and parts together).
+constexpr int kMergeWarps = 8, kMergeMost = 1024;
 
 template <int D, typename QT>
 __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R, int G)
 {
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, AHEAD = 4;  // parts in flight per warp
     using F = typename std::conditional<V == 4, float4, float2>::type;
-    __shared__ int list[kMergeMost], listed;
-    __shared__ float top[kMergeWarps], sums[kMergeWarps][kMergeQuad];
-    __shared__ __align__(16) float part[kMergeWarps][kMergeQuad][D];  // (read and written in pieces of F)
+    __shared__ int4 item_of[kMergeMost];
+    __shared__ int c0_of[kMergeMost], parts_of[kMergeMost], warp_n[kMergeWarps];
+    __shared__ float sums[kMergeWarps];
+    __shared__ __align__(16) float part[kMergeWarps][D];  // (read and written in pieces of F)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    if (warp == 0) {
-        int n = 0;
-#pragma unroll 4
-        for (int c = lane; c < (G + 31) / 32 * 32; c += 32) {
-            const bool has = c < G && p.merge[2 * c + 1].x > 0;
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
-            if (has) list[n + __popc(m & ((1u << lane) - 1u))] = c;
-            n += __popc(m);
+    int entries = 0;
+    for (int from = 0; from < G; from += kMergeWarps * 32) {  // the list, without its empty entries
+        const int c = from + tid;
+        const int n = c < G ? p.merge[2 * c + 1].x : 0;
+        const int4 item = c < G ? p.merge[2 * c] : make_int4(0, 0, 0, 0);
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, n > 0);
+        if (lane == 0) warp_n[warp] = __popc(m);
+        __syncthreads();
+        int at = entries + __popc(m & ((1u << lane) - 1u));
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            if (w < warp) at += warp_n[w];
+            entries += warp_n[w];
         }
-        if (lane == 0) listed = n;
+        if (n > 0) {
+            item_of[at] = item;
+            c0_of[at] = c;
+            parts_of[at] = n;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int entries = listed;
-    for (int64_t k = blockIdx.x; k < static_cast<int64_t>(entries) * (R / kMergeQuad); k += gridDim.x) {
-        const int c0 = list[k % entries], r0 = static_cast<int>(k / entries) * kMergeQuad;
-        const int4 item = p.merge[2 * c0];
-        const int parts = p.merge[2 * c0 + 1].x, rows = min(kMergeQuad, item.z - r0);
-        if (rows <= 0) continue;  // (the whole block)
-        // the rows' maxima: two warps a row
-        float m = -INFINITY;
-        if (warp / 2 < rows)
-            for (int i = (warp & 1) * 32 + lane; i < parts; i += 64) m = fmaxf(m, p.part_ml[paged_slot(c0, i) * R + r0 + warp / 2].x);
+    for (int64_t k = blockIdx.x; k < static_cast<int64_t>(entries) * R; k += gridDim.x) {
+        const int r = static_cast<int>(k / entries), which = static_cast<int>(k - static_cast<int64_t>(r) * entries);
+        const int4 item = item_of[which];
+        const int c0 = c0_of[which], parts = parts_of[which];
+        if (r >= item.z) continue;  // (the whole block)
+        // every warp finds the row's maximum for itself
+        float M = -INFINITY;
+        for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[paged_slot(c0, i) * R + r].x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (lane == 0) top[warp] = m;
-        __syncthreads();
-        float M[kMergeQuad], L[kMergeQuad], acc[kMergeQuad][V];
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        float L = 0.f, acc[V];
 #pragma unroll
-        for (int q = 0; q < kMergeQuad; ++q) {
-            M[q] = fmaxf(top[2 * q], top[2 * q + 1]);
-            L[q] = 0.f;
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+        for (int i0 = warp; i0 < parts; i0 += AHEAD * kMergeWarps) {
+            F x[AHEAD];
+            float2 ml[AHEAD];
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[q][v] = 0.f;
-        }
-#pragma unroll 2
-        for (int i = warp; i < parts; i += kMergeWarps) {
-            const int64_t row = paged_slot(c0, i) * R + r0;
-            F x[kMergeQuad];
-            float2 ml[kMergeQuad];
-#pragma unroll
-            for (int q = 0; q < kMergeQuad; ++q) {
-                const int64_t at = row + (q < rows ? q : 0);
-                ml[q] = p.part_ml[at];
-                x[q] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
+            for (int a = 0; a < AHEAD; ++a) {
+                const int i = i0 + a * kMergeWarps;
+                const int64_t at = paged_slot(c0, i < parts ? i : i0) * R + r;
+                ml[a] = p.part_ml[at];
+                x[a] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
+                if (i >= parts) ml[a] = make_float2(-INFINITY, 0.f);
             }
 #pragma unroll
-            for (int q = 0; q < kMergeQuad; ++q) {
-                const float f = ml[q].x == -INFINITY ? 0.f : ex2(ml[q].x - M[q]);
-                L[q] = fmaf(f, ml[q].y, L[q]);
-                const float *xs = reinterpret_cast<const float *>(&x[q]);
+            for (int a = 0; a < AHEAD; ++a) {
+                const float f = ml[a].x == -INFINITY ? 0.f : ex2(ml[a].x - M);
+                L = fmaf(f, ml[a].y, L);
+                const float *xs = reinterpret_cast<const float *>(&x[a]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) acc[q][v] = fmaf(f, xs[v], acc[q][v]);
+                for (int v = 0; v < V; ++v) acc[v] = fmaf(f, xs[v], acc[v]);
             }
         }
+        F mine;
+        float *ms = reinterpret_cast<float *>(&mine);
 #pragma unroll
-        for (int q = 0; q < kMergeQuad; ++q) {
-            F x;
-            float *xs = reinterpret_cast<float *>(&x);
-#pragma unroll
-            for (int v = 0; v < V; ++v) xs[v] = acc[q][v];
-            *reinterpret_cast<F *>(&part[warp][q][V * lane]) = x;
-            if (lane == 0) sums[warp][q] = L[q];
-        }
+        for (int v = 0; v < V; ++v) ms[v] = acc[v];
+        *reinterpret_cast<F *>(&part[warp][V * lane]) = mine;
+        if (lane == 0) sums[warp] = L;
         __syncthreads();
-        const int q = tid / 64, d = tid % 64 * 2;
-        if (q < rows && d < D) {
+        if (2 * tid < D) {
             float total = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
             for (int w = 0; w < kMergeWarps; ++w) {
-                total += sums[w][q];
-                a += part[w][q][d];
-                b += part[w][q][d + 1];
+                total += sums[w];
+                a += part[w][2 * tid];
+                b += part[w][2 * tid + 1];
             }
-            const int rr = item.y + r0 + q, t = p.by_group.div(rr), hd = item.w * p.group + rr - t * p.group;
+            const int rr = item.y + r, t = p.by_group.div(rr), hd = item.w * p.group + rr - t * p.group;
             const float inv = total > 0.f || total != total ? p.v_scale / total : 0.f;
-            *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + (item.x + t) * p.o_ts + hd * p.o_hs + d) =
+            *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + (item.x + t) * p.o_ts + hd * p.o_hs + 2 * tid) =
                 pack2<QT>(a * inv, b * inv);
-            if (d == 0 && p.lse) {
-                const float mm = fmaxf(top[2 * q], top[2 * q + 1]);
+            if (tid == 0 && p.lse)
                 p.lse[static_cast<int64_t>(item.x + t) * p.kv_heads * p.group + hd] =
-                    mm == -INFINITY ? -INFINITY : (mm + lg2(total)) * 0.69314718055994531f;
-            }
+                    M == -INFINITY ? -INFINITY : (M + lg2(total)) * 0.69314718055994531f;
         }
         __syncthreads();
     }
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
 template <int D, int MT>
 constexpr size_t rows_smem()
 {
-    return rows_q_bytes<D, MT>() + kRowsWarps * kRowsRing;
+    return rows_q_bytes<D, MT>() + kRowsWarps * rows_ring<MT>();
 }
 
 // Calls f with the kernel of a variant and its shared memory.

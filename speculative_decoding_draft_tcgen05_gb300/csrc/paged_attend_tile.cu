@@ -17,6 +17,10 @@ constexpr int kLoadWarps = 3;
 constexpr int kStreamRegs = 208, kOtherRegs = 88;
 
 constexpr uint32_t kTmemCols = 512;
+#ifndef DFL_TILE_COST
+#define DFL_TILE_COST 4
+#endif
+constexpr int kTileCost = DFL_TILE_COST, kTileLeast = 1;
 
 template <int D>
 struct TileShape {
@@ -246,6 +250,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
 {
     using SH = TileShape<D>;
     constexpr int R = kTileRows, U = kTileUnit, S = SH::STAGES;
+    constexpr PagedCut cut = {R, U, kTileCost};
     const AttendParams &p = tp.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileBars bars;
@@ -278,12 +283,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
-    const PagedPlan plan = paged_plan<kTileThreads>(p, R, U, reinterpret_cast<int *>(smem));  // holds block barriers
+    const PagedPlan plan = paged_plan<kTileThreads>(p, cut, kTileLeast, reinterpret_cast<int *>(smem));  // holds block barriers
     tc_fence_after_sync();
     const uint32_t tmem = bars.tmem;
     int *const ab = &bars.abort_flag;
     PagedWalk walk;
-    walk.start(p, plan, R, U);
+    walk.start(p, plan, cut);
 
     if (warp < 8) {
         // ------------------------------------------------------ softmax streams
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             warp_arrive(&bars.q_full[i], lane);
         };
 
-        bool ok = true, more = walk.left > 0;
+        bool ok = true, more = walk.more;
         Row c = {};
         if (more) {
             c = row_of(walk.pc);
@@ -409,13 +414,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             // ---- the next piece's queries are on their way before this one's result is complete. (A short
             // item's join uses the queries' place: there they wait.)
             const Row e = c;
-            const bool begins = walk.pc.a == 0, split = !begins || walk.pc.e < walk.pc.it.units, joined = e.alt && walk.pc.e - walk.pc.a > 1;
-            const int2 share = split ? paged_sharers(plan, walk) : make_int2(0, 1);
+            const bool begins = walk.pc.a == 0, split = walk.split(), joined = e.alt && walk.pc.e - walk.pc.a > 1;
+            const int2 share = split ? paged_sharers(plan, walk, cut) : make_int2(0, 1);
             if (begins && share.y > kTicketParts) {  // (the CTA's last piece)
                 merge0 = make_int4(walk.pc.s.t0, walk.pc.rt * R, min(R, walk.pc.s.n * p.group - walk.pc.rt * R), walk.pc.kvh);
                 merge1 = make_int4(share.y, 0, 0, 0);
             }
-            more = walk.next(p, R, U);
+            more = walk.next(p, cut);
             if (more) c = row_of(walk.pc);
             if (more && !e.alt) load_q(c);
             if (e.steps > 0) {
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_mn(ring, SH::BOX);
             uint32_t seq = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             bool ok = true;
-            while (ok && walk.left > 0) {
+            while (ok && walk.more) {
                 const PagedPiece &pc = walk.pc;
                 const bool alt = pc.s.n * p.group - pc.rt * R <= 128;
                 const int n = pc.e - pc.a;
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                             if (ok && t + 1 < steps[i]) scores(i, t + 1);
                         }
                 seq += 2u * n;
-                walk.next(p, R, U);
+                walk.next(p, cut);
             }
             if (!ok) {  // products in flight still write TMEM: see them off before it is freed
                 umma_commit_if(who, &bars.done);
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             const int br = tp.box_rows, groups = U / br;  // row groups of a tile: 1, 2, 4 or 8
             uint32_t seq = 0, last_tma = 0;
             bool ok = true, any_tma = false;
-            while (ok && walk.left > 0) {
+            while (ok && walk.more) {
                 const PagedPiece &pc = walk.pc;
                 const int n = pc.e - pc.a, len = pc.s.len, lo = pc.it.lo, hi = pc.it.hi;
                 const int from = p.by_page.div(lo) * p.page;  // the first page that is used
@@ -718,7 +723,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         if (lane == 0) mbar_arrive(bar);
                     }
                 }
-                walk.next(p, R, U);
+                walk.next(p, cut);
             }
             // On an abort: wait (again with a limit) for the copies in flight. Stages are filled in order, so
             // those of the last S tiles cover them.
