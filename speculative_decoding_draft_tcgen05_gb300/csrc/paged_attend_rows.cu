@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                         M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
             };
             // a warp always takes the same rows, so the CTAs that share an item join them warp by warp
-            for (int i = tid; i < rows * (D / 8); i += kRowsThreads) {
+#pragma unroll
+            for (int i = tid; i < R * (D / 8); i += kRowsThreads) {
                 const int r = i / (D / 8), c = i % (D / 8);
                 float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                         reinterpret_cast<const float *>(ring_ptr + w * kRowsRing) + r * OS + 8 * c);
                     add8(acc, f, src[0], src[1]);
                 }
+                if (r >= rows) continue;
                 if (!split) {
                     finish(r, c, acc, M, L);
                 } else {
@@ -563,7 +565,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
         const int4 item = item_of[which];
         const int c0 = c0_of[which], parts = parts_of[which];
         if (r >= item.z) continue;  // (the whole block)
-        // every warp finds the row's maximum for itself
+        // the first parts of this warp are on their way while it finds the row's maximum
+        F x[AHEAD];
+        float2 ml[AHEAD];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+                const int i = i0 + a * kMergeWarps;
+                const int64_t at = paged_slot(c0, i < parts ? i : 0) * R + r;
+                ml[a] = p.part_ml[at];
+                x[a] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
+                if (i >= parts) ml[a] = make_float2(-INFINITY, 0.f);
+            }
+        };
+        fetch(warp);
         float M = -INFINITY;
         for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[paged_slot(c0, i) * R + r].x);
 #pragma unroll
@@ -572,16 +587,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.f;
         for (int i0 = warp; i0 < parts; i0 += AHEAD * kMergeWarps) {
-            F x[AHEAD];
-            float2 ml[AHEAD];
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int i = i0 + a * kMergeWarps;
-                const int64_t at = paged_slot(c0, i < parts ? i : i0) * R + r;
-                ml[a] = p.part_ml[at];
-                x[a] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
-                if (i >= parts) ml[a] = make_float2(-INFINITY, 0.f);
-            }
+            if (i0 != warp) fetch(i0);
 #pragma unroll
             for (int a = 0; a < AHEAD; ++a) {
                 const float f = ml[a].x == -INFINITY ? 0.f : ex2(ml[a].x - M);

@@ -89,19 +89,27 @@ def _stream_of(t, stream):
     return _binding()[2](stream)
 
 
-def _rows(t, tokens, heads, head_dim, dtype, name):
-    """(address, token stride, head stride) of [tokens, heads, head_dim] rows with a contiguous last dimension."""
+def _rows(t, shape, dtype, name):
+    """(address, token stride, head stride) of rows [tokens, heads, head_dim] with a contiguous last dimension."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (tokens, heads, head_dim):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     a, b, c = t.stride()
     if c != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     # a dimension of one row may carry any stride
-    return t.data_ptr(), a if tokens > 1 else 0, b if heads > 1 else 0
+    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
+
+
+def _positions(t, tokens):
+    if t.dtype is not _torch().int32:
+        raise TypeError(f"positions must be torch.int32, got {t.dtype}")
+    if t.shape != (tokens,) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"positions must be a contiguous CUDA tensor [{tokens}]")
+    return t.data_ptr()
 
 
 def _int32(t, shape, name):
@@ -192,28 +200,31 @@ class PagedBatch:
         self.ref = ctypes.addressof(self.c)
 
 
+_NONE = (None, 0, 0)
+
+
 def dflash_qk_norm_rope(q, k, q_out, k_out, transform, positions=None, stream=None):
     """q_out, k_out [tokens, heads, head_dim] = the transform of q and k (either pair may be None; in place is
     allowed); positions [tokens] int32."""
-    L, check, _ = _binding()
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    tokens, _, head_dim = x.shape
     dt = x.dtype
-    code = _dtypes().get(dt)
-    transform.check(dt, head_dim)
-    none = (None, 0, 0)
-    a = b = c = d = none
-    hq = hk = 0
+    qs = ks = None
+    a = b = c = d = _NONE
     if q is not None:
-        hq = q.shape[1]
-        a, b = _rows(q, tokens, hq, head_dim, dt, "q"), _rows(q_out, tokens, hq, head_dim, dt, "q_out")
+        qs = q.shape
+        a, b = _rows(q, qs, dt, "q"), _rows(q_out, qs, dt, "q_out")
     if k is not None:
-        hk = k.shape[1]
-        c, d = _rows(k, tokens, hk, head_dim, dt, "k"), _rows(k_out, tokens, hk, head_dim, dt, "k_out")
-    at = None if positions is None else _int32(positions, (tokens,), "positions")
-    st = L.dflash_qk_norm_rope(*a, *b, *c, *d, tokens, hq, hk, head_dim, -1 if code is None else code, transform.ref, at,
+        ks = k.shape
+        c, d = _rows(k, ks, dt, "k"), _rows(k_out, ks, dt, "k_out")
+        if qs is not None and (ks[0] != qs[0] or ks[2] != qs[2]):
+            raise ValueError(f"q and k must have the same tokens and head_dim, got {list(qs)} and {list(ks)}")
+    tokens, _, head_dim = x.shape
+    transform.check(dt, head_dim)
+    L, check, _ = _binding()
+    st = L.dflash_qk_norm_rope(*a, *b, *c, *d, tokens, qs[1] if qs else 0, ks[1] if ks else 0, head_dim,
+                               _dtypes().get(dt, -1), transform.ref, None if positions is None else _positions(positions, tokens),
                                _stream_of(x, stream))
     if st:
         check(st, "dflash_qk_norm_rope")
@@ -234,43 +245,44 @@ def dflash_paged_init(*, heads, kv_heads, head_dim, page_size, dtype, cache_dtyp
 
 def dflash_paged_append(handle, cache, batch, k, v, transform=None, *, q=None, q_out=None, positions=None, stream=None):
     """Writes k (transformed) and v [tokens, kv_heads, head_dim] to the batch's places in the cache; with q also
-    q_out = the transformed queries [tokens, heads, head_dim]."""
-    L, check, _ = _binding()
-    tokens, hk, head_dim = k.shape
-    dt = k.dtype
-    if transform is not None:
-        transform.check(dt, head_dim)
-    none = (None, 0, 0)
-    a = b = none
+    q_out = the transformed queries [tokens, heads, head_dim]. All of the handle's shapes and dtype."""
+    dt, ks = k.dtype, k.shape
+    tokens = ks[0]
+    a = b = _NONE
     if q is not None:
-        hq = q.shape[1]
-        a, b = _rows(q, tokens, hq, head_dim, dt, "q"), _rows(q_out, tokens, hq, head_dim, dt, "q_out")
-    at = None if positions is None else _int32(positions, (tokens,), "positions")
+        qs = q.shape
+        if qs[0] != tokens:
+            raise ValueError(f"q and k must have the same tokens, got {qs[0]} and {tokens}")
+        a, b = _rows(q, qs, dt, "q"), _rows(q_out, qs, dt, "q_out")
+    ref = None
+    if transform is not None:
+        transform.check(dt, ks[2])
+        ref = transform.ref
     batch.c.tokens = tokens
-    st = L.dflash_paged_append(handle, cache.ref, batch.ref, *_rows(k, tokens, hk, head_dim, dt, "k"),
-                               *_rows(v, tokens, hk, head_dim, dt, "v"), None if transform is None else transform.ref,
-                               at, *a, *b, _stream_of(k, stream))
+    L, check, _ = _binding()
+    st = L.dflash_paged_append(handle, cache.ref, batch.ref, *_rows(k, ks, dt, "k"), *_rows(v, ks, dt, "v"), ref,
+                               None if positions is None else _positions(positions, tokens), *a, *b,
+                               _stream_of(k, stream))
     if st:
         check(st, "dflash_paged_append")
 
 
 def dflash_paged_attend(handle, cache, batch, q, out, *, lse=None, causal=True, window=0, scale=None, stream=None):
     """out [tokens, heads, head_dim] = attention of q over the cache (scale None: 1 / sqrt(head_dim)); lse
-    [tokens, heads] fp32."""
-    L, check, _ = _binding()
-    tokens, heads, head_dim = q.shape
-    dt = q.dtype
+    [tokens, heads] fp32. All of the handle's shapes and dtype."""
+    dt, qs = q.dtype, q.shape
     at = None
     if lse is not None:
         if lse.dtype is not _torch().float32:
             raise TypeError(f"lse must be torch.float32, got {lse.dtype}")
-        if lse.shape != (tokens, heads) or not lse.is_contiguous() or not lse.is_cuda:
-            raise ValueError(f"lse must be a contiguous CUDA tensor [{tokens}, {heads}]")
+        if lse.shape != qs[:2] or not lse.is_contiguous() or not lse.is_cuda:
+            raise ValueError(f"lse must be a contiguous CUDA tensor {list(qs[:2])}")
         at = lse.data_ptr()
-    batch.c.tokens = tokens
-    st = L.dflash_paged_attend(handle, cache.ref, batch.ref, *_rows(q, tokens, heads, head_dim, dt, "q"),
-                               *_rows(out, tokens, heads, head_dim, dt, "out"), at, 1 if causal else 0, window,
-                               head_dim ** -0.5 if scale is None else scale, _stream_of(q, stream))
+    batch.c.tokens = qs[0]
+    L, check, _ = _binding()
+    st = L.dflash_paged_attend(handle, cache.ref, batch.ref, *_rows(q, qs, dt, "q"), *_rows(out, qs, dt, "out"), at,
+                               1 if causal else 0, window, qs[2] ** -0.5 if scale is None else scale,
+                               _stream_of(q, stream))
     if st:
         check(st, "dflash_paged_attend")
 
@@ -303,8 +315,8 @@ class PagedAttention:
                              f"{cache.dtype} [pages, {', '.join(map(str, cache.shape))}]")
         if x.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}, got {x.dtype}")
-        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != self.head_dim:
-            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(x.shape)}")
+        if x.shape[1:] != (heads, self.head_dim):
+            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {list(x.shape)}")
 
     def append(self, cache, batch, k, v, transform=None, *, q=None, q_out=None, positions=None, stream=None):
         self._fits(cache, k, self.kv_heads, "k")
