@@ -280,7 +280,7 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     p.by_group = dfl::FastDiv(p.group);
     p.by_page = dfl::FastDiv(p.page);
     p.causal = causal;
-    p.window = window;
+    p.window = window < (1 << 30) ? window : 1 << 30;  // (places are sums with it)
     p.scale_log2 = scale * 1.44269504088896341f * (fp8 ? cache->k_scale : 1.f);
     p.v_scale = fp8 ? cache->v_scale : 1.f;
     p.part_o = h->part_o;
@@ -310,7 +310,7 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
         grid = (rows == 16 ? 3 : 2) * h->num_sms;
         e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, grid, s);
     }
-    if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, s);
+    if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, rows == dfl::kTileRows, 3 * h->num_sms, s);
     if (e != cudaSuccess) return paged_fail(DFLASH_ERR_CUDA, "attention: a launch failed (error %lld)", e);
     return DFLASH_OK;
 }

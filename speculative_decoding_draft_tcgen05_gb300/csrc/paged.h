@@ -80,7 +80,7 @@ struct AttendParams {
     // (a counter per warp's rows, at the CTA that begins the item, zero between
     // calls); one over more CTAs by the merge kernel, whose list has entry c
     // for the item that CTA c begins.
-    float *part_o;     // [2 * grid][rows][head_dim]
+    float *part_o;     // [2 * grid][rows * head_dim]
     float2 *part_ml;   // [2 * grid][rows] running maximum (log2) and sum
     int4 *merge;       // [2 * grid]: first token row, first row, rows, key/value head | CTAs (0: nothing to do)
     unsigned *ticket;  // [grid][kTicketWarps]
@@ -102,7 +102,9 @@ int tile_box_rows(int page);
 // tm_k, tm_v: host_make_tmap_pages() with boxes of tile_box_rows() slots.
 cudaError_t launch_attend_tile(const AttendParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int head_dim,
                                int dtype, int grid, cudaStream_t s);
-// Joins the partial results of the split items (rows per item, `grid` CTAs of the attention launch).
-cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s);
+// Joins the items split over many CTAs (rows per item, `entries` CTAs of the
+// attention launch); by_value: parts laid out [value / 4][row][4] instead of [row][value].
+cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int entries, bool by_value,
+                                int grid, cudaStream_t s);
 
 }  // namespace dfl

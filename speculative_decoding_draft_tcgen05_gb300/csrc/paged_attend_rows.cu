@@ -524,11 +524,12 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
 // row's parts in turn, several in flight, and their sums are added in shared
 // memory. Which warp adds which parts is fixed, so the result does not depend
 // on the order in which anything finished. A call with few rows is all
-// latency here: three dependent reads (list; maxima and parts together).
+// latency here: two dependent reads (the list; maxima and parts together).
+// Value d of row r of a part is at r * row_step + d / 4 * value_step + d % 4.
 constexpr int kMergeWarps = 8, kMergeMost = 1024;
 
 template <int D, typename QT>
-__global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R, int G)
+__global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __grid_constant__ AttendParams p, int R, int G, int row_step, int value_step)
 {
     constexpr int V = D / 32, AHEAD = 4;  // parts in flight per warp
     using F = typename std::conditional<V == 4, float4, float2>::type;
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
                 const int i = i0 + a * kMergeWarps;
                 const int64_t at = paged_slot(c0, i < parts ? i : 0) * R + r;
                 ml[a] = p.part_ml[at];
-                x[a] = *reinterpret_cast<const F *>(p.part_o + at * D + V * lane);
+                x[a] = *reinterpret_cast<const F *>(p.part_o + (at - r) * D + r * row_step + V * lane / 4 * value_step + V * lane % 4);
                 if (i >= parts) ml[a] = make_float2(-INFINITY, 0.f);
             }
         };
@@ -675,15 +676,19 @@ cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, i
     });
 }
 
-cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int grid, cudaStream_t s)
+cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int entries, bool by_value,
+                                int grid, cudaStream_t s)
 {
-    if (grid > kMergeMost) return cudaErrorInvalidValue;
+    if (entries > kMergeMost) return cudaErrorInvalidValue;
     const dim3 g(grid), b(kMergeWarps * 32);
+    const int row_step = by_value ? 4 : head_dim, value_step = by_value ? 4 * rows : 4;
     if (head_dim == 128)
-        return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<128, __nv_bfloat16>, g, b, 0, s, 1, p, rows, grid)
-                                    : launch_ex(attend_merge_kernel<128, __half>, g, b, 0, s, 1, p, rows, grid);
-    return dtype == DFLASH_BF16 ? launch_ex(attend_merge_kernel<64, __nv_bfloat16>, g, b, 0, s, 1, p, rows, grid)
-                                : launch_ex(attend_merge_kernel<64, __half>, g, b, 0, s, 1, p, rows, grid);
+        return dtype == DFLASH_BF16
+                   ? launch_ex(attend_merge_kernel<128, __nv_bfloat16>, g, b, 0, s, 1, p, rows, entries, row_step, value_step)
+                   : launch_ex(attend_merge_kernel<128, __half>, g, b, 0, s, 1, p, rows, entries, row_step, value_step);
+    return dtype == DFLASH_BF16
+               ? launch_ex(attend_merge_kernel<64, __nv_bfloat16>, g, b, 0, s, 1, p, rows, entries, row_step, value_step)
+               : launch_ex(attend_merge_kernel<64, __half>, g, b, 0, s, 1, p, rows, entries, row_step, value_step);
 }
 
 }  // namespace dfl

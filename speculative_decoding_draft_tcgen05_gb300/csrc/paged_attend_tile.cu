@@ -35,9 +35,10 @@ struct TileShape {
 
 struct TileBars {
     uint64_t full[10], empty[10];  // ring of tiles
-    uint64_t q_full[2];            // (one arrival per warp, here and below) a stream's queries are in shared memory
+    uint64_t q_full[2];            // a stream's queries are in shared memory
+    uint64_t q_empty;              // the piece is done with the queries' place
     uint64_t s_full[2];            // its scores are in TMEM
-    uint64_t p_full[2];            // its weights are in TMEM
+    uint64_t p_full[2];            // its weights are in TMEM (an arrival per warp)
     uint64_t o_full[2];            // its results are complete
     uint64_t x_given, x_taken;     // joining the two streams of a short item
     uint64_t done;                 // on an abort: products in flight
@@ -172,6 +173,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
         : "memory");
 }
 
+// The n lowest bits (n of any size).
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -265,11 +272,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             mbar_init(smem_u32(&bars.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.q_full[i]), 4);
+            mbar_init(smem_u32(&bars.q_full[i]), kLoadWarps);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
             mbar_init(smem_u32(&bars.p_full[i]), 4);
             mbar_init(smem_u32(&bars.o_full[i]), 1);
         }
+        mbar_init(smem_u32(&bars.q_empty), 1);
         mbar_init(smem_u32(&bars.x_given), 4);
         mbar_init(smem_u32(&bars.x_taken), 4);
         mbar_init(smem_u32(&bars.done), 1);
@@ -322,28 +330,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             c.steps = stream_steps(pc.e - pc.a, c.alt, i);
             return c;
         };
-        // Its query to shared memory (of a short item, stream 0's rows serve both).
-        auto load_q = [&](const Row &c) {
-            if (c.alt && i == 1) return;
-            const T *src = static_cast<const T *>(p.q) + c.tok * p.q_ts + c.head * p.q_hs;
-            uint8_t *dst = smem + i * SH::TILE + row * 128;
-            uint4 v[D / 8];
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k)
-                v[k] = c.real ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k)
-                *reinterpret_cast<uint4 *>(dst + (k >> 3) * SH::BOX + (((k & 7) ^ (row & 7)) * 16)) = v[k];
-            fence_async_proxy();
-            warp_arrive(&bars.q_full[i], lane);
-        };
-
         bool ok = true, more = walk.more;
         Row c = {};
-        if (more) {
-            c = row_of(walk.pc);
-            load_q(c);
-        }
+        if (more) c = row_of(walk.pc);
         while (more) {
             const int least_upto = __reduce_min_sync(0xFFFFFFFFu, c.real ? c.upto : 0x7FFFFFFF);
             const int most_after = __reduce_max_sync(0xFFFFFFFFu, c.real ? c.after : -1);
@@ -356,10 +345,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 uint32_t sr[128];
                 tmem_load128(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
-                    const int hi = c.upto - key0, lo = c.after - key0;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k > hi || k <= lo) sr[k] = __float_as_uint(-INFINITY);
+                    for (int g = 0; g < 4; ++g) {  // a bit per key of 32
+                        const uint32_t seen = low_bits(c.upto + 1 - key0 - 32 * g) & ~low_bits(c.after + 1 - key0 - 32 * g);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(seen & (1u << k))) sr[32 * g + k] = __float_as_uint(-INFINITY);
+                    }
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -411,8 +403,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             }
             if (!ok) break;
 
-            // ---- the next piece's queries are on their way before this one's result is complete. (A short
-            // item's join uses the queries' place: there they wait.)
             const Row e = c;
             const bool begins = walk.pc.a == 0, split = walk.split(), joined = e.alt && walk.pc.e - walk.pc.a > 1;
             const int2 share = split ? paged_sharers(plan, walk, cut) : make_int2(0, 1);
@@ -422,7 +412,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             }
             more = walk.next(p, cut);
             if (more) c = row_of(walk.pc);
-            if (more && !e.alt) load_q(c);
             if (e.steps > 0) {
                 if (!(ok = warp_wait(&bars.o_full[i], o_phase, ab))) break;
                 o_phase ^= 1;
@@ -492,6 +481,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         p.lse[static_cast<int64_t>(e.tok) * p.kv_heads * p.group + e.head] =
                             M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
                 };
+                // Parts are laid out [value / 4][row]: a warp's rows are adjacent, so its accesses are whole lines.
+                auto part_at = [&](int64_t slot, int k) {
+                    return reinterpret_cast<float4 *>(p.part_o) + (slot * (D / 4) + k / 4) * R + e.r;
+                };
                 bool last = false;
                 unsigned *const ticket = p.ticket + share.x * kTicketWarps + warp;
                 const bool by_ticket = split && share.y <= kTicketParts;
@@ -508,7 +501,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                     // the last to finish need not write its part down
                     if (by_ticket) last = paged_all_others(ticket, share.y, lane);
                     if (!last) {
-                        const int64_t at = paged_slot(share.x, mine) * R + e.r;
+                        const int64_t slot = paged_slot(share.x, mine);
 #pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
                             float v[32];
@@ -516,10 +509,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                             if (e.real) {
 #pragma unroll
                                 for (int b = 0; b < 32; b += 4)
-                                    *reinterpret_cast<float4 *>(p.part_o + at * D + k + b) = make_float4(v[b], v[b + 1], v[b + 2], v[b + 3]);
+                                    *part_at(slot, k + b) = make_float4(v[b], v[b + 1], v[b + 2], v[b + 3]);
                             }
                         }
-                        if (e.real) p.part_ml[at] = make_float2(m, l);
+                        if (e.real) p.part_ml[slot * R + e.r] = make_float2(m, l);
                         if (by_ticket) last = paged_last(ticket, share.y, lane);
                     }
                 }
@@ -550,11 +543,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                             if (part == mine) {
                                 own(k, x);
                             } else {
-                                const float4 *src = reinterpret_cast<const float4 *>(
-                                    p.part_o + (paged_slot(share.x, part) * R + e.r) * D + k);
+                                const int64_t slot = paged_slot(share.x, part);
 #pragma unroll
                                 for (int b = 0; b < 8; ++b) {
-                                    const float4 y = e.real ? __ldcg(src + b) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    const float4 y = e.real ? __ldcg(part_at(slot, k + 4 * b)) : make_float4(0.f, 0.f, 0.f, 0.f);
                                     x[4 * b] = y.x, x[4 * b + 1] = y.y, x[4 * b + 2] = y.z, x[4 * b + 3] = y.w;
                                 }
                             }
@@ -571,7 +563,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 if (i == 0) warp_arrive(&bars.x_taken, lane);
                 if (!(ok = warp_wait(&bars.x_taken, x_phase, ab))) break;
                 x_phase ^= 1;
-                if (more) load_q(c);
+                if (tid == 0) mbar_arrive(smem_u32(&bars.q_empty));
             }
         }
         if (tid == 0) {
@@ -612,6 +604,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                     }
                     umma_commit_if(who, &bars.s_full[i]);
                     if (alt || i == 1) umma_commit_if(who, &bars.empty[st]);
+                    if (!alt && i == 1 && t + 1 == steps[1]) umma_commit_if(who, &bars.q_empty);
                 };
                 auto results = [&](int i, int t) {
                     const uint32_t k = seq + 2u * (alt ? 2 * t + i : t) + 1, st = __shfl_sync(0xFFFFFFFFu, k % S, 0);
@@ -655,8 +648,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             // -------------------------------------------------- keys and values
             const int lw = warp - 9, ltid = tid - 9 * 32;
             const int br = tp.box_rows, groups = U / br;  // row groups of a tile: 1, 2, 4 or 8
-            uint32_t seq = 0, last_tma = 0;
+            uint32_t seq = 0, last_tma = 0, q_phase = 1;
             bool ok = true, any_tma = false;
+            // The piece's queries, once the one before is done with their place; rows past the item's are zero.
+            auto load_q = [&](const PagedPiece &pc) {
+                if (!(ok = warp_wait(&bars.q_empty, q_phase, ab))) return;
+                q_phase ^= 1;
+                const int r0 = pc.rt * R, rows = min(R, pc.s.n * p.group - r0);
+                constexpr int CH = D / 8;  // 16-byte pieces of a row
+                for (int i = 0; i < (rows <= 128 ? 1 : 2); ++i) {
+#pragma unroll 8
+                    for (int x = ltid; x < 128 * CH; x += 32 * kLoadWarps) {
+                        const int row = x / CH, c = x % CH, r = 128 * i + row;
+                        const int t = p.by_group.div(r0 + r), g = r0 + r - t * p.group;
+                        const int64_t o = r < rows ? (pc.s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c : 0;
+                        const int bytes = r < rows ? 16 : 0;  // 0: zeros
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         q_s + i * SH::TILE + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16)),
+                                     "l"(static_cast<const T *>(p.q) + o), "r"(bytes)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_async_proxy();
+                    warp_arrive(&bars.q_full[i], lane);
+                }
+            };
             while (ok && walk.more) {
                 const PagedPiece &pc = walk.pc;
                 const int n = pc.e - pc.a, len = pc.s.len, lo = pc.it.lo, hi = pc.it.hi;
@@ -722,6 +738,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         }
                         if (lane == 0) mbar_arrive(bar);
                     }
+                    // (after the first keys and values: those find room in the ring while the piece before ends,
+                    // which the queries have to wait for)
+                    if (ok && j == 0) load_q(pc);
                 }
                 walk.next(p, cut);
             }
