@@ -33,7 +33,7 @@ __device__ __forceinline__ int warp_find(const int32_t *cu, int B, int t, int la
 }
 
 // ---------------------------------------------------------------------------
-// A block takes up to kPrepTokens tokens. It first finds their places in the
+// A block takes up to prep_tokens() tokens. It first finds their places in the
 // cache and positions (a chain of dependent small reads, once per block) and
 // brings their cosines and sines to shared memory. Then its warps share the
 // jobs: 32 / LPH heads of the queries, keys or values (LPH = D / 8 lanes to a
@@ -44,76 +44,79 @@ __device__ __forceinline__ int warp_find(const int32_t *cu, int B, int t, int la
 // between lanes, and the sum of squares is a shuffle over the head's lanes.
 //
 // Bound by HBM when the instructions per value stay near ten (each value is
-// read and written once); a job's loads are all in flight before the first is
-// used.
+// read and written once). Inputs come through asynchronous copies to shared
+// memory, kPrepAhead jobs of a warp in flight: the first ones while the block
+// looks up its places and angles, the others while the warp works.
 // ---------------------------------------------------------------------------
-constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
-constexpr int kPrepTokens = 16;
-constexpr int kPrepJob = 4;
+constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32, kPrepBlocks = 4;
+constexpr int kPrepJob = 4, kPrepAhead = 2;
+
+// Tokens of a block (with the copies' 32 KB, what fits 48 KB of shared memory).
+template <int D>
+constexpr int prep_tokens()
+{
+    return D <= 128 ? 16 : 8;
+}
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kPrepThreads, 3) prep_kernel(const __grid_constant__ PrepParams p, int per_block)
+__global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) prep_kernel(const __grid_constant__ PrepParams p, int per_block)
 {
     constexpr int LPH = D / 8, HPP = 32 / LPH;
-    __shared__ int tok_page[kPrepTokens], tok_slot[kPrepTokens], tok_pos[kPrepTokens];
-    __shared__ float4 angles[kPrepTokens * D / 4];  // [token][rotary]: cosines, then sines
+    constexpr int TOKENS = prep_tokens<D>();
+    __shared__ int64_t tok_row[TOKENS];        // its row of the cache (without the head)
+    __shared__ int tok_pos[TOKENS], tok_is[TOKENS];  // position; 1: stored, 0: no place, -1: padding
+    __shared__ float4 angles[TOKENS * D / 4];  // [token][rotary]: cosines, then sines
+    __shared__ uint4 ring[kPrepWarps][kPrepAhead][kPrepJob][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % LPH, grp = lane / LPH;
     const int pq = (p.q.heads + HPP - 1) / HPP, pk = (p.k.heads + HPP - 1) / HPP, pv = (p.v.heads + HPP - 1) / HPP;
     const int passes = pq + pk + pv, R = p.rotary;
     const int t0 = blockIdx.x * per_block, nt = min(per_block, p.tokens - t0);
-    const int jobs = passes * ((nt + kPrepJob - 1) / kPrepJob), stride = kPrepWarps * gridDim.y;
+    const int groups = (nt + kPrepJob - 1) / kPrepJob, stride = kPrepWarps * gridDim.y;
     const int rot_lanes = R / 8;
     pdl_trigger();
     pdl_wait();
 
-    // What the current job is: heads of `part`, tokens k0 .. k0 + kPrepJob - 1.
-    int part = 0, h = 0, k0 = 0, oa = 0, ob = 0;
-    bool two = false, active = false;
-    const PrepRows *x = &p.q;
-    uint2 ra[kPrepJob], rb[kPrepJob];
-    auto load = [&](int j) {
-        if (j >= jobs) return;
-        const int g = j / passes, pass = j - g * passes;
-        k0 = g * kPrepJob;
-        part = pass < pq ? 0 : (pass < pq + pk ? 1 : 2);
-        x = part == 0 ? &p.q : (part == 1 ? &p.k : &p.v);
-        h = (pass - (part == 0 ? 0 : (part == 1 ? pq : pq + pk))) * HPP + grp;
-        active = h < x->heads;
-        // Values oa .. oa + 3 and ob .. ob + 3 of a head: pair k of the lane is (f[k], f[4 + k]) where `two`, else
-        // (f[2 k], f[2 k + 1]). Lanes past the rotated part share the rest in the same way.
-        two = R > 0 && !p.interleaved && part < 2;
-        oa = two ? (sub < rot_lanes ? 4 * sub : R + 4 * (sub - rot_lanes)) : 8 * sub;
-        ob = two ? (sub < rot_lanes ? R / 2 + 4 * sub : R + (D - R) / 2 + 4 * (sub - rot_lanes)) : 8 * sub + 4;
-        const T *src = static_cast<const T *>(x->in) + (t0 + k0) * x->in_ts + h * x->in_hs;
-#pragma unroll
-        for (int u = 0; u < kPrepJob; ++u, src += x->in_ts) {
-            ra[u] = rb[u] = make_uint2(0u, 0u);
-            if (active && k0 + u < nt) {
-                if (two) {
-                    ra[u] = *reinterpret_cast<const uint2 *>(src + oa);
-                    rb[u] = *reinterpret_cast<const uint2 *>(src + ob);
-                } else {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + oa);
-                    ra[u] = make_uint2(v.x, v.y);
-                    rb[u] = make_uint2(v.z, v.w);
-                }
-            }
-        }
+    // Job (pass, g): the pass's heads of tokens kPrepJob * g ... A warp takes every stride-th, passes first.
+    struct Job {
+        int pass, g;
     };
-    int j = warp + kPrepWarps * blockIdx.y;
-    load(j);
+    auto step = [&](Job &j) {
+        for (j.pass += stride; j.pass >= passes; j.pass -= passes) ++j.g;
+    };
+    Job now = {warp + kPrepWarps * static_cast<int>(blockIdx.y), 0};
+    for (; now.pass >= passes; now.pass -= passes) ++now.g;
+    Job ahead = now;
+    auto part_of = [&](int pass) { return pass < pq ? 0 : (pass < pq + pk ? 1 : 2); };
+    auto rows_of = [&](int part) -> const PrepRows & { return part == 0 ? p.q : (part == 1 ? p.k : p.v); };
+    auto head_of = [&](int pass, int part) { return (pass - (part == 0 ? 0 : (part == 1 ? pq : pq + pk))) * HPP + grp; };
+    auto fetch = [&](int slot) {
+        if (ahead.g < groups) {
+            const int part = part_of(ahead.pass), h = head_of(ahead.pass, part), k0 = ahead.g * kPrepJob;
+            const PrepRows &x = rows_of(part);
+            const T *src = static_cast<const T *>(x.in) + (t0 + k0) * x.in_ts + h * x.in_hs + 8 * sub;
+#pragma unroll
+            for (int u = 0; u < kPrepJob; ++u, src += x.in_ts)
+                if (h < x.heads && k0 + u < nt)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring[warp][slot][u][lane])), "l"(src)
+                                 : "memory");
+            step(ahead);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int a = 0; a < kPrepAhead; ++a) fetch(a);
 
     // ---- places, pages and positions
     if (p.append) {
         for (int k = warp; k < nt; k += kPrepWarps) {
             const int t = t0 + k, b = warp_find(p.batch.cu_tokens, p.batch.batch, t, lane);
-            int page = -2, slot = 0, place = 0;  // -2: padding
-            if (b < p.batch.batch) {
+            int page = -1, slot = 0, place = 0;
+            const bool padding = b >= p.batch.batch;
+            if (!padding) {
                 const int from = __ldg(p.batch.cu_tokens + b), to = __ldg(p.batch.cu_tokens + b + 1);
                 place = __ldg(p.batch.lens + b) - (to - from) + (t - from);
                 const int col = place / p.page;
                 slot = place - col * p.page;
-                page = -1;
                 if (place >= 0 && col < p.batch.table_cols) page = __ldg(p.batch.page_table + b * p.batch.table_stride + col);
                 if (page < 0 || page >= p.cache.num_pages) {
                     page = -1;
@@ -121,9 +124,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) prep_kernel(const __grid_cons
                 }
             }
             if (lane == 0) {
-                tok_page[k] = page;
-                tok_slot[k] = slot;
-                tok_pos[k] = page == -2 || !p.positions ? place : __ldg(p.positions + t);
+                tok_is[k] = padding ? -1 : page >= 0;
+                tok_row[k] = page * p.cache.page_stride + slot * p.cache.slot_stride;
+                tok_pos[k] = padding || !p.positions ? place : __ldg(p.positions + t);
             }
         }
         __syncthreads();
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) prep_kernel(const __grid_cons
             const int k = i / (R / 4);
             int pos = p.append ? tok_pos[k] : __ldg(p.positions + t0 + k);
             if (pos < 0 || pos >= p.positions_n) {
-                if (p.append && tok_page[k] != -2 && i % (R / 4) == 0) atomicOr(p.err, DEV_ERR_PLACE);
+                if (p.append && tok_is[k] >= 0 && i % (R / 4) == 0) atomicOr(p.err, DEV_ERR_PLACE);
                 pos = min(max(pos, 0), p.positions_n - 1);
             }
             angles[i] = __ldg(reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(pos) * R) + i % (R / 4));
@@ -141,93 +144,127 @@ __global__ void __launch_bounds__(kPrepThreads, 3) prep_kernel(const __grid_cons
         __syncthreads();
     }
 
-    for (; j < jobs; j += stride, load(j)) {
-        const bool normed = part < 2 && x->weight, turned = part < 2 && sub < rot_lanes;
-        const bool cached = part > 0 && p.append;
-        float w[8];
-        if (normed) {
-            const T *wt = static_cast<const T *>(x->weight);
-            const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(wt + oa)), wb = __ldg(reinterpret_cast<const uint2 *>(wt + ob));
-            const float2 w0 = unpack2<T>(wa.x), w1 = unpack2<T>(wa.y), w2 = unpack2<T>(wb.x), w3 = unpack2<T>(wb.y);
-            w[0] = w0.x, w[1] = w0.y, w[2] = w1.x, w[3] = w1.y, w[4] = w2.x, w[5] = w2.y, w[6] = w3.x, w[7] = w3.y;
-        }
-        const bool plain = !normed && !(part < 2 && R > 0) && !(cached && p.fp8);  // a copy
-        const float4 *ang = angles + k0 * (R / 4) + sub;
-        T *dst = static_cast<T *>(x->out) + (t0 + k0) * x->out_ts + h * x->out_hs;
+    const float k_inv = p.fp8 ? 1.f / p.cache.k_scale : 1.f, v_inv = p.fp8 ? 1.f / p.cache.v_scale : 1.f;
+    for (int slot = 0; now.g < groups; step(now), slot = (slot + 1) % kPrepAhead) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kPrepAhead - 1) : "memory");
+        __syncwarp();
+        const int part = part_of(now.pass), h = head_of(now.pass, part), k0 = now.g * kPrepJob;
+        const PrepRows &x = rows_of(part);
+        const bool active = h < x.heads, cached = part > 0 && p.append, quant = cached && p.fp8;
+        const T *const weight = part < 2 ? static_cast<const T *>(x.weight) : nullptr;
+        const bool turn = part < 2 && R > 0;
+
+        // Eight values of a head, in 16 or 8 bits, in two pieces of 4 (from oa and ob).
+        auto store = [&](int u, int oa, int ob, uint2 ya, uint2 yb) {
+            const int k = k0 + u;
+            if (!active || k >= nt || (p.append && tok_is[k] < (cached ? 1 : 0))) return;
+            T *to = cached ? static_cast<T *>(part == 1 ? p.cache.k : p.cache.v) + tok_row[k] + h * p.cache.head_stride
+                           : static_cast<T *>(x.out) + (t0 + k) * x.out_ts + h * x.out_hs;
+            if (ob == oa + 4) {
+                *reinterpret_cast<uint4 *>(to + oa) = make_uint4(ya.x, ya.y, yb.x, yb.y);
+            } else {
+                *reinterpret_cast<uint2 *>(to + oa) = ya;
+                *reinterpret_cast<uint2 *>(to + ob) = yb;
+            }
+        };
+        auto store_e4m3 = [&](int u, int oa, int ob, const float2(&f)[4]) {
+            const int k = k0 + u;
+            if (!active || k >= nt || tok_is[k] < 1) return;
+            uint8_t *to = static_cast<uint8_t *>(part == 1 ? p.cache.k : p.cache.v) + tok_row[k] + h * p.cache.head_stride;
+            const float inv = part == 1 ? k_inv : v_inv;
+            const float2 by = make_float2(inv, inv);
+            uint32_t y[4];
 #pragma unroll
-        for (int u = 0; u < kPrepJob; ++u, dst += x->out_ts, ang += R / 4) {
-            if (k0 + u >= nt) break;
-            uint2 ya = ra[u], yb = rb[u];
-            float f[8];
-            if (!plain) {
-                const float2 a0 = unpack2<T>(ya.x), a1 = unpack2<T>(ya.y), b0 = unpack2<T>(yb.x), b1 = unpack2<T>(yb.y);
-                f[0] = a0.x, f[1] = a0.y, f[2] = a1.x, f[3] = a1.y, f[4] = b0.x, f[5] = b0.y, f[6] = b1.x, f[7] = b1.y;
-                if (normed) {
-                    float ss = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const float2 g = __fmul2_rn(f[e], by);
+                y[e] = f32x2_to_e4m3x2(g.x, g.y);
+            }
+            if (ob == oa + 4) {
+                *reinterpret_cast<uint2 *>(to + oa) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+            } else {
+                *reinterpret_cast<uint32_t *>(to + oa) = y[0] | y[1] << 16;
+                *reinterpret_cast<uint32_t *>(to + ob) = y[2] | y[3] << 16;
+            }
+        };
+        // Norm and rotation: f[0], f[1] and f[2], f[3] are the lane's two pieces.
+        auto transform = [&](auto halves, int oa, int ob) {
+            float2 w[4];
+            if (weight) {
+                const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(weight + oa)), wb = __ldg(reinterpret_cast<const uint2 *>(weight + ob));
+                w[0] = unpack2<T>(wa.x), w[1] = unpack2<T>(wa.y), w[2] = unpack2<T>(wb.x), w[3] = unpack2<T>(wb.y);
+            }
+            const float4 *ang = angles + k0 * (R / 4) + sub;
+            const bool turned = turn && sub < rot_lanes;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+            for (int u = 0; u < kPrepJob; ++u) {
+                const T *row = reinterpret_cast<const T *>(ring[warp][slot][u]) + grp * D;
+                const uint2 xa = *reinterpret_cast<const uint2 *>(row + oa), xb = *reinterpret_cast<const uint2 *>(row + ob);
+                float2 f[4] = {unpack2<T>(xa.x), unpack2<T>(xa.y), unpack2<T>(xb.x), unpack2<T>(xb.y)};
+                if (weight) {
+                    float2 s2 = __fmul2_rn(f[0], f[0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(f[e], f[e], s2);
+                    float ss = s2.x + s2.y;
 #pragma unroll
                     for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
                     const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                    const float2 by = make_float2(r, r);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = f[k] * r * w[k];
+                    for (int e = 0; e < 4; ++e) f[e] = __fmul2_rn(__fmul2_rn(f[e], by), w[e]);
                 }
                 if (turned) {
-                    const float4 c = ang[0], s = ang[R / 8];
-                    const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-                    if (two) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float a = f[k], b = f[4 + k];
-                            f[k] = a * cs[k] - b * sn[k];
-                            f[4 + k] = b * cs[k] + a * sn[k];
-                        }
+                    const float4 c = ang[u * (R / 4)], s = ang[u * (R / 4) + R / 8];
+                    if constexpr (decltype(halves)::value) {
+                        const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+                        const float2 s0 = make_float2(s.x, s.y), s1 = make_float2(s.z, s.w);
+                        const float2 n0 = make_float2(-s.x, -s.y), n1 = make_float2(-s.z, -s.w);
+                        const float2 a0 = f[0], a1 = f[1], b0 = f[2], b1 = f[3];
+                        f[0] = __ffma2_rn(a0, c0, __fmul2_rn(b0, n0));
+                        f[1] = __ffma2_rn(a1, c1, __fmul2_rn(b1, n1));
+                        f[2] = __ffma2_rn(b0, c0, __fmul2_rn(a0, s0));
+                        f[3] = __ffma2_rn(b1, c1, __fmul2_rn(a1, s1));
                     } else {
+                        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float a = f[2 * k], b = f[2 * k + 1];
-                            f[2 * k] = a * cs[k] - b * sn[k];
-                            f[2 * k + 1] = b * cs[k] + a * sn[k];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            f[e] = __ffma2_rn(f[e], make_float2(cs[e], cs[e]),
+                                              __fmul2_rn(make_float2(f[e].y, f[e].x), make_float2(-sn[e], sn[e])));
                     }
                 }
-                ya = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
-                yb = make_uint2(pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                if (quant)
+                    store_e4m3(u, oa, ob, f);
+                else
+                    store(u, oa, ob, make_uint2(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y)),
+                          make_uint2(pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y)));
             }
-            if (!active) continue;
-            T *to = dst;
-            if (cached) {
-                const int page = tok_page[k0 + u];
-                if (page < 0) continue;
-                const int64_t row = page * p.cache.page_stride + tok_slot[k0 + u] * p.cache.slot_stride + h * p.cache.head_stride;
-                void *base = part == 1 ? p.cache.k : p.cache.v;
-                if (p.fp8) {
-                    const float scale = part == 1 ? p.cache.k_scale : p.cache.v_scale;
+        };
+        if (turn && !p.interleaved) {
+            // 4 values of each half; lanes past the rotated part share the rest in the same way
+            const int oa = sub < rot_lanes ? 4 * sub : R + 4 * (sub - rot_lanes);
+            transform(std::true_type(), oa, oa + (sub < rot_lanes ? R / 2 : (D - R) / 2));
+        } else if (weight || turn) {
+            transform(std::false_type(), 8 * sub, 8 * sub + 4);
+        } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], scale);
-                    uint8_t *c = static_cast<uint8_t *>(base) + row;
-                    *reinterpret_cast<uint32_t *>(c + oa) = f32x2_to_e4m3x2(f[0], f[1]) | f32x2_to_e4m3x2(f[2], f[3]) << 16;
-                    *reinterpret_cast<uint32_t *>(c + ob) = f32x2_to_e4m3x2(f[4], f[5]) | f32x2_to_e4m3x2(f[6], f[7]) << 16;
-                    continue;
+            for (int u = 0; u < kPrepJob; ++u) {
+                const uint4 v = ring[warp][slot][u][lane];
+                if (quant) {
+                    const float2 f[4] = {unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w)};
+                    store_e4m3(u, 8 * sub, 8 * sub + 4, f);
+                } else {
+                    store(u, 8 * sub, 8 * sub + 4, make_uint2(v.x, v.y), make_uint2(v.z, v.w));
                 }
-                to = static_cast<T *>(base) + row;
-            } else if (p.append && tok_page[k0 + u] == -2) {
-                continue;  // padding
-            }
-            if (two) {
-                *reinterpret_cast<uint2 *>(to + oa) = ya;
-                *reinterpret_cast<uint2 *>(to + ob) = yb;
-            } else {
-                *reinterpret_cast<uint4 *>(to + oa) = make_uint4(ya.x, ya.y, yb.x, yb.y);
             }
         }
+        __syncwarp();
+        fetch(slot);
     }
 }
 
 template <int D, typename T>
 cudaError_t go(const PrepParams &p, cudaStream_t s)
 {
-    // As many tokens a block as fill every SM's three blocks once, up to kPrepTokens (a large batch then shares
+    // As many tokens a block as fill every SM's kPrepBlocks blocks once, up to prep_tokens() (a large batch then shares
     // place and angle reads between a block's warps); a small batch has one token a block, and where blocks are
     // left its jobs are spread over several of them.
     constexpr int HPP = 32 / (D / 8);
@@ -235,8 +272,8 @@ cudaError_t go(const PrepParams &p, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int slots = 3 * sms, per = (p.tokens + slots - 1) / slots;
-    const int per_block = per < kPrepTokens ? per : kPrepTokens, blocks = (p.tokens + per_block - 1) / per_block;
+    const int slots = kPrepBlocks * sms, per = (p.tokens + slots - 1) / slots;
+    const int per_block = per < prep_tokens<D>() ? per : prep_tokens<D>(), blocks = (p.tokens + per_block - 1) / per_block;
     const int passes = (p.q.heads + HPP - 1) / HPP + (p.k.heads + HPP - 1) / HPP + (p.v.heads + HPP - 1) / HPP;
     const int jobs = passes * ((per_block + kPrepJob - 1) / kPrepJob);
     int y = slots / blocks;
