@@ -102,10 +102,11 @@ dflash_status host_make_tmap(CUtensorMap *tm, const void *ptr, int64_t rows, int
     return make_tmap(tm, ptr, rows, cols, box_rows);
 }
 
-// 16-bit values [pages, slots of a page, heads, head_dim] (strides in values,
-// head_dim contiguous) as the 4D map (value, slot, head, page), boxes of 64
-// values x box_rows slots, 128B swizzle.
-dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, bool bf16, int head_dim, int slots, int heads,
+// Values [pages, slots of a page, heads, head_dim] (strides in values,
+// head_dim contiguous) as the 4D map (value, slot, head, page). 16-bit values:
+// boxes of 64 values x box_rows slots, 128B swizzle; 8-bit ones: boxes of
+// whole rows x box_rows slots as they are stored.
+dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, int bytes, int head_dim, int slots, int heads,
                                    int64_t pages, int64_t slot_stride, int64_t head_stride, int64_t page_stride,
                                    int box_rows)
 {
@@ -116,13 +117,14 @@ dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, bool bf16, 
     if (pages == 1) page_stride = head_dim;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(slots), static_cast<cuuint64_t>(heads),
                           static_cast<cuuint64_t>(pages)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2,
-                             static_cast<cuuint64_t>(page_stride) * 2};
-    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot_stride) * bytes, static_cast<cuuint64_t>(head_stride) * bytes,
+                             static_cast<cuuint64_t>(page_stride) * bytes};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(bytes == 2 ? 64 : head_dim), static_cast<cuuint32_t>(box_rows), 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = fn(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+    CUresult r = fn(tm, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                     const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a cache of %lld pages", static_cast<int>(r),
                     static_cast<long long>(pages));

@@ -9,7 +9,7 @@
 
 namespace dfl {
 dflash_status host_fail(dflash_status st, const char *msg);
-dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, bool bf16, int head_dim, int slots, int heads,
+dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, int bytes, int head_dim, int slots, int heads,
                                    int64_t pages, int64_t slot_stride, int64_t head_stride, int64_t page_stride,
                                    int box_rows);
 }
@@ -292,19 +292,18 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     const int64_t most_rows = static_cast<int64_t>(batch->max_tokens) * p.group;
     cudaError_t e;
     int rows, grid;
-    if (most_rows > DFL_TILE_MIN_ROWS && !fp8) {
+    if (most_rows > DFL_TILE_MIN_ROWS) {
         CUtensorMap tm_k, tm_v;
-        const int box = dfl::tile_box_rows(p.page);
-        const bool bf16 = h->cfg.dtype == DFLASH_BF16;
-        dflash_status st2 = dfl::host_make_tmap_pages(&tm_k, p.k, bf16, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
+        const int box = dfl::tile_box_rows(p.page), bytes = fp8 ? 1 : 2;
+        dflash_status st2 = dfl::host_make_tmap_pages(&tm_k, p.k, bytes, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
                                                       p.slot_stride, p.head_stride, p.page_stride, box);
         if (st2 == DFLASH_OK)
-            st2 = dfl::host_make_tmap_pages(&tm_v, p.v, bf16, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
+            st2 = dfl::host_make_tmap_pages(&tm_v, p.v, bytes, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
                                             p.slot_stride, p.head_stride, p.page_stride, box);
         if (st2 != DFLASH_OK) return st2;
         rows = dfl::kTileRows;
         grid = h->num_sms;
-        e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, grid, s);
+        e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, fp8, grid, s);
     } else {
         rows = most_rows <= 16 ? 16 : 32;
         grid = (rows == 16 ? 3 : 2) * h->num_sms;

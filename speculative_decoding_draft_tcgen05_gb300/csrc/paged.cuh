@@ -24,6 +24,14 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+// Two e4m3 values in the low 16 bits -> two fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t x)
+{
+    uint32_t y;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>

@@ -101,7 +101,7 @@ cudaError_t prepare_attend_tile(int smem_optin);
 int tile_box_rows(int page);
 // tm_k, tm_v: host_make_tmap_pages() with boxes of tile_box_rows() slots.
 cudaError_t launch_attend_tile(const AttendParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int head_dim,
-                               int dtype, int grid, cudaStream_t s);
+                               int dtype, int fp8, int grid, cudaStream_t s);
 // Joins the items split over many CTAs (rows per item, `entries` CTAs of the
 // attention launch); by_value: parts laid out [value / 4][row][4] instead of [row][value].
 cudaError_t launch_attend_merge(const AttendParams &p, int head_dim, int dtype, int rows, int entries, bool by_value,

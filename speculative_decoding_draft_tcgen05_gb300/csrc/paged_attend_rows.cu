@@ -73,14 +73,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values in the low 16 bits -> two fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t x)
-{
-    uint32_t y;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}\n" : "=r"(y) : "r"(x));
-    return y;
-}
-
 // Shapes of one variant. CH: 16-byte chunks of a key's row; a stage of a
 // warp's ring holds 16 keys and their values.
 template <int D, int MT, bool FP8>

@@ -12,9 +12,11 @@ namespace {
 // the matrix products, warps 9-11 bring keys and values to shared memory.
 constexpr int kTileThreads = 384;
 constexpr int kLoadWarps = 3;
-// Registers: 168 a thread at launch; the streams take 208, the rest keep 88
-// (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int kStreamRegs = 208, kOtherRegs = 88;
+// Registers: 168 a thread at launch; the streams take 208 and the rest keep
+// 88, or 200 and 104 where the load warps convert (256 * 208 + 128 * 88 =
+// 256 * 200 + 128 * 104 = 384 * 168).
+constexpr int stream_regs(bool fp8) { return fp8 ? 200 : 208; }
+constexpr int other_regs(bool fp8) { return fp8 ? 104 : 88; }
 
 constexpr uint32_t kTmemCols = 512;
 #ifndef DFL_TILE_COST
@@ -22,19 +24,22 @@ constexpr uint32_t kTmemCols = 512;
 #endif
 constexpr int kTileCost = DFL_TILE_COST, kTileLeast = 1;
 
-template <int D>
+template <int D, bool FP8>
 struct TileShape {
     static constexpr int BOXES = D / 64;                // 64 values (128 bytes) of 128 rows each
     static constexpr uint32_t BOX = 128 * 128;          // bytes
     static constexpr uint32_t TILE = BOXES * BOX;       // 128 rows of queries, keys or values
-    static constexpr int STAGES = D == 128 ? 5 : 10;    // tiles of keys or values in flight
-    static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr int STAGES = (FP8 ? 3 : 5) * (D == 128 ? 1 : 2);  // tiles of keys or values in flight
+    static constexpr int RAWS = FP8 ? 4 : 0;            // and, of an 8-bit cache, tiles as they are stored
+    static constexpr uint32_t RAW = 128 * D;
+    static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + RAWS * RAW + 1024;
     static_assert(SMEM + 2048 <= 227 * 1024, "with the static shared memory, what a block can have");
     static constexpr uint32_t O_COL = 256;              // TMEM: scores 0-127 | 128-255, results from 256
 };
 
 struct TileBars {
     uint64_t full[10], empty[10];  // ring of tiles
+    uint64_t raw_full[4], raw_empty[4];  // ring of 8-bit tiles
     uint64_t q_full[2];            // a stream's queries are in shared memory
     uint64_t q_empty;              // the piece is done with the queries' place
     uint64_t s_full[2];            // its scores are in TMEM
@@ -246,22 +251,24 @@ __device__ __forceinline__ int stream_steps(int n, bool alt, int i)
 // ---------------------------------------------------------------------------
 struct TileParams {
     AttendParams a;
-    CUtensorMap tm_k, tm_v;  // [pages][heads][slots][values], boxes of 64 values x box_rows slots
+    CUtensorMap tm_k, tm_v;  // [pages][heads][slots][values], boxes of box_rows slots
     int box_rows;
 };
 
 namespace {
 
-template <int D, typename T>
+template <int D, typename T, bool FP8>
 __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams tp)
 {
-    using SH = TileShape<D>;
+    using SH = TileShape<D, FP8>;
+    using CT = typename std::conditional<FP8, __half, T>::type;  // type of the matrix products
     constexpr int R = kTileRows, U = kTileUnit, S = SH::STAGES;
     constexpr PagedCut cut = {R, U, kTileCost};
     const AttendParams &p = tp.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileBars bars;
     __shared__ float2 x_ml[128];
+    __shared__ uint8_t q_exp[FP8 ? 256 : 1];  // a query row was scaled by 2^(108 - this)
     uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t q_s = smem_u32(smem), ring = q_s + 2 * SH::TILE;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -270,6 +277,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         for (int i = 0; i < S; ++i) {
             mbar_init(smem_u32(&bars.full[i]), kLoadWarps);
             mbar_init(smem_u32(&bars.empty[i]), 1);
+        }
+        for (int i = 0; i < SH::RAWS; ++i) {
+            mbar_init(smem_u32(&bars.raw_full[i]), kLoadWarps);
+            mbar_init(smem_u32(&bars.raw_empty[i]), kLoadWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.q_full[i]), kLoadWarps);
@@ -300,13 +311,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
 
     if (warp < 8) {
         // ------------------------------------------------------ softmax streams
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStreamRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(stream_regs(FP8)));
         const int i = warp >> 2, row = tid & 127;
         const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
         const uint32_t s_col = tmem + lane_base + 128u * i, o_col = tmem + lane_base + SH::O_COL + D * i;
         uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
         int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
-        const float factor = p.scale_log2;
 
         // This thread's row of a piece.
         struct Row {
@@ -336,12 +346,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         while (more) {
             const int least_upto = __reduce_min_sync(0xFFFFFFFFu, c.real ? c.upto : 0x7FFFFFFF);
             const int most_after = __reduce_max_sync(0xFFFFFFFFu, c.real ? c.after : -1);
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, factor = p.scale_log2;
             for (int t = 0; t < c.steps; ++t) {
                 const int key0 = c.key0 + (c.alt ? 2 * t + i : t) * U;
                 if (!(ok = warp_wait(&bars.s_full[i], s_phase, ab))) break;
                 s_phase ^= 1;
                 tc_fence_after_sync();
+                if (FP8 && t == 0) factor *= __uint_as_float((19u + q_exp[c.r]) << 23);
                 uint32_t sr[128];
                 tmem_load128(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         sum[k & 1] = __fadd2_rn(sum[k & 1], x);
-                        w[k] = pack2<T>(x.x, x.y);
+                        w[k] = pack2<CT>(x.x, x.y);
                     }
                     tmem_store32(s_col + 32 * h, w);
                 }
@@ -571,12 +582,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             p.merge[2 * blockIdx.x + 1] = merge1;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(FP8)));
         if (warp == 8) {
             // -------------------------------------------------- matrix products
             // (the whole warp runs this role, one lane issues)
             const uint32_t who = elect_one();
-            constexpr uint32_t id_s = idesc_16<T>(128, 128, false), id_o = idesc_16<T>(128, D, true);
+            constexpr uint32_t id_s = idesc_16<CT>(128, 128, false), id_o = idesc_16<CT>(128, D, true);
             // a descriptor's low bits are the address in units of 16 bytes: stepping it is an addition
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_mn(ring, SH::BOX);
@@ -648,108 +659,191 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             // -------------------------------------------------- keys and values
             const int lw = warp - 9, ltid = tid - 9 * 32;
             const int br = tp.box_rows, groups = U / br;  // row groups of a tile: 1, 2, 4 or 8
-            uint32_t seq = 0, last_tma = 0, q_phase = 1;
+            uint32_t seq = 0, last_tma = 0, q_phase = 1;  // (last_tma: number of the tile)
             bool ok = true, any_tma = false;
             // The piece's queries, once the one before is done with their place; rows past the item's are zero.
             auto load_q = [&](const PagedPiece &pc) {
                 if (!(ok = warp_wait(&bars.q_empty, q_phase, ab))) return;
                 q_phase ^= 1;
                 const int r0 = pc.rt * R, rows = min(R, pc.s.n * p.group - r0);
+                constexpr int kQPieces = (128 * (D / 8) + 32 * kLoadWarps - 1) / (32 * kLoadWarps) * (32 * kLoadWarps);
                 constexpr int CH = D / 8;  // 16-byte pieces of a row
                 for (int i = 0; i < (rows <= 128 ? 1 : 2); ++i) {
-#pragma unroll 8
-                    for (int x = ltid; x < 128 * CH; x += 32 * kLoadWarps) {
+#pragma unroll(FP8 ? 1 : 8)
+                    for (int x = ltid; x < kQPieces; x += 32 * kLoadWarps) {
                         const int row = x / CH, c = x % CH, r = 128 * i + row;
                         const int t = p.by_group.div(r0 + r), g = r0 + r - t * p.group;
-                        const int64_t o = r < rows ? (pc.s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c : 0;
-                        const int bytes = r < rows ? 16 : 0;  // 0: zeros
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         q_s + i * SH::TILE + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16)),
-                                     "l"(static_cast<const T *>(p.q) + o), "r"(bytes)
-                                     : "memory");
+                        const bool in = r < rows && row < 128;
+                        const T *src = static_cast<const T *>(p.q) +
+                                       (in ? (pc.s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c : 0);
+                        const uint32_t to = i * SH::TILE + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16);
+                        if constexpr (FP8) {
+                            // fp16 with the row's largest value in [2^8, 2^9), by a power of two: queries of any
+                            // size fit (the lanes of a row are neighbours)
+                            const uint4 v = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+                            const float2 f[4] = {unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w)};
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+#pragma unroll
+                            for (int o = CH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal
+                            e = max(-100, min(100, e));
+                            const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+                            if (row < 128) {
+                                *reinterpret_cast<uint4 *>(smem + to) =
+                                    make_uint4(pack2<CT>(f[0].x * up, f[0].y * up), pack2<CT>(f[1].x * up, f[1].y * up),
+                                               pack2<CT>(f[2].x * up, f[2].y * up), pack2<CT>(f[3].x * up, f[3].y * up));
+                                if (c == 0) q_exp[r] = static_cast<uint8_t>(e + 100);
+                            }
+                        } else if (row < 128) {
+                            const int bytes = in ? 16 : 0;  // 0: zeros
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_s + to), "l"(src), "r"(bytes)
+                                         : "memory");
+                        }
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_async_proxy();
                     warp_arrive(&bars.q_full[i], lane);
                 }
             };
-            while (ok && walk.more) {
-                const PagedPiece &pc = walk.pc;
-                const int n = pc.e - pc.a, len = pc.s.len, lo = pc.it.lo, hi = pc.it.hi;
-                const int from = p.by_page.div(lo) * p.page;  // the first page that is used
-                const int32_t *const pages = p.table + pc.b * p.table_stride;
-                // lane g: the page of row group g of a tile (-1: no key of it is used)
-                auto page_of = [&](int j) {
-                    const int key = (pc.it.u0 + pc.a + j) * U + lane * br;
-                    return lane < groups && key >= from && key < hi ? __ldg(pages + p.by_page.div(key)) : -1;
-                };
-                int ahead = page_of(0);
-                for (int j = 0; j < n && ok; ++j) {
-                    const int key0 = (pc.it.u0 + pc.a + j) * U, key = key0 + lane * br;
-                    int page = ahead;
-                    if (j + 1 < n) ahead = page_of(j + 1);
-                    if (lane < groups && key >= from && key < hi && (page < 0 || page >= p.num_pages)) {
-                        page = -1;
+            // One tile of keys or values of `w`'s piece on its way to `dst` (16-bit: swizzled boxes; 8-bit: rows as
+            // they are stored): boxes by TMA, and by the load warps those that hold places past the sequence's end
+            // or no key in use. Every load warp arrives on `bar`, the first of them with the boxes' bytes.
+            struct Source {
+                PagedWalk w;
+                int j, page, coming;  // tile; lane g: page of its row group g, and of the next tile's
+            };
+            // lane g: the page of row group g of tile j (kUnused: no key of it is used)
+            constexpr int kUnused = -0x7FFFFFFF - 1;
+            auto page_of = [&](const PagedWalk &w, int j) {
+                const int key = (w.pc.it.u0 + w.pc.a + j) * U + lane * br;
+                return lane < groups && key >= p.by_page.div(w.pc.it.lo) * p.page && key < w.pc.it.hi
+                           ? __ldg(p.table + w.pc.b * p.table_stride + p.by_page.div(key)) : kUnused;
+            };
+            auto bring = [&](Source &f, int kv, uint32_t dst, uint64_t *full, uint32_t number) {
+                const uint32_t bar = smem_u32(full);
+                const PagedPiece &pc = f.w.pc;
+                const int key0 = (pc.it.u0 + pc.a + f.j) * U, key = key0 + lane * br, len = pc.s.len;
+                if (kv == 0) {  // the values' pages are the keys'
+                    f.page = f.coming;
+                    if (f.j + 1 < pc.e - pc.a) f.coming = page_of(f.w, f.j + 1);
+                    if (f.page != kUnused && (f.page < 0 || f.page >= p.num_pages)) {
+                        f.page = -1;
                         atomicOr(p.err, DEV_ERR_PLACE);
                     }
-                    const int slot = key - p.by_page.div(key) * p.page;
-                    // groups that TMA brings whole, and those that hold places past the end (or no key in use)
-                    const unsigned tma = __ballot_sync(0xFFFFFFFFu, page >= 0 && key + br <= len);
-                    const int soft = groups - __popc(tma);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
-                        const uint32_t st = seq % S, bar = smem_u32(&bars.full[st]);
-                        if (!(ok = warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab))) break;
-                        const uint32_t dst = ring + st * SH::TILE;
-                        if (lw == 0 && tma) {
-                            if (lane == 0) mbar_expect_tx(bar, __popc(tma) * br * SH::BOXES * 128u);
-                            __syncwarp();
-                            const int g = lane & 7, box = lane >> 3;
-                            const int pg = __shfl_sync(0xFFFFFFFFu, page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
-                            if (box < SH::BOXES && (tma >> g & 1))
-                                tma_load_4d(dst + box * SH::BOX + g * br * 128, kv ? &tp.tm_v : &tp.tm_k, 64 * box, sl, pc.kvh,
-                                            pg, bar);
-                            any_tma = true;
-                            last_tma = seq;
-                        }
-                        if (soft) {
-                            const uint8_t *base = static_cast<const uint8_t *>(kv ? p.v : p.k);
-                            constexpr int CH = D / 8;  // 16-byte pieces of a row
-                            for (int g = 0; g < groups; ++g) {
-                                if (tma >> g & 1) continue;
-                                const int pg = __shfl_sync(0xFFFFFFFFu, page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
-                                const int64_t at = pg * p.page_stride + sl * p.slot_stride + pc.kvh * p.head_stride;
-#pragma unroll 4
-                                for (int x = ltid; x < br * CH; x += 32 * kLoadWarps) {
-                                    const int row = x / CH, c = x % CH, k = key0 + g * br + row;
-                                    const bool in = pg >= 0 && k < len;
-                                    const int64_t o = in ? at + row * p.slot_stride + 8 * c : 0;
-                                    const int bytes = in ? 16 : 0;  // 0: zeros
-                                    const int rw = g * br + row;
-                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                                     dst + (c >> 3) * SH::BOX + rw * 128 + (((c & 7) ^ (rw & 7)) * 16)),
-                                                 "l"(base + 2 * o), "r"(bytes)
-                                                 : "memory");
-                                }
-                            }
-                            asm volatile("cp.async.wait_all;" ::: "memory");
-                            fence_async_proxy();
-                            __syncwarp();
-                        }
-                        if (lane == 0) mbar_arrive(bar);
-                    }
-                    // (after the first keys and values: those find room in the ring while the piece before ends,
-                    // which the queries have to wait for)
-                    if (ok && j == 0) load_q(pc);
                 }
-                walk.next(p, cut);
+                const int slot = key - p.by_page.div(key) * p.page;
+                const unsigned tma = __ballot_sync(0xFFFFFFFFu, f.page >= 0 && key + br <= len);
+                constexpr int BOXES = FP8 ? 1 : SH::BOXES, ROW = FP8 ? D : 128;  // boxes of a row group; bytes of a box's row
+                if (lw == 0 && tma) {
+                    if (lane == 0) mbar_expect_tx(bar, __popc(tma) * br * BOXES * ROW);
+                    __syncwarp();
+                    const int g = lane & 7, box = lane >> 3;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, f.page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
+                    if (box < BOXES && (tma >> g & 1))
+                        tma_load_4d(dst + box * SH::BOX + g * br * ROW, kv ? &tp.tm_v : &tp.tm_k, 64 * box, sl, pc.kvh, pg, bar);
+                    any_tma = true;
+                    last_tma = number;
+                }
+                if (__popc(tma) < groups) {
+                    const uint8_t *base = static_cast<const uint8_t *>(kv ? p.v : p.k);
+                    constexpr int ES = FP8 ? 1 : 2, CH = D * ES / 16;  // 16-byte pieces of a row
+                    for (int g = 0; g < groups; ++g) {
+                        if (tma >> g & 1) continue;
+                        const int pg = __shfl_sync(0xFFFFFFFFu, f.page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
+                        const int64_t at = pg * p.page_stride + sl * p.slot_stride + pc.kvh * p.head_stride;
+#pragma unroll(FP8 ? 1 : 4)
+                        for (int x = ltid; x < br * CH; x += 32 * kLoadWarps) {
+                            const int row = x / CH, c = x % CH, rw = g * br + row;
+                            const bool in = pg >= 0 && key0 + rw < len;
+                            const int64_t o = in ? (at + row * p.slot_stride) * ES + 16 * c : 0;
+                            const int bytes = in ? 16 : 0;  // 0: zeros
+                            const uint32_t to = FP8 ? rw * D + 16 * c : (c >> 3) * SH::BOX + rw * 128 + (((c & 7) ^ (rw & 7)) * 16);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + to), "l"(base + o), "r"(bytes)
+                                         : "memory");
+                        }
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (!FP8) fence_async_proxy();
+                }
+                warp_arrive(full, lane);
+            };
+
+            if constexpr (!FP8) {
+                Source f = {walk, 0, kUnused, walk.more ? page_of(walk, 0) : kUnused};
+                while (ok && f.w.more) {
+                    const int n = f.w.pc.e - f.w.pc.a;
+                    for (f.j = 0; f.j < n && ok; ++f.j) {
+#pragma unroll 1
+                        for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+                            const uint32_t st = seq % S;
+                            if (!(ok = warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab))) break;
+                            bring(f, kv, ring + st * SH::TILE, &bars.full[st], seq);
+                        }
+                        // (after the first keys and values: those find room in the ring while the piece before ends,
+                        // which the queries have to wait for)
+                        if (ok && f.j == 0) load_q(f.w.pc);
+                    }
+                    if (f.w.next(p, cut)) f.coming = page_of(f.w, 0);
+                }
+            } else {
+                // An 8-bit cache: tiles come as they are stored, up to RAWS of them ahead, and are converted
+                // (exactly) to fp16 in shared memory.
+                const uint32_t raw_s = ring + S * SH::TILE;
+                Source f = {walk, 0, kUnused, walk.more ? page_of(walk, 0) : kUnused};
+                int kv = 0;
+                uint32_t put = 0;
+                auto ahead = [&]() {
+                    if (!ok || !f.w.more) return;
+                    const uint32_t rs = put % SH::RAWS;
+                    if (!(ok = warp_wait(&bars.raw_empty[rs], ((put / SH::RAWS) & 1) ^ 1, ab))) return;
+                    bring(f, kv, raw_s + rs * SH::RAW, &bars.raw_full[rs], put);
+                    ++put;
+                    kv ^= 1;
+                    if (kv == 0 && ++f.j == f.w.pc.e - f.w.pc.a) {
+                        f.j = 0;
+                        if (f.w.next(p, cut)) f.coming = page_of(f.w, 0);
+                    }
+                };
+#pragma unroll 1
+                for (int i = 0; i < SH::RAWS - 1; ++i) ahead();
+                // a thread's pieces of a tile: 16 stored values of one row after another, STEP rows apart
+                constexpr int CH = D / 16, STEP = 32 * kLoadWarps / CH;
+                const int row0 = ltid / CH, c = 2 * (ltid % CH);
+                while (ok && walk.more) {
+                    const int tiles = 2 * (walk.pc.e - walk.pc.a);
+                    for (int t = 0; t < tiles && ok; ++t, ++seq) {
+                        ahead();
+                        const uint32_t st = seq % S, rs = seq % SH::RAWS;
+                        ok = ok && warp_wait(&bars.raw_full[rs], (seq / SH::RAWS) & 1, ab) &&
+                             warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab);
+                        if (!ok) break;
+                        const uint8_t *src = smem + (2 + S) * SH::TILE + rs * SH::RAW + 16 * ltid;
+                        uint8_t *dst = smem + (2 + st) * SH::TILE + (c >> 3) * SH::BOX;
+#pragma unroll 4
+                        for (int row = row0; row < 128; row += STEP, src += 16 * 32 * kLoadWarps) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c & 7) ^ (row & 7)) * 16)) =
+                                make_uint4(e4m3x2_to_h2(v.x), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y), e4m3x2_to_h2(v.y >> 16));
+                            *reinterpret_cast<uint4 *>(dst + row * 128 + ((((c & 7) + 1) ^ (row & 7)) * 16)) =
+                                make_uint4(e4m3x2_to_h2(v.z), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w), e4m3x2_to_h2(v.w >> 16));
+                        }
+                        fence_async_proxy();
+                        warp_arrive(&bars.full[st], lane);
+                        if (lane == 0) mbar_arrive(smem_u32(&bars.raw_empty[rs]));
+                        if (t == 1) load_q(walk.pc);
+                    }
+                    walk.next(p, cut);
+                }
             }
-            // On an abort: wait (again with a limit) for the copies in flight. Stages are filled in order, so
-            // those of the last S tiles cover them.
+            // On an abort: wait (again with a limit) for the copies in flight. Stages are filled in order, so the
+            // last ones' cover them.
             if (!ok && any_tma && lane == 0) {
-                const uint32_t first = last_tma >= S - 1 ? last_tma - (S - 1) : 0;
+                constexpr uint32_t N = FP8 ? SH::RAWS : S;
+                const uint32_t first = last_tma >= N - 1 ? last_tma - (N - 1) : 0;
                 for (uint32_t q = first; q <= last_tma; ++q)
-                    mbar_wait(smem_u32(&bars.full[q % S]), (q / S) & 1, ab, false);
+                    mbar_wait(smem_u32(FP8 ? &bars.raw_full[q % N] : &bars.full[q % N]), (q / N) & 1, ab, false);
             }
         }
     }
@@ -762,13 +856,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
 }
 
 template <typename F>
-cudaError_t tile_variant(int head_dim, int dtype, F &&f)
+cudaError_t tile_variant(int head_dim, int dtype, int fp8, F &&f)
 {
-    if (head_dim == 128)
-        return dtype == DFLASH_BF16 ? f(attend_tile_kernel<128, __nv_bfloat16>, TileShape<128>::SMEM)
-                                    : f(attend_tile_kernel<128, __half>, TileShape<128>::SMEM);
-    return dtype == DFLASH_BF16 ? f(attend_tile_kernel<64, __nv_bfloat16>, TileShape<64>::SMEM)
-                                : f(attend_tile_kernel<64, __half>, TileShape<64>::SMEM);
+    using B = __nv_bfloat16;
+    using H = __half;
+#define DFL_TILE(D)                                                                                                  \
+    if (head_dim == D) {                                                                                             \
+        if (fp8)                                                                                                     \
+            return dtype == DFLASH_BF16 ? f(attend_tile_kernel<D, B, true>, TileShape<D, true>::SMEM)                \
+                                        : f(attend_tile_kernel<D, H, true>, TileShape<D, true>::SMEM);               \
+        return dtype == DFLASH_BF16 ? f(attend_tile_kernel<D, B, false>, TileShape<D, false>::SMEM)                  \
+                                    : f(attend_tile_kernel<D, H, false>, TileShape<D, false>::SMEM);                 \
+    }
+    DFL_TILE(128)
+    DFL_TILE(64)
+#undef DFL_TILE
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -776,10 +879,12 @@ cudaError_t tile_variant(int head_dim, int dtype, F &&f)
 cudaError_t prepare_attend_tile(int smem_optin)
 {
     for (int d : {64, 128})
-        for (int dt : {DFLASH_BF16, DFLASH_FP16}) {
-            const cudaError_t e = tile_variant(d, dt, [&](auto kern, size_t) { return set_max_dynamic_smem(kern, smem_optin); });
-            if (e != cudaSuccess) return e;
-        }
+        for (int dt : {DFLASH_BF16, DFLASH_FP16})
+            for (int fp8 : {0, 1}) {
+                const cudaError_t e =
+                    tile_variant(d, dt, fp8, [&](auto kern, size_t) { return set_max_dynamic_smem(kern, smem_optin); });
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
@@ -795,14 +900,14 @@ int tile_box_rows(int page)
 }
 
 cudaError_t launch_attend_tile(const AttendParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int head_dim,
-                               int dtype, int grid, cudaStream_t s)
+                               int dtype, int fp8, int grid, cudaStream_t s)
 {
     TileParams tp;
     tp.a = p;
     tp.tm_k = tm_k;
     tp.tm_v = tm_v;
     tp.box_rows = tile_box_rows(p.page);
-    return tile_variant(head_dim, dtype, [&](auto kern, size_t smem) {
+    return tile_variant(head_dim, dtype, fp8, [&](auto kern, size_t smem) {
         return launch_ex(kern, dim3(grid), dim3(kTileThreads), smem, s, 1, tp);
     });
 }
