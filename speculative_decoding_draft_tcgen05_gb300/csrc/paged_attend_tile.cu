@@ -9,14 +9,15 @@ namespace dfl {
 namespace {
 
 // Warps 0-3 and 4-7 are two softmax streams (a thread per row), warp 8 issues
-// the matrix products, warps 9-11 bring keys and values to shared memory.
-constexpr int kTileThreads = 384;
-constexpr int kLoadWarps = 3;
-// Registers: 168 a thread at launch; the streams take 208 and the rest keep
-// 88, or 200 and 104 where the load warps convert (256 * 208 + 128 * 88 =
-// 256 * 200 + 128 * 104 = 384 * 168).
-constexpr int stream_regs(bool fp8) { return fp8 ? 200 : 208; }
-constexpr int other_regs(bool fp8) { return fp8 ? 104 : 88; }
+// the matrix products, and the others bring keys, values and queries to shared
+// memory: warps 9-11 for a 16-bit cache; warp 9, and warps 10-15 to convert,
+// for an 8-bit one.
+constexpr int tile_threads(bool fp8) { return fp8 ? 512 : 384; }
+constexpr int load_warps(bool fp8) { return fp8 ? 6 : 3; }  // that queries and finished tiles come from
+// Registers: 168 (128) a thread at launch; the streams take 208 (184) and the
+// rest keep 88 (72): 256 * 208 + 128 * 88 = 384 * 168, 256 * 184 + 256 * 72 = 512 * 128.
+constexpr int stream_regs(bool fp8) { return fp8 ? 184 : 208; }
+constexpr int other_regs(bool fp8) { return fp8 ? 72 : 88; }
 
 constexpr uint32_t kTmemCols = 512;
 #ifndef DFL_TILE_COST
@@ -134,7 +135,8 @@ __device__ __forceinline__ void umma_commit_if(uint32_t who, uint64_t *bar)
         : "memory");
 }
 
-#define DFL_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+// (written before the last operand is read)
+#define DFL_R8(r, i) "=&r"(r[i]), "=&r"(r[i + 1]), "=&r"(r[i + 2]), "=&r"(r[i + 3]), "=&r"(r[i + 4]), "=&r"(r[i + 5]), "=&r"(r[i + 6]), "=&r"(r[i + 7])
 #define DFL_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
 
 // 32 consecutive columns of this thread's lane; waits for the load.
@@ -149,23 +151,23 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32])
         : "memory");
 }
 
-// 128 consecutive columns of this thread's lane.
+// 128 consecutive columns of this thread's lane; waits for the loads.
 __device__ __forceinline__ void tmem_load128(uint32_t taddr, uint32_t (&r)[128])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
         "tcgen05.wait::ld.sync.aligned;\n"
         : DFL_R8(r, 0), DFL_R8(r, 8), DFL_R8(r, 16), DFL_R8(r, 24), DFL_R8(r, 32), DFL_R8(r, 40), DFL_R8(r, 48),
           DFL_R8(r, 56), DFL_R8(r, 64), DFL_R8(r, 72), DFL_R8(r, 80), DFL_R8(r, 88), DFL_R8(r, 96), DFL_R8(r, 104),
           DFL_R8(r, 112), DFL_R8(r, 120)
-        : "r"(taddr)
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
         : "memory");
 }
 
@@ -258,11 +260,11 @@ struct TileParams {
 namespace {
 
 template <int D, typename T, bool FP8>
-__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams tp)
+__global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const __grid_constant__ TileParams tp)
 {
     using SH = TileShape<D, FP8>;
     using CT = typename std::conditional<FP8, __half, T>::type;  // type of the matrix products
-    constexpr int R = kTileRows, U = kTileUnit, S = SH::STAGES;
+    constexpr int R = kTileRows, U = kTileUnit, S = SH::STAGES, kLoadWarps = load_warps(FP8);
     constexpr PagedCut cut = {R, U, kTileCost};
     const AttendParams &p = tp.a;
     extern __shared__ uint8_t smem_raw[];
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             mbar_init(smem_u32(&bars.empty[i]), 1);
         }
         for (int i = 0; i < SH::RAWS; ++i) {
-            mbar_init(smem_u32(&bars.raw_full[i]), kLoadWarps);
+            mbar_init(smem_u32(&bars.raw_full[i]), 1);
             mbar_init(smem_u32(&bars.raw_empty[i]), kLoadWarps);
         }
         for (int i = 0; i < 2; ++i) {
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
-    const PagedPlan plan = paged_plan<kTileThreads>(p, cut, kTileLeast, reinterpret_cast<int *>(smem));  // holds block barriers
+    const PagedPlan plan = paged_plan<tile_threads(FP8)>(p, cut, kTileLeast, reinterpret_cast<int *>(smem));  // holds block barriers
     tc_fence_after_sync();
     const uint32_t tmem = bars.tmem;
     int *const ab = &bars.abort_flag;
@@ -657,7 +659,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             __syncwarp();
         } else {
             // -------------------------------------------------- keys and values
-            const int lw = warp - 9, ltid = tid - 9 * 32;
+            constexpr int kFirst = FP8 ? 10 : 9;            // of the warps that queries come from
+            const int ltid = tid - 32 * kFirst;             // (negative: warp 9 of an 8-bit cache's)
             const int br = tp.box_rows, groups = U / br;  // row groups of a tile: 1, 2, 4 or 8
             uint32_t seq = 0, last_tma = 0, q_phase = 1;  // (last_tma: number of the tile)
             bool ok = true, any_tma = false;
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 constexpr int kQPieces = (128 * (D / 8) + 32 * kLoadWarps - 1) / (32 * kLoadWarps) * (32 * kLoadWarps);
                 constexpr int CH = D / 8;  // 16-byte pieces of a row
                 for (int i = 0; i < (rows <= 128 ? 1 : 2); ++i) {
-#pragma unroll(FP8 ? 1 : 8)
+#pragma unroll(FP8 ? 4 : 8)
                     for (int x = ltid; x < kQPieces; x += 32 * kLoadWarps) {
                         const int row = x / CH, c = x % CH, r = 128 * i + row;
                         const int t = p.by_group.div(r0 + r), g = r0 + r - t * p.group;
@@ -709,7 +712,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             };
             // One tile of keys or values of `w`'s piece on its way to `dst` (16-bit: swizzled boxes; 8-bit: rows as
             // they are stored): boxes by TMA, and by the load warps those that hold places past the sequence's end
-            // or no key in use. Every load warp arrives on `bar`, the first of them with the boxes' bytes.
+            // or no key in use. Each arrives on `full`, the first of them with the boxes' bytes too.
             struct Source {
                 PagedWalk w;
                 int j, page, coming;  // tile; lane g: page of its row group g, and of the next tile's
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 const int slot = key - p.by_page.div(key) * p.page;
                 const unsigned tma = __ballot_sync(0xFFFFFFFFu, f.page >= 0 && key + br <= len);
                 constexpr int BOXES = FP8 ? 1 : SH::BOXES, ROW = FP8 ? D : 128;  // boxes of a row group; bytes of a box's row
-                if (lw == 0 && tma) {
+                if (warp == 9 && tma) {
                     if (lane == 0) mbar_expect_tx(bar, __popc(tma) * br * BOXES * ROW);
                     __syncwarp();
                     const int g = lane & 7, box = lane >> 3;
@@ -753,8 +756,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                         if (tma >> g & 1) continue;
                         const int pg = __shfl_sync(0xFFFFFFFFu, f.page, g), sl = __shfl_sync(0xFFFFFFFFu, slot, g);
                         const int64_t at = pg * p.page_stride + sl * p.slot_stride + pc.kvh * p.head_stride;
-#pragma unroll(FP8 ? 1 : 4)
-                        for (int x = ltid; x < br * CH; x += 32 * kLoadWarps) {
+#pragma unroll(FP8 ? 2 : 4)
+                        for (int x = FP8 ? lane : ltid; x < br * CH; x += FP8 ? 32 : 32 * kLoadWarps) {
                             const int row = x / CH, c = x % CH, rw = g * br + row;
                             const bool in = pg >= 0 && key0 + rw < len;
                             const int64_t o = in ? (at + row * p.slot_stride) * ES + 16 * c : 0;
@@ -788,53 +791,50 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                     if (f.w.next(p, cut)) f.coming = page_of(f.w, 0);
                 }
             } else {
-                // An 8-bit cache: tiles come as they are stored, up to RAWS of them ahead, and are converted
-                // (exactly) to fp16 in shared memory.
+                // An 8-bit cache: warp 9 brings tiles as they are stored, the others convert them (exactly) to fp16.
                 const uint32_t raw_s = ring + S * SH::TILE;
-                Source f = {walk, 0, kUnused, walk.more ? page_of(walk, 0) : kUnused};
-                int kv = 0;
-                uint32_t put = 0;
-                auto ahead = [&]() {
-                    if (!ok || !f.w.more) return;
-                    const uint32_t rs = put % SH::RAWS;
-                    if (!(ok = warp_wait(&bars.raw_empty[rs], ((put / SH::RAWS) & 1) ^ 1, ab))) return;
-                    bring(f, kv, raw_s + rs * SH::RAW, &bars.raw_full[rs], put);
-                    ++put;
-                    kv ^= 1;
-                    if (kv == 0 && ++f.j == f.w.pc.e - f.w.pc.a) {
-                        f.j = 0;
+                if (warp == 9) {
+                    Source f = {walk, 0, kUnused, walk.more ? page_of(walk, 0) : kUnused};
+                    while (ok && f.w.more) {
+                        const int n = f.w.pc.e - f.w.pc.a;
+                        for (f.j = 0; f.j < n && ok; ++f.j) {
+#pragma unroll 1
+                            for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+                                const uint32_t rs = seq % SH::RAWS;
+                                if (!(ok = warp_wait(&bars.raw_empty[rs], ((seq / SH::RAWS) & 1) ^ 1, ab))) break;
+                                bring(f, kv, raw_s + rs * SH::RAW, &bars.raw_full[rs], seq);
+                            }
+                        }
                         if (f.w.next(p, cut)) f.coming = page_of(f.w, 0);
                     }
-                };
-#pragma unroll 1
-                for (int i = 0; i < SH::RAWS - 1; ++i) ahead();
-                // a thread's pieces of a tile: 16 stored values of one row after another, STEP rows apart
-                constexpr int CH = D / 16, STEP = 32 * kLoadWarps / CH;
-                const int row0 = ltid / CH, c = 2 * (ltid % CH);
-                while (ok && walk.more) {
-                    const int tiles = 2 * (walk.pc.e - walk.pc.a);
-                    for (int t = 0; t < tiles && ok; ++t, ++seq) {
-                        ahead();
-                        const uint32_t st = seq % S, rs = seq % SH::RAWS;
-                        ok = ok && warp_wait(&bars.raw_full[rs], (seq / SH::RAWS) & 1, ab) &&
-                             warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab);
-                        if (!ok) break;
-                        const uint8_t *src = smem + (2 + S) * SH::TILE + rs * SH::RAW + 16 * ltid;
-                        uint8_t *dst = smem + (2 + st) * SH::TILE + (c >> 3) * SH::BOX;
-#pragma unroll 4
-                        for (int row = row0; row < 128; row += STEP, src += 16 * 32 * kLoadWarps) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c & 7) ^ (row & 7)) * 16)) =
-                                make_uint4(e4m3x2_to_h2(v.x), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y), e4m3x2_to_h2(v.y >> 16));
-                            *reinterpret_cast<uint4 *>(dst + row * 128 + ((((c & 7) + 1) ^ (row & 7)) * 16)) =
-                                make_uint4(e4m3x2_to_h2(v.z), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w), e4m3x2_to_h2(v.w >> 16));
+                } else {
+                    // a thread's pieces of a tile: 16 stored values of one row after another, STEP rows apart
+                    constexpr int CH = D / 16, STEP = 32 * kLoadWarps / CH;
+                    const int row0 = ltid / CH, c = 2 * (ltid % CH);
+                    while (ok && walk.more) {
+                        const int tiles = 2 * (walk.pc.e - walk.pc.a);
+                        for (int t = 0; t < tiles && ok; ++t, ++seq) {
+                            const uint32_t st = seq % S, rs = seq % SH::RAWS;
+                            ok = warp_wait(&bars.raw_full[rs], (seq / SH::RAWS) & 1, ab) &&
+                                 warp_wait(&bars.empty[st], ((seq / S) & 1) ^ 1, ab);
+                            if (!ok) break;
+                            const uint8_t *src = smem + (2 + S) * SH::TILE + rs * SH::RAW + 16 * ltid;
+                            uint8_t *dst = smem + (2 + st) * SH::TILE + (c >> 3) * SH::BOX;
+#pragma unroll 3
+                            for (int row = row0; row < 128; row += STEP, src += 16 * 32 * kLoadWarps) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = make_uint4(
+                                    e4m3x2_to_h2(v.x), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y), e4m3x2_to_h2(v.y >> 16));
+                                *reinterpret_cast<uint4 *>(dst + row * 128 + ((((c & 7) + 1) ^ (row & 7)) * 16)) = make_uint4(
+                                    e4m3x2_to_h2(v.z), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w), e4m3x2_to_h2(v.w >> 16));
+                            }
+                            fence_async_proxy();
+                            warp_arrive(&bars.full[st], lane);
+                            if (lane == 0) mbar_arrive(smem_u32(&bars.raw_empty[rs]));
+                            if (t == 1) load_q(walk.pc);
                         }
-                        fence_async_proxy();
-                        warp_arrive(&bars.full[st], lane);
-                        if (lane == 0) mbar_arrive(smem_u32(&bars.raw_empty[rs]));
-                        if (t == 1) load_q(walk.pc);
+                        walk.next(p, cut);
                     }
-                    walk.next(p, cut);
                 }
             }
             // On an abort: wait (again with a limit) for the copies in flight. Stages are filled in order, so the
@@ -908,7 +908,7 @@ cudaError_t launch_attend_tile(const AttendParams &p, const CUtensorMap &tm_k, c
     tp.tm_v = tm_v;
     tp.box_rows = tile_box_rows(p.page);
     return tile_variant(head_dim, dtype, fp8, [&](auto kern, size_t smem) {
-        return launch_ex(kern, dim3(grid), dim3(kTileThreads), smem, s, 1, tp);
+        return launch_ex(kern, dim3(grid), dim3(tile_threads(fp8 != 0)), smem, s, 1, tp);
     });
 }
 
