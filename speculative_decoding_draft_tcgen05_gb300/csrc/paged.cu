@@ -305,8 +305,8 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
         grid = h->num_sms;
         e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, fp8, grid, s);
     } else {
-        rows = most_rows <= 16 ? 16 : 32;
-        grid = (rows == 16 ? 3 : 2) * h->num_sms;
+        rows = most_rows <= 8 ? 8 : (most_rows <= 16 ? 16 : 32);
+        grid = (rows <= 16 ? 3 : 2) * h->num_sms;
         e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, grid, s);
     }
     if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, rows == dfl::kTileRows, 3 * h->num_sms, s);

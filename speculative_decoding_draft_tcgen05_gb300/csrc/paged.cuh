@@ -24,12 +24,12 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// Two e4m3 values in the low 16 bits -> two fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t x)
+// Four e4m3 values -> two pairs of fp16 (exact).
+__device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t y;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}\n" : "=r"(y) : "r"(x));
-    return y;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 template <typename T>

@@ -88,7 +88,7 @@ struct AttendParams {
 };
 
 // Rows of a work item and keys of a work unit of the two kernels.
-constexpr int kRowsUnit = 64;    // few rows: 16 or 32 rows, units of 64 keys
+constexpr int kRowsUnit = 64;    // few rows: 8, 16 or 32 rows, units of 64 keys
 constexpr int kTileRows = 256;   // many rows
 constexpr int kTileUnit = 128;
 constexpr int kTicketParts = 4, kTicketWarps = 8;

@@ -25,6 +25,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit()
 {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -89,6 +94,8 @@ struct RowsShape {
         const int x = CH >= 8 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & (CH - 1)));
         return static_cast<uint32_t>(row * ROW + x * 16);
     }
+    // at(row + n, c) = at(row, c) + n * ROW with this turned in the chunk's bits (n a multiple of 32 / CH > row).
+    __device__ static constexpr uint32_t turn(int n) { return CH >= 8 ? (n & 7) * 16 : 0; }
 };
 
 __device__ __forceinline__ void add8(float (&acc)[8], float f, const float4 &x, const float4 &y)
@@ -115,7 +122,7 @@ constexpr int kRowsPad = 8;  // floats between merge rows
 // One CTA walks its even share of all (sequence, key/value head, row tile)
 // items' keys. Of every unit of 64 keys warp w takes keys 16 w .. 16 w + 15,
 // with its own ring of asynchronous copies, its own running maximum and sum
-// and its own accumulator over all MT * 16 rows: warps meet only at the end of
+// and its own accumulator over all R rows: warps meet only at the end of
 // a piece, where their four results are joined in shared memory. What a CTA
 // does not finish goes to the workspace for the merge kernel.
 //
@@ -125,13 +132,14 @@ constexpr int kRowsPad = 8;  // floats between merge rows
 // 32 op/byte at 32 rows, which mma.sync sustains; the tensor memory path would
 // leave 3/4 or more of its 128-row tiles empty here.
 // ---------------------------------------------------------------------------
-template <int D, int MT, typename QT, bool FP8>
-__global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
+template <int D, int R, typename QT, bool FP8>
+__global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
 {
     using CT = typename std::conditional<FP8, __half, QT>::type;  // type of the matrix products
+    constexpr int MT = (R + 15) / 16, NH = R / 8;  // 16-row products, and halves of them that hold rows
     using SH = RowsShape<D, MT, FP8>;
     constexpr int kRowsRing = rows_ring<MT>();
-    constexpr int R = MT * 16, S = SH::STAGES, CH = SH::CH;
+    constexpr int S = SH::STAGES, CH = SH::CH;
     constexpr int QCH = D * 2 / 16;  // chunks of a query row
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float q_undo[R];  // FP8: what a query row was scaled by, undone
@@ -162,6 +170,11 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
             const uint8_t *kb = static_cast<const uint8_t *>(p.k);
             const uint8_t *vb = static_cast<const uint8_t *>(p.v);
             constexpr int ES = FP8 ? 1 : 2;
+            // a lane copies one 16-byte piece of every RS-th key
+            constexpr int RS = 32 / CH;
+            const int row0 = lane / CH;
+            const uint32_t x0 = SH::at(row0, lane % CH) - row0 * SH::ROW;
+            const int64_t lane_off = row0 * p.slot_stride * ES + 16 * (lane % CH), row_step = RS * p.slot_stride * ES;
             int pages = -1;  // lane l: the page of unit pages_from + l
             int pages_from = -(1 << 30);
             auto issue = [&](int j) {
@@ -181,15 +194,25 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                     const int page = __shfl_sync(0xFFFFFFFFu, pages, j - pages_from);
                     const int key = (first + j) * kRowsUnit + 16 * warp;
                     const int slot = key - p.by_page.div(key) * p.page;
-                    const int64_t at = page * p.page_stride + slot * p.slot_stride + pc.kvh * p.head_stride;
-                    const uint32_t dst = ring + (j % S) * SH::STAGE;
+                    const int64_t at = (page * p.page_stride + slot * p.slot_stride + pc.kvh * p.head_stride) * ES + lane_off;
+                    const uint8_t *ks = kb + at, *vs = vb + at;
+                    const uint32_t dst = ring + (j % S) * SH::STAGE + row0 * SH::ROW;
+                    if (page >= 0 && key >= lo && key + 16 <= hi) {
 #pragma unroll
-                    for (int i = 0; i < 16 * CH / 32; ++i) {
-                        const int row = (32 * i + lane) / CH, c = (32 * i + lane) % CH;
-                        const bool ok = page >= 0 && key + row >= lo && key + row < hi;
-                        const int64_t o = ok ? (at + row * p.slot_stride) * ES + 16 * c : 0;
-                        cp_async16(dst + SH::at(row, c), kb + o, ok);
-                        cp_async16(dst + SH::TILE + SH::at(row, c), vb + o, ok);
+                        for (int i = 0; i < 16 / RS; ++i, ks += row_step, vs += row_step) {
+                            const uint32_t to = dst + i * RS * SH::ROW + (x0 ^ SH::turn(i * RS));
+                            cp_async16(to, ks);
+                            cp_async16(to + SH::TILE, vs);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16 / RS; ++i, ks += row_step, vs += row_step) {
+                            const int k = key + row0 + i * RS;
+                            const bool ok = page >= 0 && k >= lo && k < hi;
+                            const uint32_t to = dst + i * RS * SH::ROW + (x0 ^ SH::turn(i * RS));
+                            cp_async16(to, ok ? ks : kb, ok);
+                            cp_async16(to + SH::TILE, ok ? vs : vb, ok);
+                        }
                     }
                 }
                 cp_async_commit();
@@ -233,11 +256,11 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
             __syncthreads();
 
             // ---- limits of this thread's rows (8 h + lane / 4 of row tile mt): keys in (after, upto]
-            int upto[2 * MT], after[2 * MT];
-            float factor[2 * MT];
+            int upto[NH], after[NH];
+            float factor[NH];
             int most_after = -1, least_upto = 0x7FFFFFFF;
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
+            for (int i = 0; i < NH; ++i) {
                 const int r = 8 * i + (lane >> 2);
                 const int place = base + p.by_group.div(pc.rt * R + r);
                 upto[i] = r < rows ? (p.causal ? min(place, s.len - 1) : s.len - 1) : -1;
@@ -251,10 +274,21 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
             least_upto = __reduce_min_sync(0xFFFFFFFFu, least_upto);
             most_after = __reduce_max_sync(0xFFFFFFFFu, most_after);
 
-            float o[MT][D / 8][4];
-            float m[2 * MT], l[2 * MT];
+            // An 8-bit cache's products take a query row's values 16 c + 4 (lane % 4) .. + 3 (see below); those of up
+            // to 8 rows stay in registers.
+            auto q_pair = [&](int r, int c) {
+                return *reinterpret_cast<const uint2 *>(smem + q_at(r, 2 * c + ((lane & 3) >> 1)) + 8 * (lane & 1));
+            };
+            uint2 qf[FP8 && NH == 1 ? D / 16 : 1];
+            if constexpr (FP8 && NH == 1) {
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
+                for (int c = 0; c < D / 16; ++c) qf[c] = q_pair(lane >> 2, c);
+            }
+
+            float o[MT][D / 8][4];
+            float m[NH], l[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
                 m[i] = -INFINITY;
                 l[i] = 0.f;
             }
@@ -291,20 +325,23 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                         ldsm4(ks + SH::at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c2 + (lane >> 4)), kf);
 #pragma unroll
                         for (int hc = 0; hc < 2; ++hc) {
-                            const uint32_t b00 = e4m3x2_to_h2(kf[2 * hc]), b01 = e4m3x2_to_h2(kf[2 * hc] >> 16);
-                            const uint32_t b10 = e4m3x2_to_h2(kf[2 * hc + 1]), b11 = e4m3x2_to_h2(kf[2 * hc + 1] >> 16);
+                            uint32_t b00, b01, b10, b11;
+                            e4m3x4_to_h2x2(kf[2 * hc], b00, b01);
+                            e4m3x4_to_h2x2(kf[2 * hc + 1], b10, b11);
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
-                                uint32_t a[4];
-                                const int r = 16 * i + (lane >> 2);
-                                // values 16 (2 c2 + hc) + 4 (lane % 4) .. + 3 of rows r and r + 8
-                                const int c = 2 * (2 * c2 + hc) + ((lane & 3) >> 1);
-                                const uint2 x = *reinterpret_cast<const uint2 *>(smem + q_at(r, c) + 8 * (lane & 1));
-                                const uint2 y = *reinterpret_cast<const uint2 *>(smem + q_at(r + 8, c) + 8 * (lane & 1));
-                                a[0] = x.x;
-                                a[1] = y.x;
-                                a[2] = x.y;
-                                a[3] = y.y;
+                                uint32_t a[4] = {0u, 0u, 0u, 0u};
+                                if constexpr (NH == 1) {
+                                    a[0] = qf[2 * c2 + hc].x;
+                                    a[2] = qf[2 * c2 + hc].y;
+                                } else {
+                                    const uint2 x = q_pair(16 * i + (lane >> 2), 2 * c2 + hc);
+                                    const uint2 y = q_pair(16 * i + (lane >> 2) + 8, 2 * c2 + hc);
+                                    a[0] = x.x;
+                                    a[1] = y.x;
+                                    a[2] = x.y;
+                                    a[3] = y.y;
+                                }
                                 mma16816<CT>(sc[i][0], a, b00, b01);
                                 mma16816<CT>(sc[i][1], a, b10, b11);
                             }
@@ -323,9 +360,9 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
 
                 // ---- scale, mask, running maximum
                 const bool whole = key0 > most_after && key0 + 15 <= least_upto;
-                float top[2 * MT];
+                float top[NH];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
+                for (int i = 0; i < NH; ++i) {
                     top[i] = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
@@ -345,14 +382,14 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                 // hardly ever rescaled. The first unit sets it.
                 bool grew = false;
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
+                for (int i = 0; i < NH; ++i) {
                     top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
                     top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
                     grew |= top[i] > m[i] + 8.f;
                 }
                 if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i) {
+                    for (int i = 0; i < NH; ++i) {
                         const float now = fmaxf(m[i], top[i]);
                         const float f = now == -INFINITY ? 1.f : ex2(m[i] - now);
                         m[i] = now;
@@ -367,8 +404,9 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
 
                 // ---- weights, rounded to the values' 16-bit type for the product; the sum takes them unrounded
                 uint32_t pf[MT][4];
+                if constexpr (NH == 1) pf[0][1] = pf[0][3] = 0u;  // (no rows there)
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
+                for (int i = 0; i < NH; ++i) {
                     const float mm = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
@@ -389,9 +427,9 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
                         // chunk make one 8-column tile, the odd ones the next
 #pragma unroll
                         for (int hc = 0; hc < 2; ++hc) {
-                            const uint32_t x = vf[2 * hc], y = vf[2 * hc + 1];
-                            const uint32_t e0 = e4m3x2_to_h2(__byte_perm(x, 0, 0x4420)), e1 = e4m3x2_to_h2(__byte_perm(y, 0, 0x4420));
-                            const uint32_t d0 = e4m3x2_to_h2(__byte_perm(x, 0, 0x4431)), d1 = e4m3x2_to_h2(__byte_perm(y, 0, 0x4431));
+                            uint32_t e0, e1, d0, d1;
+                            e4m3x4_to_h2x2(__byte_perm(vf[2 * hc], 0, 0x3120), e0, d0);
+                            e4m3x4_to_h2x2(__byte_perm(vf[2 * hc + 1], 0, 0x3120), e1, d1);
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
                                 mma16816<CT>(o[i][2 * (c + hc)], pf[i], e0, e1);
@@ -414,7 +452,7 @@ __global__ void __launch_bounds__(kRowsThreads, MT == 1 ? 3 : 2) attend_rows_ker
             constexpr int OS = D + kRowsPad;
             float *mine = reinterpret_cast<float *>(ring_ptr + warp * kRowsRing);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
+            for (int i = 0; i < NH; ++i) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
                 const int r = 8 * i + (lane >> 2);
@@ -617,9 +655,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
     }
 }
 
-template <int D, int MT>
+template <int D, int R>
 constexpr size_t rows_smem()
 {
+    constexpr int MT = (R + 15) / 16;
     return rows_q_bytes<D, MT>() + kRowsWarps * rows_ring<MT>();
 }
 
@@ -629,17 +668,19 @@ cudaError_t rows_variant(int head_dim, int dtype, int fp8, int rows, F &&f)
 {
     using B = __nv_bfloat16;
     using H = __half;
-#define DFL_ROWS(D, MT)                                                                                            \
-    if (head_dim == D && rows == 16 * MT) {                                                                        \
-        if (dtype == DFLASH_BF16 && !fp8) return f(attend_rows_kernel<D, MT, B, false>, rows_smem<D, MT>());       \
-        if (dtype == DFLASH_BF16) return f(attend_rows_kernel<D, MT, B, true>, rows_smem<D, MT>());                \
-        if (!fp8) return f(attend_rows_kernel<D, MT, H, false>, rows_smem<D, MT>());                               \
-        return f(attend_rows_kernel<D, MT, H, true>, rows_smem<D, MT>());                                          \
+#define DFL_ROWS(D, R)                                                                                       \
+    if (head_dim == D && rows == R) {                                                                        \
+        if (dtype == DFLASH_BF16 && !fp8) return f(attend_rows_kernel<D, R, B, false>, rows_smem<D, R>());   \
+        if (dtype == DFLASH_BF16) return f(attend_rows_kernel<D, R, B, true>, rows_smem<D, R>());            \
+        if (!fp8) return f(attend_rows_kernel<D, R, H, false>, rows_smem<D, R>());                           \
+        return f(attend_rows_kernel<D, R, H, true>, rows_smem<D, R>());                                      \
     }
-    DFL_ROWS(128, 1)
-    DFL_ROWS(128, 2)
-    DFL_ROWS(64, 1)
-    DFL_ROWS(64, 2)
+    DFL_ROWS(128, 8)
+    DFL_ROWS(128, 16)
+    DFL_ROWS(128, 32)
+    DFL_ROWS(64, 8)
+    DFL_ROWS(64, 16)
+    DFL_ROWS(64, 32)
 #undef DFL_ROWS
     return cudaErrorInvalidValue;
 }
@@ -651,7 +692,7 @@ cudaError_t prepare_attend_rows(int smem_optin)
     for (int d : {64, 128})
         for (int dt : {DFLASH_BF16, DFLASH_FP16})
             for (int fp8 : {0, 1})
-                for (int rows : {16, 32}) {
+                for (int rows : {8, 16, 32}) {
                     const cudaError_t e = rows_variant(d, dt, fp8, rows, [&](auto kern, size_t) {
                         return set_max_dynamic_smem(kern, smem_optin);
                     });

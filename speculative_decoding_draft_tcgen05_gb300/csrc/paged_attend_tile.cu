@@ -823,10 +823,13 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
 #pragma unroll 3
                             for (int row = row0; row < 128; row += STEP, src += 16 * 32 * kLoadWarps) {
                                 const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = make_uint4(
-                                    e4m3x2_to_h2(v.x), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y), e4m3x2_to_h2(v.y >> 16));
-                                *reinterpret_cast<uint4 *>(dst + row * 128 + ((((c & 7) + 1) ^ (row & 7)) * 16)) = make_uint4(
-                                    e4m3x2_to_h2(v.z), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w), e4m3x2_to_h2(v.w >> 16));
+                                uint4 x, y;
+                                e4m3x4_to_h2x2(v.x, x.x, x.y);
+                                e4m3x4_to_h2x2(v.y, x.z, x.w);
+                                e4m3x4_to_h2x2(v.z, y.x, y.y);
+                                e4m3x4_to_h2x2(v.w, y.z, y.w);
+                                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = x;
+                                *reinterpret_cast<uint4 *>(dst + row * 128 + ((((c & 7) + 1) ^ (row & 7)) * 16)) = y;
                             }
                             fence_async_proxy();
                             warp_arrive(&bars.full[st], lane);
