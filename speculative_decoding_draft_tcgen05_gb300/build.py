@@ -1,7 +1,8 @@
-"""Builds libdflash_select.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libdflash_select.so in-tree with nvcc for sm_103a (GB300), and the
+binding's helper module _paged_call.so with the host compiler.
 
-Every translation unit under csrc/ is compiled in parallel, then linked into
-one shared library next to this file. No GPU is needed to build.
+Every CUDA translation unit under csrc/ is compiled in parallel, then linked
+into one shared library next to this file. No GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdflash_select.so")
+CALL_SRC = os.path.join(CSRC, "paged_call.c")
+CALL = os.path.join(PKG, "_paged_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -45,7 +49,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     srcs = sources()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    if not force and not _stale(LIB, srcs + headers + [os.path.abspath(__file__)]):
+    me = os.path.abspath(__file__)
+    if force or _stale(CALL, [CALL_SRC, me] + headers):
+        tmp = CALL + f".{os.getpid()}.tmp"
+        subprocess.run([os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-I",
+                        sysconfig.get_paths()["include"], "-I", INCLUDE, CALL_SRC, "-o", tmp], check=True)
+        os.replace(tmp, CALL)
+    if not force and not _stale(LIB, srcs + headers + [me]):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()

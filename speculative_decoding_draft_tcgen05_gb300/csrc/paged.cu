@@ -309,7 +309,11 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
         grid = (rows <= 16 ? 3 : 2) * h->num_sms;
         e = dfl::launch_attend_rows(p, h->cfg.head_dim, h->cfg.dtype, fp8, rows, grid, s);
     }
-    if (e == cudaSuccess) e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, rows == dfl::kTileRows, 3 * h->num_sms, s);
+    // An item of few units is joined by the CTAs that share it.
+    const int64_t unit = rows == dfl::kTileRows ? dfl::kTileUnit : dfl::kRowsUnit;
+    const int64_t most_units = (static_cast<int64_t>(p.table_cols) * p.page + unit - 1) / unit;
+    if (e == cudaSuccess && most_units > dfl::kTicketParts)
+        e = dfl::launch_attend_merge(p, h->cfg.head_dim, h->cfg.dtype, rows, grid, rows == dfl::kTileRows, 3 * h->num_sms, s);
     if (e != cudaSuccess) return paged_fail(DFLASH_ERR_CUDA, "attention: a launch failed (error %lld)", e);
     return DFLASH_OK;
 }

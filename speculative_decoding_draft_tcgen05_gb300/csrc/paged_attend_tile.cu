@@ -552,7 +552,10 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                         for (int b = 0; b < 32; ++b) v[b] = 0.f;
 #pragma unroll 1
                         for (int part = 0; part < share.y; ++part) {
-                            const float w = part == 0 ? ml[0].x : part == 1 ? ml[1].x : part == 2 ? ml[2].x : ml[3].x;
+                            float w = 0.f;
+#pragma unroll
+                            for (int b = 0; b < kTicketParts; ++b)
+                                if (b == part) w = ml[b].x;
                             if (part == mine) {
                                 own(k, x);
                             } else {
@@ -671,19 +674,37 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 const int r0 = pc.rt * R, rows = min(R, pc.s.n * p.group - r0);
                 constexpr int kQPieces = (128 * (D / 8) + 32 * kLoadWarps - 1) / (32 * kLoadWarps) * (32 * kLoadWarps);
                 constexpr int CH = D / 8;  // 16-byte pieces of a row
-                for (int i = 0; i < (rows <= 128 ? 1 : 2); ++i) {
+                const int tiles = rows <= 128 ? 1 : 2;
+                auto place = [&](int i, int row, int c) {
+                    return i * SH::TILE + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16);
+                };
+                for (int i = 0; i < tiles; ++i) {
 #pragma unroll(FP8 ? 4 : 8)
-                    for (int x = ltid; x < kQPieces; x += 32 * kLoadWarps) {
+                    for (int x = ltid; x < 128 * CH; x += 32 * kLoadWarps) {
                         const int row = x / CH, c = x % CH, r = 128 * i + row;
                         const int t = p.by_group.div(r0 + r), g = r0 + r - t * p.group;
-                        const bool in = r < rows && row < 128;
                         const T *src = static_cast<const T *>(p.q) +
-                                       (in ? (pc.s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c : 0);
-                        const uint32_t to = i * SH::TILE + (c >> 3) * SH::BOX + row * 128 + (((c & 7) ^ (row & 7)) * 16);
-                        if constexpr (FP8) {
-                            // fp16 with the row's largest value in [2^8, 2^9), by a power of two: queries of any
-                            // size fit (the lanes of a row are neighbours)
-                            const uint4 v = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+                                       (r < rows ? (pc.s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c : 0);
+                        const int bytes = r < rows ? 16 : 0;  // 0: zeros
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_s + place(i, row, c)), "l"(src), "r"(bytes)
+                                     : "memory");
+                    }
+                    if constexpr (!FP8) {
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_async_proxy();
+                        warp_arrive(&bars.q_full[i], lane);
+                    }
+                }
+                if constexpr (FP8) {
+                    // In their place, by the thread that copied them: to fp16 with the row's largest value in
+                    // [2^8, 2^9), by a power of two, so that queries of any size fit (a row's lanes are neighbours).
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    for (int i = 0; i < tiles; ++i) {
+#pragma unroll 2
+                        for (int x = ltid; x < kQPieces; x += 32 * kLoadWarps) {
+                            const int row = x / CH, c = x % CH;
+                            uint4 *const at = reinterpret_cast<uint4 *>(smem + place(i, min(row, 127), c));
+                            const uint4 v = *at;
                             const float2 f[4] = {unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w)};
                             float top = 0.f;
 #pragma unroll
@@ -694,20 +715,14 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                             e = max(-100, min(100, e));
                             const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
                             if (row < 128) {
-                                *reinterpret_cast<uint4 *>(smem + to) =
-                                    make_uint4(pack2<CT>(f[0].x * up, f[0].y * up), pack2<CT>(f[1].x * up, f[1].y * up),
-                                               pack2<CT>(f[2].x * up, f[2].y * up), pack2<CT>(f[3].x * up, f[3].y * up));
-                                if (c == 0) q_exp[r] = static_cast<uint8_t>(e + 100);
+                                *at = make_uint4(pack2<CT>(f[0].x * up, f[0].y * up), pack2<CT>(f[1].x * up, f[1].y * up),
+                                                 pack2<CT>(f[2].x * up, f[2].y * up), pack2<CT>(f[3].x * up, f[3].y * up));
+                                if (c == 0) q_exp[128 * i + row] = static_cast<uint8_t>(e + 100);
                             }
-                        } else if (row < 128) {
-                            const int bytes = in ? 16 : 0;  // 0: zeros
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_s + to), "l"(src), "r"(bytes)
-                                         : "memory");
                         }
+                        fence_async_proxy();
+                        warp_arrive(&bars.q_full[i], lane);
                     }
-                    if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_async_proxy();
-                    warp_arrive(&bars.q_full[i], lane);
                 }
             };
             // One tile of keys or values of `w`'s piece on its way to `dst` (16-bit: swizzled boxes; 8-bit: rows as

@@ -43,17 +43,12 @@ class dflash_qk_transform(ctypes.Structure):
 
 
 def declare(L):
-    """Argument and result types of the entry points."""
-    P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    rows = [P, i64, i64]
-    L.dflash_qk_norm_rope.argtypes = rows * 4 + [i32, i32, i32, i32, i32, P, P, P]
+    """Argument and result types of the entry points (those of a step are called through _paged_call)."""
+    P = ctypes.c_void_p
     L.dflash_paged_init.argtypes = [ctypes.POINTER(dflash_paged_config), P, ctypes.POINTER(P)]
-    L.dflash_paged_append.argtypes = [P, P, P] + rows * 2 + [P, P] + rows * 2 + [P]
-    L.dflash_paged_attend.argtypes = [P, P, P] + rows * 2 + [P, i32, i32, f32, P]
     L.dflash_paged_sync_status.argtypes = [P, P]
     L.dflash_paged_destroy.argtypes = [P]
-    for f in ("dflash_qk_norm_rope", "dflash_paged_init", "dflash_paged_append", "dflash_paged_attend",
-              "dflash_paged_sync_status", "dflash_paged_destroy"):
+    for f in ("dflash_paged_init", "dflash_paged_sync_status", "dflash_paged_destroy"):
         getattr(L, f).restype = ctypes.c_int
 
 
@@ -75,41 +70,27 @@ def _dtypes():
     return {t.bfloat16: DFLASH_BF16, t.float16: DFLASH_FP16, t.float8_e4m3fn: DFLASH_E4M3}
 
 
-@functools.lru_cache(maxsize=None)
-def _raw_stream():
-    """Handle of a device's current stream (device index -> integer)."""
+_calls = None
+
+
+def _load_calls():
+    """The helper module that marshals a step's calls (raises if it has not been built)."""
+    global _calls
+    L = _binding()[0]
+    try:
+        from . import _paged_call
+    except ImportError as e:
+        raise RuntimeError("_paged_call.so is missing: build it first (python -m "
+                           "speculative_decoding_draft_tcgen05_gb300.build)") from e
     t = _torch()
-    raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
-    return raw if raw is not None else (lambda index: t.cuda.current_stream(index).cuda_stream)
-
-
-def _stream_of(t, stream):
-    if stream is None:
-        return _raw_stream()(t.device.index)
-    return _binding()[2](stream)
-
-
-def _rows(t, shape, dtype, name):
-    """(address, token stride, head stride) of rows [tokens, heads, head_dim] with a contiguous last dimension."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    a, b, c = t.stride()
-    if c != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    # a dimension of one row may carry any stride
-    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
-
-
-def _positions(t, tokens):
-    if t.dtype is not _torch().int32:
-        raise TypeError(f"positions must be torch.int32, got {t.dtype}")
-    if t.shape != (tokens,) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"positions must be a contiguous CUDA tensor [{tokens}]")
-    return t.data_ptr()
+    raw = getattr(t._C, "_cuda_getCurrentRawStream", None)  # device index -> handle of its current stream
+    if raw is None:
+        raw = lambda index: t.cuda.current_stream(index).cuda_stream  # noqa: E731
+    at = [ctypes.cast(getattr(L, f), ctypes.c_void_p).value
+          for f in ("dflash_qk_norm_rope", "dflash_paged_append", "dflash_paged_attend")]
+    _paged_call.setup(*at, raw, t.int32, t.float32, t.bfloat16, t.float16)
+    _calls = _paged_call
+    return _calls
 
 
 def _int32(t, shape, name):
@@ -151,13 +132,8 @@ class QkTransform:
             rotary_dim=rotary_dim, interleaved=int(bool(interleaved)),
             q_weight=None if q_weight is None else q_weight.data_ptr(),
             k_weight=None if k_weight is None else k_weight.data_ptr(), eps=eps)
-        self.ref = ctypes.addressof(self.c)
-        self.weight_dtype = self.weights[0].dtype if self.weights else None
-        self.weight_size = self.weights[0].shape[0] if self.weights else None
-
-    def check(self, dtype, head_dim):
-        if self.weight_dtype is not None and (self.weight_dtype is not dtype or self.weight_size != head_dim):
-            raise TypeError(f"norm weights must be {dtype} [{head_dim}], got {self.weight_dtype} [{self.weight_size}]")
+        w = self.weights[0] if self.weights else None
+        self.spec = (ctypes.addressof(self.c), None if w is None else w.dtype, 0 if w is None else w.shape[0])
 
 
 class PagedCache:
@@ -175,13 +151,11 @@ class PagedCache:
         if not (k.is_cuda and v.is_cuda):
             raise ValueError("k and v must be CUDA tensors")
         self.k, self.v = k, v
-        self.dtype = k.dtype
-        self.shape = tuple(k.shape[1:])
         page, slot, head = k.stride()[:3]
         self.c = dflash_paged_cache(k=k.data_ptr(), v=v.data_ptr(), num_pages=k.shape[0], page_stride=page,
                                     slot_stride=slot, head_stride=head if k.shape[2] > 1 else 0, k_scale=k_scale,
                                     v_scale=v_scale)
-        self.ref = ctypes.addressof(self.c)
+        self.spec = (ctypes.addressof(self.c), k.dtype, tuple(k.shape[1:]))
 
 
 class PagedBatch:
@@ -197,37 +171,19 @@ class PagedBatch:
                                     page_table=_int32(page_table, (batch, None), "page_table"),
                                     table_stride=page_table.stride(0), table_cols=page_table.shape[1], batch=batch,
                                     tokens=0, max_tokens=max_tokens)
-        self.ref = ctypes.addressof(self.c)
-
-
-_NONE = (None, 0, 0)
+        self.spec = (ctypes.addressof(self.c),)
 
 
 def dflash_qk_norm_rope(q, k, q_out, k_out, transform, positions=None, stream=None):
     """q_out, k_out [tokens, heads, head_dim] = the transform of q and k (either pair may be None; in place is
     allowed); positions [tokens] int32."""
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k must be given")
-    dt = x.dtype
-    qs = ks = None
-    a = b = c = d = _NONE
-    if q is not None:
-        qs = q.shape
-        a, b = _rows(q, qs, dt, "q"), _rows(q_out, qs, dt, "q_out")
-    if k is not None:
-        ks = k.shape
-        c, d = _rows(k, ks, dt, "k"), _rows(k_out, ks, dt, "k_out")
-        if qs is not None and (ks[0] != qs[0] or ks[2] != qs[2]):
-            raise ValueError(f"q and k must have the same tokens and head_dim, got {list(qs)} and {list(ks)}")
-    tokens, _, head_dim = x.shape
-    transform.check(dt, head_dim)
-    L, check, _ = _binding()
-    st = L.dflash_qk_norm_rope(*a, *b, *c, *d, tokens, qs[1] if qs else 0, ks[1] if ks else 0, head_dim,
-                               _dtypes().get(dt, -1), transform.ref, None if positions is None else _positions(positions, tokens),
-                               _stream_of(x, stream))
+    st = (_calls or _load_calls()).norm_rope(q, k, q_out, k_out, transform, positions, stream)
     if st:
-        check(st, "dflash_qk_norm_rope")
+        _binding()[1](st, "dflash_qk_norm_rope")
+
+
+class PagedHandle(ctypes.c_void_p):
+    """The C handle with the shapes that it was made for."""
 
 
 def dflash_paged_init(*, heads, kv_heads, head_dim, page_size, dtype, cache_dtype=None, max_batch, stream=None):
@@ -238,53 +194,28 @@ def dflash_paged_init(*, heads, kv_heads, head_dim, page_size, dtype, cache_dtyp
                               dtype=codes.get(dtype, -1),
                               cache_dtype=codes.get(dtype if cache_dtype is None else cache_dtype, -1),
                               max_batch=max_batch)
-    h = ctypes.c_void_p()
-    check(L.dflash_paged_init(ctypes.byref(cfg), get_stream(stream), ctypes.byref(h)), "dflash_paged_init")
+    h = PagedHandle()
+    check(L.dflash_paged_init(ctypes.byref(cfg), get_stream(stream), ctypes.cast(ctypes.byref(h), ctypes.POINTER(ctypes.c_void_p))),
+          "dflash_paged_init")
+    h.spec = (h.value, dtype, dtype if cache_dtype is None else cache_dtype, heads, kv_heads, head_dim,
+              (page_size, kv_heads, head_dim))
     return h
 
 
 def dflash_paged_append(handle, cache, batch, k, v, transform=None, *, q=None, q_out=None, positions=None, stream=None):
     """Writes k (transformed) and v [tokens, kv_heads, head_dim] to the batch's places in the cache; with q also
-    q_out = the transformed queries [tokens, heads, head_dim]. All of the handle's shapes and dtype."""
-    dt, ks = k.dtype, k.shape
-    tokens = ks[0]
-    a = b = _NONE
-    if q is not None:
-        qs = q.shape
-        if qs[0] != tokens:
-            raise ValueError(f"q and k must have the same tokens, got {qs[0]} and {tokens}")
-        a, b = _rows(q, qs, dt, "q"), _rows(q_out, qs, dt, "q_out")
-    ref = None
-    if transform is not None:
-        transform.check(dt, ks[2])
-        ref = transform.ref
-    batch.c.tokens = tokens
-    L, check, _ = _binding()
-    st = L.dflash_paged_append(handle, cache.ref, batch.ref, *_rows(k, ks, dt, "k"), *_rows(v, ks, dt, "v"), ref,
-                               None if positions is None else _positions(positions, tokens), *a, *b,
-                               _stream_of(k, stream))
+    q_out = the transformed queries [tokens, heads, head_dim]."""
+    st = (_calls or _load_calls()).append(handle, cache, batch, k, v, transform, q, q_out, positions, stream)
     if st:
-        check(st, "dflash_paged_append")
+        _binding()[1](st, "dflash_paged_append")
 
 
 def dflash_paged_attend(handle, cache, batch, q, out, *, lse=None, causal=True, window=0, scale=None, stream=None):
     """out [tokens, heads, head_dim] = attention of q over the cache (scale None: 1 / sqrt(head_dim)); lse
-    [tokens, heads] fp32. All of the handle's shapes and dtype."""
-    dt, qs = q.dtype, q.shape
-    at = None
-    if lse is not None:
-        if lse.dtype is not _torch().float32:
-            raise TypeError(f"lse must be torch.float32, got {lse.dtype}")
-        if lse.shape != qs[:2] or not lse.is_contiguous() or not lse.is_cuda:
-            raise ValueError(f"lse must be a contiguous CUDA tensor {list(qs[:2])}")
-        at = lse.data_ptr()
-    batch.c.tokens = qs[0]
-    L, check, _ = _binding()
-    st = L.dflash_paged_attend(handle, cache.ref, batch.ref, *_rows(q, qs, dt, "q"), *_rows(out, qs, dt, "out"), at,
-                               1 if causal else 0, window, qs[2] ** -0.5 if scale is None else scale,
-                               _stream_of(q, stream))
+    [tokens, heads] fp32."""
+    st = (_calls or _load_calls()).attend(handle, cache, batch, q, out, lse, causal, window, scale, stream)
     if st:
-        check(st, "dflash_paged_attend")
+        _binding()[1](st, "dflash_paged_attend")
 
 
 def dflash_paged_sync_status(handle, stream=None):
@@ -299,37 +230,24 @@ def dflash_paged_destroy(handle):
 
 
 class PagedAttention:
-    """Owns a handle; checks that what it is called with has the handle's shapes."""
+    """Owns a handle (convenience only)."""
 
     def __init__(self, *, heads, kv_heads, head_dim, page_size, dtype, cache_dtype=None, max_batch):
-        self.heads, self.kv_heads, self.head_dim, self.dtype = heads, kv_heads, head_dim, dtype
-        self.cache_dtype = dtype if cache_dtype is None else cache_dtype
-        self.cache_shape = (page_size, kv_heads, head_dim)
         self.h = None
         self.h = dflash_paged_init(heads=heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, dtype=dtype,
                                    cache_dtype=cache_dtype, max_batch=max_batch)
 
-    def _fits(self, cache, x, heads, name):
-        if cache.dtype is not self.cache_dtype or cache.shape != self.cache_shape:
-            raise ValueError(f"the cache must be {self.cache_dtype} [pages, {', '.join(map(str, self.cache_shape))}], got "
-                             f"{cache.dtype} [pages, {', '.join(map(str, cache.shape))}]")
-        if x.dtype is not self.dtype:
-            raise TypeError(f"{name} must be {self.dtype}, got {x.dtype}")
-        if x.shape[1:] != (heads, self.head_dim):
-            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {list(x.shape)}")
-
     def append(self, cache, batch, k, v, transform=None, *, q=None, q_out=None, positions=None, stream=None):
-        self._fits(cache, k, self.kv_heads, "k")
-        if q is not None:
-            self._fits(cache, q, self.heads, "q")
-        dflash_paged_append(self.h, cache, batch, k, v, transform, q=q, q_out=q_out, positions=positions, stream=stream)
+        st = (_calls or _load_calls()).append(self.h, cache, batch, k, v, transform, q, q_out, positions, stream)
+        if st:
+            _binding()[1](st, "dflash_paged_append")
 
     def attend(self, cache, batch, q, out=None, *, lse=None, causal=True, window=0, scale=None, stream=None):
-        self._fits(cache, q, self.heads, "q")
         if out is None:
             out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
-        dflash_paged_attend(self.h, cache, batch, q, out, lse=lse, causal=causal, window=window, scale=scale,
-                            stream=stream)
+        st = (_calls or _load_calls()).attend(self.h, cache, batch, q, out, lse, causal, window, scale, stream)
+        if st:
+            _binding()[1](st, "dflash_paged_attend")
         return out
 
     def sync_status(self, stream=None):
