@@ -91,7 +91,7 @@ struct AttendParams {
 constexpr int kRowsUnit = 64;    // few rows: 8, 16 or 32 rows, units of 64 keys
 constexpr int kTileRows = 256;   // many rows
 constexpr int kTileUnit = 128;
-constexpr int kTicketParts = 8, kTicketWarps = 8;
+constexpr int kTicketParts = 4, kTicketWarps = 8;
 
 cudaError_t prepare_attend_rows(int smem_optin);
 cudaError_t launch_attend_rows(const AttendParams &p, int head_dim, int dtype, int fp8, int rows, int grid,
