@@ -124,6 +124,7 @@ struct PagedPlan {
     int ctas;      // G
     int b;         // sequence of `begin`
     int kvh, off;  // the head that it falls into, and the offset within the head
+    PagedSeq s;    // the sequence
 };
 
 // n / d, which the 64-bit division (some hundred cycles) is only needed for when n does not fit 32 bits.
@@ -151,13 +152,83 @@ __device__ __forceinline__ int paged_cost_warp(const AttendParams &p, const Page
     return __reduce_add_sync(0xFFFFFFFFu, u);
 }
 
+// This CTA's share of `total`.
+__device__ __forceinline__ void paged_share(PagedPlan &plan, int64_t total, int least)
+{
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), paged_div(total + least - 1, least)));
+    const int c = blockIdx.x;
+    plan.total = total;
+    plan.ctas = G;
+    plan.begin = plan.end = 0;
+    if (c < G) {  // total * c / G, in parts that fit
+        const int64_t q = paged_div(total, G);
+        const int rest = static_cast<int>(total - q * G);
+        plan.begin = q * c + static_cast<uint32_t>(rest * c) / static_cast<uint32_t>(G);
+        plan.end = q * (c + 1) + static_cast<uint32_t>(rest * (c + 1)) / static_cast<uint32_t>(G);
+    }
+}
+
+// What paged_seq() had to clamp.
+__device__ __forceinline__ void paged_report(const AttendParams &p, int b)
+{
+    const int len = __ldg(p.lens + b), t0 = __ldg(p.cu + b), t1 = __ldg(p.cu + b + 1);
+    if (len < 0 || len > static_cast<int64_t>(p.table_cols) * p.page || t0 < 0 || t1 < t0 || t1 > p.tokens)
+        atomicOr(p.err, DEV_ERR_PLACE);
+}
+
+// The plan of up to 32 sequences, by one warp, a lane each: one round of reads
+// and no barrier (a call of few units is all latency).
+__device__ __forceinline__ PagedPlan paged_plan_warp(const AttendParams &p, PagedCut cut, int least, int lane)
+{
+    PagedPlan plan;
+    PagedSeq s = {0, 0, 0};
+    int head = 0;  // cost per key/value head
+    bool by_warp = false;
+    if (lane < p.B) {
+        s = paged_seq(p, lane);
+        by_warp = paged_row_tiles(p, s, cut.R) > 2;
+        if (!by_warp) head = paged_cost(p, s, cut);
+    }
+    for (unsigned m = __ballot_sync(0xFFFFFFFFu, by_warp); m; m &= m - 1) {
+        const int b = __ffs(m) - 1;
+        const PagedSeq of = {0, __shfl_sync(0xFFFFFFFFu, s.n, b), __shfl_sync(0xFFFFFFFFu, s.len, b)};
+        const int u = paged_cost_warp(p, of, cut, lane);
+        if (lane == b) head = u;
+    }
+    const int64_t mine = static_cast<int64_t>(head) * p.kv_heads;
+    int64_t upto = mine;
+    for (int o = 1; o < p.B; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    paged_share(plan, __shfl_sync(0xFFFFFFFFu, upto, p.B - 1), least);
+    const unsigned at = __ballot_sync(0xFFFFFFFFu, lane < p.B && plan.begin < upto);
+    plan.b = max(0, __ffs(at) - 1);  // (sequences without new tokens cost nothing and are passed over)
+    plan.s = {__shfl_sync(0xFFFFFFFFu, s.t0, plan.b), __shfl_sync(0xFFFFFFFFu, s.n, plan.b), __shfl_sync(0xFFFFFFFFu, s.len, plan.b)};
+    const int64_t off = plan.begin - __shfl_sync(0xFFFFFFFFu, upto - mine, plan.b);
+    const int per_head = max(1, __shfl_sync(0xFFFFFFFFu, head, plan.b));
+    plan.kvh = static_cast<int>(paged_div(off, per_head));
+    plan.off = static_cast<int>(off - static_cast<int64_t>(plan.kvh) * per_head);
+    if (blockIdx.x == 0 && lane < p.B) paged_report(p, lane);
+    return plan;
+}
+
 // cost: kPlanSeqs ints of shared memory that are free until the plan is made.
+// The block meets in here at least once.
 template <int NT>
 __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, int *cost)
 {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ PagedPlan plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.B <= 32) {
+        if (warp == 0) {
+            const PagedPlan small = paged_plan_warp(p, cut, least, lane);
+            if (lane == 0) plan = small;
+        }
+        __syncthreads();
+        return plan;
+    }
     const int per = (p.B + NT - 1) / NT;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     const bool kept = p.B <= kPlanSeqs;
@@ -171,11 +242,7 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, 
             cost[b] = by_warp ? -1 : paged_cost(p, s, cut);
             many |= by_warp;
         }
-        if (blockIdx.x == 0) {  // what paged_seq() had to clamp
-            const int len = __ldg(p.lens + b), t0 = __ldg(p.cu + b), t1 = __ldg(p.cu + b + 1);
-            if (len < 0 || len > static_cast<int64_t>(p.table_cols) * p.page || t0 < 0 || t1 < t0 || t1 > p.tokens)
-                atomicOr(p.err, DEV_ERR_PLACE);
-        }
+        if (blockIdx.x == 0) paged_report(p, b);
     }
     if (__syncthreads_or(many)) {
         for (int b = warp; b < p.B; b += NT / 32)
@@ -190,14 +257,10 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, 
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(head_cost(b)) * p.kv_heads;
     int64_t scan = mine;
-    if (p.B > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-            if (lane >= o) scan += v;
-        }
-    } else {
-        scan = __shfl_sync(0xFFFFFFFFu, mine, 0);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
     }
     if (lane == 31) warp_sum[warp] = scan;
     __syncthreads();
@@ -207,31 +270,22 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, 
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), paged_div(total + least - 1, least)));
-    const int c = blockIdx.x;
-    int64_t begin = 0, end = 0;
-    if (c < G) {  // total * c / G, in parts that fit
-        const int64_t q = paged_div(total, G);
-        const int rest = static_cast<int>(total - q * G);
-        begin = q * c + static_cast<uint32_t>(rest * c) / static_cast<uint32_t>(G);
-        end = q * (c + 1) + static_cast<uint32_t>(rest * (c + 1)) / static_cast<uint32_t>(G);
-    }
-    if (begin < end ? (before <= begin && begin < before + mine) : tid == 0) {
-        int64_t off = begin - before;
+    PagedPlan made;
+    paged_share(made, total, least);
+    if (made.begin < made.end ? (before <= made.begin && made.begin < before + mine) : tid == 0) {
+        int64_t off = made.begin - before;
         int b = b0, per_head = 1;
-        if (begin < end)
+        if (made.begin < made.end)
             for (; b < b1; ++b) {
                 per_head = head_cost(b);
                 if (off < static_cast<int64_t>(per_head) * p.kv_heads) break;
                 off -= static_cast<int64_t>(per_head) * p.kv_heads;
             }
-        plan.total = total;
-        plan.begin = begin;
-        plan.end = end;
-        plan.ctas = G;
-        plan.b = b;
-        plan.kvh = begin < end ? static_cast<int>(paged_div(off, per_head)) : 0;
-        plan.off = static_cast<int>(off - static_cast<int64_t>(plan.kvh) * per_head);
+        made.b = b;
+        made.kvh = made.begin < made.end ? static_cast<int>(paged_div(off, per_head)) : 0;
+        made.off = static_cast<int>(off - static_cast<int64_t>(made.kvh) * per_head);
+        made.s = paged_seq(p, min(b, p.B - 1));
+        plan = made;
     }
     __syncthreads();
     return plan;
@@ -264,7 +318,7 @@ struct PagedWalk {
         if (!more) return;
         const int lane = threadIdx.x & 31;
         pc.b = plan.b;
-        pc.s = paged_seq(p, pc.b);
+        pc.s = plan.s;
         nrt = paged_row_tiles(p, pc.s, k.R);
         pc.kvh = plan.kvh;
         pc.rt = 0;

@@ -14,10 +14,10 @@ namespace {
 // for an 8-bit one.
 constexpr int tile_threads(bool fp8) { return fp8 ? 512 : 384; }
 constexpr int load_warps(bool fp8) { return fp8 ? 6 : 3; }  // that queries and finished tiles come from
-// Registers: 168 (128) a thread at launch; the streams take 208 (184) and the
-// rest keep 88 (72): 256 * 208 + 128 * 88 = 384 * 168, 256 * 184 + 256 * 72 = 512 * 128.
-constexpr int stream_regs(bool fp8) { return fp8 ? 184 : 208; }
-constexpr int other_regs(bool fp8) { return fp8 ? 72 : 88; }
+// Registers: 168 (128) a thread at launch; the streams take 200 (184) and the
+// rest keep 104 (72): 256 * 200 + 128 * 104 = 384 * 168, 256 * 184 + 256 * 72 = 512 * 128.
+constexpr int stream_regs(bool fp8) { return fp8 ? 184 : 200; }
+constexpr int other_regs(bool fp8) { return fp8 ? 72 : 104; }
 
 constexpr uint32_t kTmemCols = 512;
 #ifndef DFL_TILE_COST
@@ -135,8 +135,9 @@ __device__ __forceinline__ void umma_commit_if(uint32_t who, uint64_t *bar)
         : "memory");
 }
 
+#define DFL_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 // (written before the last operand is read)
-#define DFL_R8(r, i) "=&r"(r[i]), "=&r"(r[i + 1]), "=&r"(r[i + 2]), "=&r"(r[i + 3]), "=&r"(r[i + 4]), "=&r"(r[i + 5]), "=&r"(r[i + 6]), "=&r"(r[i + 7])
+#define DFL_E8(r, i) "=&r"(r[i]), "=&r"(r[i + 1]), "=&r"(r[i + 2]), "=&r"(r[i + 3]), "=&r"(r[i + 4]), "=&r"(r[i + 5]), "=&r"(r[i + 6]), "=&r"(r[i + 7])
 #define DFL_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
 
 // 32 consecutive columns of this thread's lane; waits for the load.
@@ -151,24 +152,45 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32])
         : "memory");
 }
 
-// 128 consecutive columns of this thread's lane; waits for the loads.
+// 128 consecutive columns of this thread's lane; waits for the load (FEW: in
+// four instructions, which a kernel of 128 registers a thread at launch needs).
+template <bool FEW>
 __device__ __forceinline__ void tmem_load128(uint32_t taddr, uint32_t (&r)[128])
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : DFL_R8(r, 0), DFL_R8(r, 8), DFL_R8(r, 16), DFL_R8(r, 24), DFL_R8(r, 32), DFL_R8(r, 40), DFL_R8(r, 48),
-          DFL_R8(r, 56), DFL_R8(r, 64), DFL_R8(r, 72), DFL_R8(r, 80), DFL_R8(r, 88), DFL_R8(r, 96), DFL_R8(r, 104),
-          DFL_R8(r, 112), DFL_R8(r, 120)
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
-        : "memory");
+    if constexpr (!FEW) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+            "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+            "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+            "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+            "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+            "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+            "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+            "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+            "tcgen05.wait::ld.sync.aligned;\n"
+            : DFL_R8(r, 0), DFL_R8(r, 8), DFL_R8(r, 16), DFL_R8(r, 24), DFL_R8(r, 32), DFL_R8(r, 40), DFL_R8(r, 48),
+              DFL_R8(r, 56), DFL_R8(r, 64), DFL_R8(r, 72), DFL_R8(r, 80), DFL_R8(r, 88), DFL_R8(r, 96), DFL_R8(r, 104),
+              DFL_R8(r, 112), DFL_R8(r, 120)
+            : "r"(taddr)
+            : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+            "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+            "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+            "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
+            "tcgen05.wait::ld.sync.aligned;\n"
+            : DFL_E8(r, 0), DFL_E8(r, 8), DFL_E8(r, 16), DFL_E8(r, 24), DFL_E8(r, 32), DFL_E8(r, 40), DFL_E8(r, 48),
+              DFL_E8(r, 56), DFL_E8(r, 64), DFL_E8(r, 72), DFL_E8(r, 80), DFL_E8(r, 88), DFL_E8(r, 96), DFL_E8(r, 104),
+              DFL_E8(r, 112), DFL_E8(r, 120)
+            : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+            : "memory");
+    }
 }
 
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32])
@@ -356,7 +378,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 tc_fence_after_sync();
                 if (FP8 && t == 0) factor *= __uint_as_float((19u + q_exp[c.r]) << 23);
                 uint32_t sr[128];
-                tmem_load128(s_col, sr);
+                tmem_load128<FP8>(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {  // a bit per key of 32
