@@ -176,25 +176,37 @@ __device__ __forceinline__ void paged_report(const AttendParams &p, int b)
         atomicOr(p.err, DEV_ERR_PLACE);
 }
 
-// The plan of up to 32 sequences, by one warp, a lane each: one round of reads
-// and no barrier (a call of few units is all latency).
-__device__ __forceinline__ PagedPlan paged_plan_warp(const AttendParams &p, PagedCut cut, int least, int lane)
+// The plan of up to 32 sequences, a lane each: one round of reads, by every
+// warp of the block (a call of few units is all latency). Long sequences'
+// costs are shared out between the warps, through `cost`; warp 0 returns the
+// plan.
+template <int NT>
+__device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, PagedCut cut, int least, int *cost)
 {
-    PagedPlan plan;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    PagedPlan plan = {};
     PagedSeq s = {0, 0, 0};
     int head = 0;  // cost per key/value head
-    bool by_warp = false;
+    bool many = false;
     if (lane < p.B) {
         s = paged_seq(p, lane);
-        by_warp = paged_row_tiles(p, s, cut.R) > 2;
-        if (!by_warp) head = paged_cost(p, s, cut);
+        many = paged_row_tiles(p, s, cut.R) > 2;
+        if (!many) head = paged_cost(p, s, cut);
     }
-    for (unsigned m = __ballot_sync(0xFFFFFFFFu, by_warp); m; m &= m - 1) {
-        const int b = __ffs(m) - 1;
-        const PagedSeq of = {0, __shfl_sync(0xFFFFFFFFu, s.n, b), __shfl_sync(0xFFFFFFFFu, s.len, b)};
-        const int u = paged_cost_warp(p, of, cut, lane);
-        if (lane == b) head = u;
+    const unsigned long_ones = __ballot_sync(0xFFFFFFFFu, many);
+    if (long_ones) {
+        int k = 0;
+        for (unsigned m = long_ones; m; m &= m - 1, ++k) {
+            if (k % (NT / 32) != warp) continue;
+            const int b = __ffs(m) - 1;
+            const PagedSeq of = {0, __shfl_sync(0xFFFFFFFFu, s.n, b), __shfl_sync(0xFFFFFFFFu, s.len, b)};
+            const int u = paged_cost_warp(p, of, cut, lane);
+            if (lane == 0) cost[b] = u;
+        }
+        __syncthreads();
+        if (many) head = cost[lane];
     }
+    if (warp > 0) return plan;
     const int64_t mine = static_cast<int64_t>(head) * p.kv_heads;
     int64_t upto = mine;
     for (int o = 1; o < p.B; o <<= 1) {
@@ -222,10 +234,8 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int least, 
     __shared__ PagedPlan plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.B <= 32) {
-        if (warp == 0) {
-            const PagedPlan small = paged_plan_warp(p, cut, least, lane);
-            if (lane == 0) plan = small;
-        }
+        const PagedPlan small = paged_plan_warps<NT>(p, cut, least, cost);
+        if (tid == 0) plan = small;
         __syncthreads();
         return plan;
     }
@@ -411,19 +421,23 @@ __device__ __forceinline__ bool paged_last(unsigned *ticket, int parts, int lane
     return got == static_cast<unsigned>(parts) - 1;
 }
 
-// True (and the counter is cleared) if all parts but this warp's are written
-// already: then it need not write its own.
-__device__ __forceinline__ bool paged_all_others(unsigned *ticket, int parts, int lane)
+// How many parts have been written (lane 0 reads; what they are is read after
+// paged_all_others()).
+__device__ __forceinline__ unsigned paged_written(const unsigned *ticket, int lane)
 {
-    unsigned got = 0;
-    if (lane == 0) {
-        got = atomicAdd(ticket, 0u);
-        if (got == static_cast<unsigned>(parts) - 1) *ticket = 0;
-    }
-    got = __shfl_sync(0xFFFFFFFFu, got, 0);
-    if (got != static_cast<unsigned>(parts) - 1) return false;
-    __threadfence();
-    return true;
+    unsigned n = 0;
+    if (lane == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(ticket) : "memory");
+    return n;
+}
+
+// True (and the counter is cleared) if that was all parts but this warp's: then
+// it need not write its own.
+__device__ __forceinline__ bool paged_all_others(unsigned *ticket, unsigned written, int parts, int lane)
+{
+    const bool all = __shfl_sync(0xFFFFFFFFu, written, 0) == static_cast<unsigned>(parts) - 1;
+    if (all && lane == 0) *ticket = 0;
+    if (all) __threadfence();
+    return all;
 }
 
 }  // namespace dfl

@@ -323,6 +323,10 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
         tmem_alloc(smem_u32(&bars.tmem), kTmemCols);
         tmem_relinquish();
     }
+    if (tid == 9 * 32) {
+        tma_prefetch_desc(&tp.tm_k);
+        tma_prefetch_desc(&tp.tm_v);
+    }
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
@@ -445,6 +449,9 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 merge0 = make_int4(walk.pc.s.t0, walk.pc.rt * R, min(R, walk.pc.s.n * p.group - walk.pc.rt * R), walk.pc.kvh);
                 merge1 = make_int4(share.y, 0, 0, 0);
             }
+            const bool by_ticket = split && share.y <= kTicketParts && !(e.alt && i == 1);
+            unsigned *const ticket = p.ticket + share.x * kTicketWarps + warp;
+            const unsigned written = by_ticket ? paged_written(ticket, lane) : 0;  // (on its way while the products end)
             more = walk.next(p, cut);
             if (more) c = row_of(walk.pc);
             if (e.steps > 0) {
@@ -521,8 +528,6 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                     return reinterpret_cast<float4 *>(p.part_o) + (slot * (D / 4) + k / 4) * R + e.r;
                 };
                 bool last = false;
-                unsigned *const ticket = p.ticket + share.x * kTicketWarps + warp;
-                const bool by_ticket = split && share.y <= kTicketParts;
                 if (!split) {
                     const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;
 #pragma unroll 1
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                     store_lse(m, l);
                 } else {
                     // the last to finish need not write its part down
-                    if (by_ticket) last = paged_all_others(ticket, share.y, lane);
+                    if (by_ticket) last = paged_all_others(ticket, written, share.y, lane);
                     if (!last) {
                         const int64_t slot = paged_slot(share.x, mine);
 #pragma unroll 1
