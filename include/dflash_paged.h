@@ -109,18 +109,18 @@ dflash_status dflash_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t
                                   const int32_t *positions, void *stream);
 
 /* Checks the shapes and allocates the workspace that attention over split
- * sequences needs (the only allocation; about 100 MB). One handle serves all
+ * sequences needs (the only allocation; 40 MB with head_dim 128). One handle serves all
  * layers of a model; its calls must not overlap on the GPU (order them on one
  * stream). Errors: INVALID_ARG, UNSUPPORTED (also: not an sm_103 GPU), CUDA. */
 dflash_status dflash_paged_init(const dflash_paged_config *cfg, void *stream, dflash_paged_handle *out);
 
 /* Writes k and v [tokens, kv_heads, head_dim] of the batch's new tokens to
  * their places in the cache, k after the transform (NULL: as it is), both
- * divided by their scale and rounded (saturating) for E4M3. With q also
- * q_out = the transformed q [tokens, heads, head_dim] (in place is allowed).
- * A token's position is its place, or positions[token] where given. A token
- * without a valid place or page is not written and latched as
- * DEVICE_CHECK. Errors: INVALID_ARG, CUDA. */
+ * divided by their scale (a product with its fp32 reciprocal) and rounded
+ * (saturating) for E4M3. With q also q_out = the transformed q [tokens, heads,
+ * head_dim] (in place is allowed). A token's position is its place, or
+ * positions[token] where given. Keys and values of a token without a valid
+ * place or page are not written, and it is latched as DEVICE_CHECK. Errors: INVALID_ARG, CUDA. */
 dflash_status dflash_paged_append(dflash_paged_handle h, const dflash_paged_cache *cache,
                                   const dflash_paged_batch *batch, const void *k, int64_t k_token_stride,
                                   int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
@@ -136,10 +136,13 @@ dflash_status dflash_paged_append(dflash_paged_handle h, const dflash_paged_cach
  * sum of exp(score), -inf for such a token. out must not overlap q.
  * Sums, maxima and products accumulate in fp32; the softmax weights are
  * rounded to the cache's 16-bit type (fp16 for E4M3 caches) for the matrix
- * product. Values outside [0, lens[b]) and pages that no key of a call's
- * tokens is on are never read; a place's key and value have to be finite
- * unless every token of the call that shares its sequence sees it. An invalid page id
- * or a length beyond the table reads as zeros and is latched as DEVICE_CHECK.
+ * product. What is stored at places >= lens[b], and on pages that hold no key
+ * that some token of the call sees, is never used and may be anything (those
+ * pages need no entry in the table). The values (not the keys) at the other
+ * places have to be finite for the tokens that do not see them too: their
+ * weight there is zero. Keys on an invalid page read as zeros, a length beyond
+ * the table is cut to it, and both are latched as DEVICE_CHECK. lens[b] stays
+ * below 2^31 - 4096.
  * Errors: INVALID_ARG, CUDA. */
 dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash_paged_cache *cache,
                                   const dflash_paged_batch *batch, const void *q, int64_t q_token_stride,

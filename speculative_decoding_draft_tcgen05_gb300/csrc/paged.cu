@@ -14,10 +14,6 @@ dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, int bytes, 
                                    int box_rows);
 }
 
-#ifndef DFL_TILE_MIN_ROWS
-#define DFL_TILE_MIN_ROWS 32
-#endif
-
 struct dflash_paged_ctx {
     dflash_paged_config cfg;
     int dev = 0, num_sms = 0;
@@ -288,11 +284,16 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     p.merge = h->merge;
     p.ticket = h->ticket;
     p.err = h->err;
+    if (!isnormal(p.scale_log2))
+        return paged_fail(DFLASH_ERR_INVALID_ARG, "scale (times k_scale) must be an ordinary fp32 number");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t most_rows = static_cast<int64_t>(batch->max_tokens) * p.group;
     cudaError_t e;
     int rows, grid;
-    if (most_rows > DFL_TILE_MIN_ROWS) {
+    // The few-row kernel keeps up to 32 rows of accumulators in registers and streams the keys at the memory's
+    // rate (32 ragged sequences of 32 rows: 102 us, by the other 124); beyond that it would read them once per
+    // 32 rows, where the tensor-memory kernel takes 256 (64 rows of 40 heads: 94 us, by this one 157).
+    if (most_rows > 32) {
         CUtensorMap tm_k, tm_v;
         const int box = dfl::tile_box_rows(p.page), bytes = fp8 ? 1 : 2;
         dflash_status st2 = dfl::host_make_tmap_pages(&tm_k, p.k, bytes, h->cfg.head_dim, p.page, p.kv_heads, p.num_pages,
@@ -327,7 +328,9 @@ extern "C" dflash_status dflash_paged_sync_status(dflash_paged_handle h, void *s
         cudaStreamSynchronize(s) != cudaSuccess)
         return paged_fail(DFLASH_ERR_CUDA, "reading the device error word failed");
     if (e == 0) return DFLASH_OK;
-    if (cudaMemsetAsync(h->err, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    // (with the counters of split items, which a pipeline that gave up may have left behind)
+    const size_t bytes = reinterpret_cast<char *>(h->err + 1) - reinterpret_cast<char *>(h->ticket);
+    if (cudaMemsetAsync(h->ticket, 0, bytes, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return paged_fail(DFLASH_ERR_CUDA, "clearing the device error word failed");
     if (e & dfl::DEV_ERR_TIMEOUT)
         return paged_fail(DFLASH_ERR_TIMEOUT, "an attention pipeline wait exceeded its time bound (error word %lld)", e);

@@ -9,13 +9,7 @@ namespace dfl {
 namespace {
 
 constexpr int kRowsThreads = 128;  // 4 warps
-#ifndef DFL_ROWS_COST
-#define DFL_ROWS_COST 5
-#endif
-#ifndef DFL_ROWS_LEAST
-#define DFL_ROWS_LEAST 1
-#endif
-constexpr int kRowsCost = DFL_ROWS_COST, kRowsLeast = DFL_ROWS_LEAST;
+constexpr int kRowsCost = 5;       // units that starting an item costs
 constexpr int kRowsWarps = kRowsThreads / 32;
 template <int MT> constexpr int rows_ring() { return MT == 1 ? 16 * 1024 : 24 * 1024; }
 
@@ -153,7 +147,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
     pdl_trigger();
     pdl_wait();
     constexpr PagedCut cut = {R, kRowsUnit, kRowsCost};
-    const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, kRowsLeast, reinterpret_cast<int *>(smem));
+    const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, reinterpret_cast<int *>(smem));
     PagedWalk walk;
     walk.start(p, plan, cut);
     int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;

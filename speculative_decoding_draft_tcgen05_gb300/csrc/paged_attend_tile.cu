@@ -20,10 +20,7 @@ constexpr int stream_regs(bool fp8) { return fp8 ? 184 : 200; }
 constexpr int other_regs(bool fp8) { return fp8 ? 72 : 104; }
 
 constexpr uint32_t kTmemCols = 512;
-#ifndef DFL_TILE_COST
-#define DFL_TILE_COST 4
-#endif
-constexpr int kTileCost = DFL_TILE_COST, kTileLeast = 1;
+constexpr int kTileCost = 4;  // tiles that starting an item costs
 
 template <int D, bool FP8>
 struct TileShape {
@@ -330,7 +327,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
-    const PagedPlan plan = paged_plan<tile_threads(FP8)>(p, cut, kTileLeast, reinterpret_cast<int *>(smem));  // holds block barriers
+    const PagedPlan plan = paged_plan<tile_threads(FP8)>(p, cut, reinterpret_cast<int *>(smem));  // holds block barriers
     tc_fence_after_sync();
     const uint32_t tmem = bars.tmem;
     int *const ab = &bars.abort_flag;

@@ -340,6 +340,46 @@ def test_attend_no_contamination_between_sequences(pkg):
     assert torch.equal(a[:2], b[:2]) and torch.equal(a[4:], b[4:]) and b[2:4].isnan().all()
 
 
+@pytest.mark.parametrize("cache", [None, FP8])
+@pytest.mark.parametrize("new,lens", [
+    ([1, 2] * 300, [1 + 7 * i % 90 + 1 for i in range(600)]),          # more sequences than are planned in shared memory
+    ([3] * 30 + [200, 0, 150] + [1] * 12, [40 + i for i in range(45)]),  # long ones among more than a warp of them;
+                                                                         # some with more new tokens than places
+    ([0, 0, 5, 0], [3, 0, 77, 9]),                                       # hardly any rows
+])
+def test_attend_many_sequences(pkg, new, lens, cache):
+    s = Paged(pkg, new, lens, heads=4, kv_heads=2, d=64, dtype=BF16, cache=cache, seed=len(new), pad=5)
+    q = s.rows(4)
+    s.check(q)
+    s.batch.c.max_tokens = 1  # by the other kernel
+    s.check(q)
+
+
+@pytest.mark.parametrize("heads", [40, 300])
+@pytest.mark.parametrize("cache", [None, FP8])
+def test_attend_wide_groups(pkg, heads, cache):
+    """One key head for 40 and 300 query heads: rows of a token spread over several tiles."""
+    s = Paged(pkg, [3, 1], [500, 70], heads=heads, kv_heads=1, d=64, dtype=FP16, cache=cache, seed=heads)
+    s.check(s.rows(heads))
+    s.check(s.rows(heads), window=33)
+
+
+def test_attend_masked_keys_may_be_anything(pkg):
+    """NaN and infinite keys at places that some tokens do not see leave those tokens alone; a value there must be finite."""
+    for new in (6, 90):
+        s = Paged(pkg, [new], [300], heads=4, kv_heads=2, d=64, dtype=BF16, seed=new, poison=False)
+        q = s.rows(4)
+        want = s.layer.attend(s.cache, s.batch, q)
+        at = 300 - 2  # seen by the last two tokens only
+        page = int(s.table[0, at // 16])
+        s.k[page, at % 16] = math.nan
+        got = s.layer.attend(s.cache, s.batch, q)
+        assert torch.equal(got[:-2], want[:-2]) and got[-2:].isnan().all()
+        s.k[page, at % 16] = math.inf
+        got = s.layer.attend(s.cache, s.batch, q)
+        assert torch.equal(got[:-2], want[:-2])
+
+
 @pytest.mark.parametrize("new,length", [(8, 40000), (1, 70001), (300, 20000)])
 def test_attend_long(pkg, new, length):
     """Long contexts: the keys of an item split over many CTAs."""
@@ -527,6 +567,7 @@ def test_refusals(pkg):
     refused(inv, lambda: s.layer.attend(s.cache, s.batch, q, window=-1))
     refused(inv, lambda: s.layer.attend(s.cache, s.batch, q, scale=0.0))
     refused(inv, lambda: s.layer.attend(s.cache, s.batch, q, scale=math.nan))
+    refused(inv, lambda: s.layer.attend(s.cache, s.batch, q, scale=1e-42))
     big = pkg.PagedBatch(torch.zeros(4, device="cuda", dtype=torch.int32), torch.zeros(3, device="cuda", dtype=torch.int32),
                          torch.zeros(3, 2, device="cuda", dtype=torch.int32), max_tokens=1)
     refused(inv, lambda: s.layer.attend(s.cache, big, q))                               # above max_batch
