@@ -37,19 +37,21 @@ __device__ __forceinline__ int warp_find(const int32_t *cu, int B, int t, int la
 // cache and positions (a chain of dependent small reads, once per block) and
 // brings their cosines and sines to shared memory. Then its warps share the
 // jobs: 32 / LPH heads of the queries, keys or values (LPH = D / 8 lanes to a
-// head, 8 values each) of kPrepJob consecutive tokens, so that a job's
-// pointers and weights are set up once for several rows. A lane holds four
+// head, 8 values each) of one token, or in a large batch of 4 consecutive
+// ones, so that a job's pointers and weights are set up once for several rows. A lane holds four
 // whole rotation pairs, 4 values from each half of the rotated part (or 8
 // adjacent ones where pairs are adjacent), so the rotation needs no exchange
 // between lanes, and the sum of squares is a shuffle over the head's lanes.
 //
 // Bound by HBM when the instructions per value stay near ten (each value is
 // read and written once). Inputs come through asynchronous copies to shared
-// memory, kPrepAhead jobs of a warp in flight: the first ones while the block
+// memory, several jobs of a warp in flight: the first ones while the block
 // looks up its places and angles, the others while the warp works.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32, kPrepBlocks = 4;
-constexpr int kPrepJob = 4, kPrepAhead = 2;
+
+// Jobs of a warp whose inputs are in flight.
+constexpr int prep_ahead(int job) { return job == 1 ? 4 : 2; }
 
 // Tokens of a block (with the copies' 32 KB, what fits 48 KB of shared memory).
 template <int D>
@@ -58,11 +60,11 @@ constexpr int prep_tokens()
     return D <= 128 ? 16 : 8;
 }
 
-template <int D, typename T>
+template <int D, typename T, int kPrepJob>
 __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) prep_kernel(const __grid_constant__ PrepParams p, int per_block)
 {
     constexpr int LPH = D / 8, HPP = 32 / LPH;
-    constexpr int TOKENS = prep_tokens<D>();
+    constexpr int TOKENS = prep_tokens<D>(), kPrepAhead = prep_ahead(kPrepJob);
     __shared__ int64_t tok_row[TOKENS];        // its row of the cache (without the head)
     __shared__ int tok_pos[TOKENS], tok_is[TOKENS];  // position; 1: stored, 0: no place, -1: padding
     __shared__ float4 angles[TOKENS * D / 4];  // [token][rotary]: cosines, then sines
@@ -265,21 +267,26 @@ template <int D, typename T>
 cudaError_t go(const PrepParams &p, cudaStream_t s)
 {
     // As many tokens a block as fill every SM's kPrepBlocks blocks once, up to prep_tokens() (a large batch then shares
-    // place and angle reads between a block's warps); a small batch has one token a block, and where blocks are
-    // left its jobs are spread over several of them.
+    // place and angle reads between a block's warps), in jobs of 4 from 3 on; a small batch has one or two tokens a
+    // block and jobs of one (272 tokens of 56 heads: 9.5 us with jobs of 4, most of them empty), spread over several
+    // blocks where some are left.
     constexpr int HPP = 32 / (D / 8);
     int dev = 0, sms = 1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int slots = kPrepBlocks * sms, per = (p.tokens + slots - 1) / slots;
-    const int per_block = per < prep_tokens<D>() ? per : prep_tokens<D>(), blocks = (p.tokens + per_block - 1) / per_block;
+    const bool many = per > 2;
+    int per_block = many ? (per + 3) / 4 * 4 : per;
+    if (per_block > prep_tokens<D>()) per_block = prep_tokens<D>();
+    const int blocks = (p.tokens + per_block - 1) / per_block;
     const int passes = (p.q.heads + HPP - 1) / HPP + (p.k.heads + HPP - 1) / HPP + (p.v.heads + HPP - 1) / HPP;
-    const int jobs = passes * ((per_block + kPrepJob - 1) / kPrepJob);
+    const int jobs = passes * (many ? per_block / 4 : per_block);
     int y = slots / blocks;
     const int most = (jobs + kPrepWarps - 1) / kPrepWarps;
     y = y < 1 ? 1 : (y > most ? most : y);
-    return launch_ex(prep_kernel<D, T>, dim3(blocks, y), dim3(kPrepThreads), 0, s, 1, p, per_block);
+    return many ? launch_ex(prep_kernel<D, T, 4>, dim3(blocks, y), dim3(kPrepThreads), 0, s, 1, p, per_block)
+                : launch_ex(prep_kernel<D, T, 1>, dim3(blocks, y), dim3(kPrepThreads), 0, s, 1, p, per_block);
 }
 
 }  // namespace
