@@ -51,6 +51,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
+// A thread's pair (row lane / 4, columns 2 (lane % 4), + 1) of an 8 x 8 matrix -> the same of its transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -130,7 +138,11 @@ template <int D, int R, typename QT, bool FP8>
 __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
 {
     using CT = typename std::conditional<FP8, __half, QT>::type;  // type of the matrix products
-    constexpr int MT = (R + 15) / 16, NH = R / 8;  // 16-row products, and halves of them that hold rows
+    // Up to 8 rows (NARROW) are the 8 columns of the products, the 16 keys or values their rows; more rows are the
+    // products' rows, in MT tiles of 16. NH: rows of a thread's state.
+    constexpr bool NARROW = R == 8;
+    constexpr int MT = (R + 15) / 16, NH = NARROW ? 2 : R / 8, OT = NARROW ? D / 16 : D / 8;
+    constexpr int LANE0 = NARROW ? 4 : 1, LANE1 = NARROW ? 32 : 4;  // lanes that share a row differ in these bits
     using SH = RowsShape<D, MT, FP8>;
     constexpr int kRowsRing = rows_ring<MT>();
     constexpr int S = SH::STAGES, CH = SH::CH;
@@ -249,13 +261,14 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
             }
             __syncthreads();
 
-            // ---- limits of this thread's rows (8 h + lane / 4 of row tile mt): keys in (after, upto]
+            // ---- limits of this thread's rows: keys in (after, upto]
+            auto row_of = [&](int i) { return NARROW ? 2 * (lane & 3) + i : 8 * i + (lane >> 2); };
             int upto[NH], after[NH];
             float factor[NH];
             int most_after = -1, least_upto = 0x7FFFFFFF;
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
-                const int r = 8 * i + (lane >> 2);
+                const int r = row_of(i);
                 const int place = base + p.by_group.div(pc.rt * R + r);
                 upto[i] = r < rows ? (p.causal ? min(place, s.len - 1) : s.len - 1) : -1;
                 after[i] = p.window > 0 ? place - p.window : -1;
@@ -268,18 +281,20 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
             least_upto = __reduce_min_sync(0xFFFFFFFFu, least_upto);
             most_after = __reduce_max_sync(0xFFFFFFFFu, most_after);
 
-            // An 8-bit cache's products take a query row's values 16 c + 4 (lane % 4) .. + 3 (see below); those of up
-            // to 8 rows stay in registers.
+            // An 8-bit cache's products take a query row's values 16 c + 4 (lane % 4) .. + 3 (see below).
             auto q_pair = [&](int r, int c) {
                 return *reinterpret_cast<const uint2 *>(smem + q_at(r, 2 * c + ((lane & 3) >> 1)) + 8 * (lane & 1));
             };
-            uint2 qf[FP8 && NH == 1 ? D / 16 : 1];
-            if constexpr (FP8 && NH == 1) {
+            uint2 qf[NARROW ? D / 16 : 1];  // up to 8 rows stay in registers
+            if constexpr (NARROW) {
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) qf[c] = q_pair(lane >> 2, c);
+                for (int c = 0; c < D / 16; ++c)
+                    qf[c] = FP8 ? q_pair(lane >> 2, c)
+                                : make_uint2(*reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c) + 4 * (lane & 3)),
+                                             *reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c + 1) + 4 * (lane & 3)));
             }
 
-            float o[MT][D / 8][4];
+            float o[MT][OT][4];
             float m[NH], l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n)
+                for (int n = 0; n < OT; ++n)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
 
@@ -309,45 +324,63 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) sc[i][n][k] = 0.f;
+                if constexpr (NARROW) {
+                    // sc[0][n][k]: key 8 n + lane / 4, row k; two sums take turns, so that the chain of products is half as long
+                    float acc[2][4];
 #pragma unroll
-                for (int c2 = 0; c2 < (FP8 ? D / 32 : D / 16); ++c2) {
-                    uint32_t kf[4];
-                    if constexpr (FP8) {
-                        // matrices: keys 0-7 and 8-15 of chunks 2 c2 and 2 c2 + 1. A thread gets 4
-                        // consecutive values of a key; they stand for k = 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-                        // of the product (the queries below are read in the same order).
-                        ldsm4(ks + SH::at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c2 + (lane >> 4)), kf);
+                    for (int k = 0; k < 4; ++k) acc[0][k] = acc[1][k] = 0.f;
 #pragma unroll
-                        for (int hc = 0; hc < 2; ++hc) {
-                            uint32_t b00, b01, b10, b11;
-                            e4m3x4_to_h2x2(kf[2 * hc], b00, b01);
-                            e4m3x4_to_h2x2(kf[2 * hc + 1], b10, b11);
+                    for (int c2 = 0; c2 < CH / 2; ++c2) {
+                        uint32_t kf[4];  // keys 0-7 and 8-15 of chunk 2 c2, and of chunk 2 c2 + 1
+                        ldsm4(ks + SH::at(lane & 15, 2 * c2 + (lane >> 4)), kf);
+                        if constexpr (FP8) {
+                            // a thread gets 4 consecutive values of a key, which stand for k = 2 j, 2 j + 1,
+                            // 2 j + 8, 2 j + 9 of the product (the queries are in the same order)
 #pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                uint32_t a[4] = {0u, 0u, 0u, 0u};
-                                if constexpr (NH == 1) {
-                                    a[0] = qf[2 * c2 + hc].x;
-                                    a[2] = qf[2 * c2 + hc].y;
-                                } else {
+                            for (int hc = 0; hc < 2; ++hc) {
+                                uint32_t a[4];
+                                e4m3x4_to_h2x2(kf[2 * hc], a[0], a[2]);
+                                e4m3x4_to_h2x2(kf[2 * hc + 1], a[1], a[3]);
+                                mma16816<CT>(acc[hc], a, qf[2 * c2 + hc].x, qf[2 * c2 + hc].y);
+                            }
+                        } else {
+                            mma16816<CT>(acc[c2 & 1], kf, qf[c2].x, qf[c2].y);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[0][k >> 1][k & 1] = acc[0][k] + acc[1][k];
+                } else {
+#pragma unroll
+                    for (int c2 = 0; c2 < (FP8 ? D / 32 : D / 16); ++c2) {
+                        uint32_t kf[4];
+                        if constexpr (FP8) {
+                            // matrices: keys 0-7 and 8-15 of chunks 2 c2 and 2 c2 + 1. A thread gets 4
+                            // consecutive values of a key; they stand for k = 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+                            // of the product (the queries below are read in the same order).
+                            ldsm4(ks + SH::at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c2 + (lane >> 4)), kf);
+#pragma unroll
+                            for (int hc = 0; hc < 2; ++hc) {
+                                uint32_t b00, b01, b10, b11;
+                                e4m3x4_to_h2x2(kf[2 * hc], b00, b01);
+                                e4m3x4_to_h2x2(kf[2 * hc + 1], b10, b11);
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
                                     const uint2 x = q_pair(16 * i + (lane >> 2), 2 * c2 + hc);
                                     const uint2 y = q_pair(16 * i + (lane >> 2) + 8, 2 * c2 + hc);
-                                    a[0] = x.x;
-                                    a[1] = y.x;
-                                    a[2] = x.y;
-                                    a[3] = y.y;
+                                    const uint32_t a[4] = {x.x, y.x, x.y, y.y};
+                                    mma16816<CT>(sc[i][0], a, b00, b01);
+                                    mma16816<CT>(sc[i][1], a, b10, b11);
                                 }
-                                mma16816<CT>(sc[i][0], a, b00, b01);
-                                mma16816<CT>(sc[i][1], a, b10, b11);
                             }
-                        }
-                    } else {
-                        ldsm4(ks + SH::at((lane & 7) + (lane >> 4) * 8, 2 * c2 + ((lane >> 3) & 1)), kf);
+                        } else {
+                            ldsm4(ks + SH::at((lane & 7) + (lane >> 4) * 8, 2 * c2 + ((lane >> 3) & 1)), kf);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            uint32_t a[4];
-                            ldsm4(q_s + q_at(16 * i + (lane & 15), 2 * c2 + (lane >> 4)), a);
-                            mma16816<CT>(sc[i][0], a, kf[0], kf[1]);
-                            mma16816<CT>(sc[i][1], a, kf[2], kf[3]);
+                            for (int i = 0; i < MT; ++i) {
+                                uint32_t a[4];
+                                ldsm4(q_s + q_at(16 * i + (lane & 15), 2 * c2 + (lane >> 4)), a);
+                                mma16816<CT>(sc[i][0], a, kf[0], kf[1]);
+                                mma16816<CT>(sc[i][1], a, kf[2], kf[3]);
+                            }
                         }
                     }
                 }
@@ -359,13 +392,13 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                 for (int i = 0; i < NH; ++i) {
                     top[i] = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < (NARROW ? 1 : 2); ++n)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            float &x = sc[i >> 1][n][2 * (i & 1) + k];
+                            float &x = NARROW ? sc[0][k][i] : sc[i >> 1][n][2 * (i & 1) + k];
                             x *= factor[i];
                             if (!whole) {
-                                const int key = key0 + 8 * n + 2 * (lane & 3) + k;
+                                const int key = key0 + (NARROW ? 8 * k + (lane >> 2) : 8 * n + 2 * (lane & 3) + k);
                                 if (key > upto[i] || key <= after[i]) x = -INFINITY;
                             }
                             top[i] = fmaxf(top[i], x);
@@ -377,8 +410,8 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                 bool grew = false;
 #pragma unroll
                 for (int i = 0; i < NH; ++i) {
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+#pragma unroll
+                    for (int x = LANE0; x < LANE1; x *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], x));
                     grew |= top[i] > m[i] + 8.f;
                 }
                 if (__any_sync(0xFFFFFFFFu, grew)) {
@@ -389,26 +422,35 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                         m[i] = now;
                         l[i] *= f;
 #pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            o[i >> 1][n][2 * (i & 1)] *= f;
-                            o[i >> 1][n][2 * (i & 1) + 1] *= f;
+                        for (int n = 0; n < OT; ++n) {
+                            o[NARROW ? 0 : i >> 1][n][NARROW ? i : 2 * (i & 1)] *= f;
+                            o[NARROW ? 0 : i >> 1][n][NARROW ? 2 + i : 2 * (i & 1) + 1] *= f;
                         }
                     }
                 }
 
                 // ---- weights, rounded to the values' 16-bit type for the product; the sum takes them unrounded
                 uint32_t pf[MT][4];
-                if constexpr (NH == 1) pf[0][1] = pf[0][3] = 0u;  // (no rows there)
 #pragma unroll
                 for (int i = 0; i < NH; ++i) {
                     const float mm = m[i] == -INFINITY ? 0.f : m[i];
+                    if constexpr (NARROW) {
+                        sc[0][0][i] = ex2(sc[0][0][i] - mm);
+                        sc[0][1][i] = ex2(sc[0][1][i] - mm);
+                        l[i] += sc[0][0][i] + sc[0][1][i];
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float a = ex2(sc[i >> 1][n][2 * (i & 1)] - mm);
-                        const float b = ex2(sc[i >> 1][n][2 * (i & 1) + 1] - mm);
-                        l[i] += a + b;
-                        pf[i >> 1][2 * n + (i & 1)] = pack2<CT>(a, b);
+                        for (int n = 0; n < 2; ++n) {
+                            const float a = ex2(sc[i >> 1][n][2 * (i & 1)] - mm);
+                            const float b = ex2(sc[i >> 1][n][2 * (i & 1) + 1] - mm);
+                            l[i] += a + b;
+                            pf[i >> 1][2 * n + (i & 1)] = pack2<CT>(a, b);
+                        }
                     }
+                }
+                if constexpr (NARROW) {  // keys by rows -> rows by keys
+                    pf[0][0] = transpose8(pack2<CT>(sc[0][0][0], sc[0][0][1]));
+                    pf[0][1] = transpose8(pack2<CT>(sc[0][1][0], sc[0][1][1]));
                 }
 
                 // ---- values
@@ -424,12 +466,20 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                             uint32_t e0, e1, d0, d1;
                             e4m3x4_to_h2x2(__byte_perm(vf[2 * hc], 0, 0x3120), e0, d0);
                             e4m3x4_to_h2x2(__byte_perm(vf[2 * hc + 1], 0, 0x3120), e1, d1);
+                            if constexpr (NARROW) {  // rows 0-7 of the product: even values, 8-15: odd ones
+                                const uint32_t a[4] = {e0, d0, e1, d1};
+                                mma16816<CT>(o[0][c + hc], a, pf[0][0], pf[0][1]);
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                mma16816<CT>(o[i][2 * (c + hc)], pf[i], e0, e1);
-                                mma16816<CT>(o[i][2 * (c + hc) + 1], pf[i], d0, d1);
+                                for (int i = 0; i < MT; ++i) {
+                                    mma16816<CT>(o[i][2 * (c + hc)], pf[i], e0, e1);
+                                    mma16816<CT>(o[i][2 * (c + hc) + 1], pf[i], d0, d1);
+                                }
                             }
                         }
+                    } else if constexpr (NARROW) {
+                        const uint32_t a[4] = {vf[0], vf[2], vf[1], vf[3]};
+                        mma16816<CT>(o[0][c / 2], a, pf[0][0], pf[0][1]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
@@ -447,12 +497,18 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
             float *mine = reinterpret_cast<float *>(ring_ptr + warp * kRowsRing);
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
-                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-                const int r = 8 * i + (lane >> 2);
-                if ((lane & 3) == 0) row_ml[warp][r] = make_float2(m[i], l[i]);
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
+                for (int x = LANE0; x < LANE1; x *= 2) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], x);
+                const int r = row_of(i);
+                if ((lane & (LANE1 - LANE0)) == 0) row_ml[warp][r] = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int n = 0; n < OT; ++n) {
+                    if constexpr (NARROW) {  // o[0][n][k]: value lane / 4 + 8 (k / 2) of 16 (FP8: 2 (lane / 4) + k / 2), row k % 2
+                        const int c = lane >> 2;
+                        mine[r * OS + 16 * n + (FP8 ? 2 * c : c)] = o[0][n][i];
+                        mine[r * OS + 16 * n + (FP8 ? 2 * c + 1 : c + 8)] = o[0][n][2 + i];
+                        continue;
+                    }
                     const float2 v = make_float2(o[i >> 1][n][2 * (i & 1)], o[i >> 1][n][2 * (i & 1) + 1]);
                     if constexpr (FP8) {  // tile 2 c + h holds values 16 c + 2 col + h
                         mine[r * OS + 16 * (n >> 1) + 4 * (lane & 3) + (n & 1)] = v.x;
