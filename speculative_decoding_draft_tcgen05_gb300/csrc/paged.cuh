@@ -112,10 +112,11 @@ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const Page
     return (s.n * p.group + R - 1) / R;
 }
 
-// The items' costs (units + C) in order (sequence, head, row tile) are split
-// evenly: boundary c of G lies at total * c / G, moved to the item's start
-// where it falls into the C, and CTA c takes what is between boundaries c and
-// c + 1. G is the grid, or the sum where that is less. Every CTA works this out
+// The items' costs (units + C) of a lane's heads in order (sequence, head, row
+// tile) are split evenly over its CTAs: boundary c of G lies at total * c / G,
+// moved to the item's start where it falls into the C, and the lane's CTA c
+// takes what is between boundaries c and c + 1. G is its CTAs, or the sum
+// where that is less. Every CTA works this out
 // for itself from the lengths on the device: the launch needs nothing from the
 // host, and a captured graph stays valid when they change. (C: 32 ragged
 // sequences of 500 to 7000 keys took 119 us with C = 0, 111 with 2, 102 with 5
@@ -124,6 +125,7 @@ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const Page
 struct PagedPlan {
     int64_t total, begin, end;
     int ctas;      // G
+    int lane0, cta;  // the lane's first CTA and this one, numbered lane by lane (an idle CTA beyond them: its block)
     int b;         // sequence of `begin`
     int kvh, off;  // the head that it falls into, and the offset within the head
     PagedSeq s;    // the sequence
@@ -154,11 +156,14 @@ __device__ __forceinline__ int paged_cost_warp(const AttendParams &p, const Page
     return __reduce_add_sync(0xFFFFFFFFu, u);
 }
 
-// This CTA's share of `total`.
-__device__ __forceinline__ void paged_share(PagedPlan &plan, int64_t total)
+// This CTA's share of `total`, its lane's costs.
+__device__ __forceinline__ void paged_share(const AttendParams &p, PagedPlan &plan, int64_t total)
 {
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    const int c = blockIdx.x;
+    const int G = static_cast<int>(min(static_cast<int64_t>(p.lane_ctas), total));
+    const int c = static_cast<int>(blockIdx.x) / p.lanes, lane = static_cast<int>(blockIdx.x) - c * p.lanes;
+    const bool idle = c >= p.lane_ctas;
+    plan.lane0 = lane * p.lane_ctas;
+    plan.cta = idle ? static_cast<int>(blockIdx.x) : plan.lane0 + c;
     plan.total = total;
     plan.ctas = G;
     plan.begin = plan.end = 0;
@@ -209,20 +214,21 @@ __device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, Pag
         if (many) head = cost[lane];
     }
     if (warp > 0) return plan;
-    const int64_t mine = static_cast<int64_t>(head) * p.kv_heads;
+    const int64_t mine = static_cast<int64_t>(head) * p.lane_heads;
     int64_t upto = mine;
     for (int o = 1; o < p.B; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
         if (lane >= o) upto += v;
     }
-    paged_share(plan, __shfl_sync(0xFFFFFFFFu, upto, p.B - 1));
+    paged_share(p, plan, __shfl_sync(0xFFFFFFFFu, upto, p.B - 1));
     const unsigned at = __ballot_sync(0xFFFFFFFFu, lane < p.B && plan.begin < upto);
     plan.b = max(0, __ffs(at) - 1);  // (sequences without new tokens cost nothing and are passed over)
     plan.s = {__shfl_sync(0xFFFFFFFFu, s.t0, plan.b), __shfl_sync(0xFFFFFFFFu, s.n, plan.b), __shfl_sync(0xFFFFFFFFu, s.len, plan.b)};
     const int64_t off = plan.begin - __shfl_sync(0xFFFFFFFFu, upto - mine, plan.b);
     const int per_head = max(1, __shfl_sync(0xFFFFFFFFu, head, plan.b));
-    plan.kvh = static_cast<int>(paged_div(off, per_head));
-    plan.off = static_cast<int>(off - static_cast<int64_t>(plan.kvh) * per_head);
+    const int head_at = static_cast<int>(paged_div(off, per_head));
+    plan.off = static_cast<int>(off - static_cast<int64_t>(head_at) * per_head);
+    plan.kvh = head_at * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
     if (blockIdx.x == 0 && lane < p.B) paged_report(p, lane);
     return plan;
 }
@@ -267,7 +273,7 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
     }
     auto head_cost = [&](int b) { return kept ? cost[b] : paged_cost(p, paged_seq(p, b), cut); };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(head_cost(b)) * p.kv_heads;
+    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(head_cost(b)) * p.lane_heads;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -283,19 +289,20 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
         total += warp_sum[w];
     }
     PagedPlan made;
-    paged_share(made, total);
+    paged_share(p, made, total);
     if (made.begin < made.end ? (before <= made.begin && made.begin < before + mine) : tid == 0) {
         int64_t off = made.begin - before;
         int b = b0, per_head = 1;
         if (made.begin < made.end)
             for (; b < b1; ++b) {
                 per_head = head_cost(b);
-                if (off < static_cast<int64_t>(per_head) * p.kv_heads) break;
-                off -= static_cast<int64_t>(per_head) * p.kv_heads;
+                if (off < static_cast<int64_t>(per_head) * p.lane_heads) break;
+                off -= static_cast<int64_t>(per_head) * p.lane_heads;
             }
         made.b = b;
-        made.kvh = made.begin < made.end ? static_cast<int>(paged_div(off, per_head)) : 0;
-        made.off = static_cast<int>(off - static_cast<int64_t>(made.kvh) * per_head);
+        const int at = made.begin < made.end ? static_cast<int>(paged_div(off, per_head)) : 0;
+        made.off = static_cast<int>(off - static_cast<int64_t>(at) * per_head);
+        made.kvh = at * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
         made.s = paged_seq(p, min(b, p.B - 1));
         plan = made;
     }
@@ -367,8 +374,9 @@ struct PagedWalk {
         if (!more) return false;
         if (++pc.rt == nrt) {
             pc.rt = 0;
-            if (++pc.kvh == p.kv_heads) {
-                pc.kvh = 0;
+            pc.kvh += p.lanes;
+            if (pc.kvh >= p.kv_heads) {
+                pc.kvh %= p.lanes;
                 do {
                     ++pc.b;
                     pc.s = paged_seq(p, pc.b);
@@ -398,7 +406,7 @@ __device__ __forceinline__ int2 paged_sharers(const PagedPlan &plan, const Paged
     const int64_t low = w.at + k.C + 1, high = w.at + k.C + w.pc.it.units;  // low <= boundary < high
     const int64_t first = paged_quot(low * plan.ctas + plan.total - 1, plan.total);  // smallest c with total * c / G >= low
     const int64_t end = paged_quot(high * plan.ctas + plan.total - 1, plan.total);   // smallest c with total * c / G >= high
-    return make_int2(static_cast<int>(first - 1), static_cast<int>(end - first + 1));
+    return make_int2(plan.lane0 + static_cast<int>(first - 1), static_cast<int>(end - first + 1));
 }
 
 // Slot of part i of the item that CTA c0 begins.

@@ -70,11 +70,12 @@ struct AttendParams {
     int64_t table_stride;
     int table_cols, num_pages;
     int B, tokens, kv_heads, group, page;  // group = query heads per key/value head
+    int lanes, lane_heads, lane_ctas;      // heads walked in step, heads and CTAs of each (set_lanes())
     FastDiv by_group, by_page;
     int causal, window;            // window 0: none
     float scale_log2;              // score scale * log2(e) (* the keys' scale)
     float v_scale;
-    // Workspace: CTA c's partial results in slots 2c (a piece that continues an
+    // Workspace: CTA c's (PagedPlan::cta) partial results in slots 2c (a piece that continues an
     // earlier CTA's item) and 2c + 1 (one that a later CTA continues). An item
     // split over at most kTicketParts CTAs is joined by whichever finishes last
     // (a counter per warp's rows, at the CTA that begins the item, zero between
@@ -84,8 +85,24 @@ struct AttendParams {
     float2 *part_ml;   // [2 * grid][rows] running maximum (log2) and sum
     int4 *merge;       // [2 * grid]: first token row, first row, rows, key/value head | CTAs (0: nothing to do)
     unsigned *ticket;  // [grid][kTicketWarps]
+    int merge_early;   // the merge kernel lets the next launch begin at once, not only when the parts are written
     int *err;
 };
+
+// Key/value heads are dealt to `lanes` groups of `lane_ctas` CTAs: group l takes heads l, l + lanes, .. and its
+// CTAs split their keys, all groups in the same way, so that the CTAs of a wave read the same keys of adjacent
+// heads, which lie next to each other where a slot holds all heads (128 single tokens, 8 heads, 8-bit cache: 88 us,
+// 101 with the heads one after the other; 16-bit 154 and 160; heads of 64 values, 8-bit 60 and 105). The most
+// lanes up to `most` that divide the heads and leave no more than 1/64 of the grid idle. The many-row kernel has
+// one: its row tiles, one after the other, find a head's keys in L2 (2048 rows of 40 heads: 416 us, 429 dealt out).
+inline void set_lanes(AttendParams &p, int grid, int most)
+{
+    p.lanes = 1;
+    for (int k = 2; k <= most && k <= grid; ++k)
+        if (p.kv_heads % k == 0 && grid % k <= grid / 64) p.lanes = k;
+    p.lane_heads = p.kv_heads / p.lanes;
+    p.lane_ctas = grid / p.lanes;
+}
 
 // Rows of a work item and keys of a work unit of the two kernels.
 constexpr int kRowsUnit = 64;    // few rows: 8, 16 or 32 rows, units of 64 keys

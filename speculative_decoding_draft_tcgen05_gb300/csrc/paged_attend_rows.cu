@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
             __syncthreads();
             const bool begins = pc.a == 0, split = walk.split();
             const int2 share = split ? paged_sharers(plan, walk, cut) : make_int2(0, 1);
-            const int64_t mine_slot = paged_slot(share.x, static_cast<int>(blockIdx.x) - share.x);
+            const int64_t mine_slot = paged_slot(share.x, plan.cta - share.x);
             auto finish = [&](int r, int c, const float(&acc)[8], float M, float L) {
                 const int rr = pc.rt * R + r, t = p.by_group.div(rr), hd = pc.kvh * p.group + rr - t * p.group;
                 const float inv = L > 0.f || L != L ? p.v_scale / L : 0.f;
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
         }
     }
     if (tid == 0) {
-        p.merge[2 * blockIdx.x] = merge0;
-        p.merge[2 * blockIdx.x + 1] = merge1;
+        p.merge[2 * plan.cta] = merge0;
+        p.merge[2 * plan.cta + 1] = merge1;
     }
 }
 
@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
     __shared__ float sums[kMergeWarps];
     __shared__ __align__(16) float part[kMergeWarps][D];  // (read and written in pieces of F)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_trigger();
+    if (p.merge_early) pdl_trigger();
     pdl_wait();
+    if (!p.merge_early) pdl_trigger();
     int entries = 0;
     for (int from = 0; from < G; from += kMergeWarps * 32) {  // the list, without its empty entries
         const int c = from + tid;

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
 
             if (!(e.alt && i == 1)) {
                 T *const dst = static_cast<T *>(p.out) + e.tok * p.o_ts + e.head * p.o_hs;
-                const int mine = static_cast<int>(blockIdx.x) - share.x;  // this CTA's part of a split item
+                const int mine = plan.cta - share.x;  // this CTA's part of a split item
                 auto own = [&](int k, float (&v)[32]) {  // 32 values of this row's result
                     uint32_t o[32];
                     tmem_load32(o_col + k, o);
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
             }
         }
         if (tid == 0) {
-            p.merge[2 * blockIdx.x] = merge0;
-            p.merge[2 * blockIdx.x + 1] = merge1;
+            p.merge[2 * plan.cta] = merge0;
+            p.merge[2 * plan.cta + 1] = merge1;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(FP8)));
