@@ -253,11 +253,15 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal
                     e = max(-100, min(100, e));
                     const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
-                    v = make_uint4(pack2<CT>(f[0] * up, f[1] * up), pack2<CT>(f[2] * up, f[3] * up),
-                                   pack2<CT>(f[4] * up, f[5] * up), pack2<CT>(f[6] * up, f[7] * up));
                     if (c == 0) q_undo[r] = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
+                    // of every 16 values 0, 1, 4, 5, 8, .. are k = 0 .. 7 of the product and the others 8 .. 15 (see the scores)
+                    *reinterpret_cast<uint2 *>(smem + q_at(r, c & ~1) + 8 * (c & 1)) =
+                        make_uint2(pack2<CT>(f[0] * up, f[1] * up), pack2<CT>(f[4] * up, f[5] * up));
+                    *reinterpret_cast<uint2 *>(smem + q_at(r, c | 1) + 8 * (c & 1)) =
+                        make_uint2(pack2<CT>(f[2] * up, f[3] * up), pack2<CT>(f[6] * up, f[7] * up));
+                } else {
+                    *reinterpret_cast<uint4 *>(smem + q_at(r, c)) = v;
                 }
-                *reinterpret_cast<uint4 *>(smem + q_at(r, c)) = v;
             }
             __syncthreads();
 
@@ -281,17 +285,12 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
             least_upto = __reduce_min_sync(0xFFFFFFFFu, least_upto);
             most_after = __reduce_max_sync(0xFFFFFFFFu, most_after);
 
-            // An 8-bit cache's products take a query row's values 16 c + 4 (lane % 4) .. + 3 (see below).
-            auto q_pair = [&](int r, int c) {
-                return *reinterpret_cast<const uint2 *>(smem + q_at(r, 2 * c + ((lane & 3) >> 1)) + 8 * (lane & 1));
-            };
             uint2 qf[NARROW ? D / 16 : 1];  // up to 8 rows stay in registers
             if constexpr (NARROW) {
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)
-                    qf[c] = FP8 ? q_pair(lane >> 2, c)
-                                : make_uint2(*reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c) + 4 * (lane & 3)),
-                                             *reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c + 1) + 4 * (lane & 3)));
+                    qf[c] = make_uint2(*reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c) + 4 * (lane & 3)),
+                                       *reinterpret_cast<const uint32_t *>(smem + q_at(lane >> 2, 2 * c + 1) + 4 * (lane & 3)));
             }
 
             float o[MT][OT][4];
@@ -365,9 +364,8 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                                 e4m3x4_to_h2x2(kf[2 * hc + 1], b10, b11);
 #pragma unroll
                                 for (int i = 0; i < MT; ++i) {
-                                    const uint2 x = q_pair(16 * i + (lane >> 2), 2 * c2 + hc);
-                                    const uint2 y = q_pair(16 * i + (lane >> 2) + 8, 2 * c2 + hc);
-                                    const uint32_t a[4] = {x.x, y.x, x.y, y.y};
+                                    uint32_t a[4];
+                                    ldsm4(q_s + q_at(16 * i + (lane & 15), 2 * (2 * c2 + hc) + (lane >> 4)), a);
                                     mma16816<CT>(sc[i][0], a, b00, b01);
                                     mma16816<CT>(sc[i][1], a, b10, b11);
                                 }
