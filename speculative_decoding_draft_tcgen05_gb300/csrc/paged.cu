@@ -297,9 +297,10 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     auto short_call = [&](int unit, int item_rows, int ctas) {
         return most_units(unit) * ((most_rows + item_rows - 1) / item_rows) * p.B * p.kv_heads <= ctas;
     };
-    // The few-row kernel keeps up to 32 rows of accumulators in registers and streams the keys at the memory's
-    // rate (32 ragged sequences of 32 rows: 102 us, by the other 124); beyond that it would read them once per
-    // 32 rows, where the tensor-memory kernel takes 256 (64 rows of 40 heads: 94 us, by this one 157).
+    // The few-row kernel keeps up to 32 rows of accumulators in registers and streams the keys near the memory's rate
+    // (32 ragged sequences of 32 rows: 98 us, 84 with an 8-bit cache; by the other 107 and 115; of 4 rows: 86 and
+    // 105). Beyond 32 it would read them once per 32 rows, where the tensor-memory kernel takes 256 (64 rows: 106 us,
+    // by this one 158).
     if (most_rows > 32) {
         CUtensorMap tm_k, tm_v;
         const int box = dfl::tile_box_rows(p.page), bytes = fp8 ? 1 : 2;
@@ -315,6 +316,8 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
         p.merge_early = short_call(dfl::kTileUnit, rows, grid);
         e = dfl::launch_attend_tile(p, tm_k, tm_v, h->cfg.head_dim, h->cfg.dtype, fp8, grid, s);
     } else {
+        // (With up to 8 rows by the variant for 16: 128 single tokens of an 8-bit cache 95 us, not 88; up to 16 by the
+        // one for 32: 80 us, not 60.)
         rows = most_rows <= 8 ? 8 : (most_rows <= 16 ? 16 : 32);
         grid = (rows <= 16 ? 3 : 2) * h->num_sms;
         dfl::set_lanes(p, grid, p.kv_heads);

@@ -118,10 +118,11 @@ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const Page
 // takes what is between boundaries c and c + 1. G is its CTAs, or the sum
 // where that is less. Every CTA works this out
 // for itself from the lengths on the device: the launch needs nothing from the
-// host, and a captured graph stays valid when they change. (C: 32 ragged
-// sequences of 500 to 7000 keys took 119 us with C = 0, 111 with 2, 102 with 5
-// in the few-row kernel, seven windowed chunks 56 and 50 us with C = 0 and 4 in
-// the other.)
+// host, and a captured graph stays valid when they change. (C, in
+// the few-row kernel: 32 ragged sequences of 32 rows and 500 to 7000 keys took
+// 112 us with C = 0, 102 with 5, 98 with 8, 101 with 14; 128 single tokens of an
+// 8-bit cache 92 us with 0, 88 with 5, 89 with 8. In the other kernel seven
+// windowed chunks took 55 us with 0, 44 with 4.)
 struct PagedPlan {
     int64_t total, begin, end;
     int ctas;      // G

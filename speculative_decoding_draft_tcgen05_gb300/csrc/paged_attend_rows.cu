@@ -9,8 +9,9 @@ namespace dfl {
 namespace {
 
 constexpr int kRowsThreads = 128;  // 4 warps
-constexpr int kRowsCost = 5;       // units that starting an item costs
+constexpr int rows_cost(int R) { return R <= 16 ? 5 : 8; }  // units that starting an item costs
 constexpr int kRowsWarps = kRowsThreads / 32;
+// Bytes of a warp's ring: 3 (2) CTAs share an SM with it, and it holds 2 (3) steps of 16 keys of 128 16-bit values.
 template <int MT> constexpr int rows_ring() { return MT == 1 ? 16 * 1024 : 24 * 1024; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
@@ -130,9 +131,20 @@ constexpr int kRowsPad = 8;  // floats between merge rows
 //
 // For every key the rows of a group (query heads that share it, times the
 // new tokens) use the same copy in shared memory, so the cache is read once.
-// The limit is HBM: 2 * D * 2 bytes per key against 4 * D * rows operations,
+// Up to 8 rows are the products' columns (keys or values their rows): half the
+// matrix instructions and accumulators that rows of 16 would take.
+//
+// The floor is HBM: 2 * D * 2 bytes per key against 4 * D * rows operations,
 // 32 op/byte at 32 rows, which mma.sync sustains; the tensor memory path would
-// leave 3/4 or more of its 128-row tiles empty here.
+// leave 3/4 or more of its 128-row tiles empty here. What keeps it from the
+// floor is the chain of each warp's step (copy wait, scores, weights, values)
+// with 8 or 12 warps an SM, and the start of each piece. Heads of 128 values,
+// 8 of them, a GB300 that copies 6.8 TB/s:
+//   128 sequences, 1 token x 4 heads, 200 to 3800 keys   16 bit 154 us 6.6 TB/s, 8 bit 88 us 5.8 TB/s
+//   32 sequences, 8 tokens x 4 heads, 500 to 7000 keys   16 bit  98 us 5.4 TB/s, 8 bit 84 us 3.2 TB/s
+//   1 sequence, 8 tokens x 4 heads, 2041 keys            13.5 us with the merge, all latency
+// Three CTAs an SM where their registers allow it (R <= 16): the first line
+// takes 160 and 90 us with two, and 8-bit heads of 64 values 78 us, not 59.
 // ---------------------------------------------------------------------------
 template <int D, int R, typename QT, bool FP8>
 __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_kernel(const __grid_constant__ AttendParams p)
@@ -158,7 +170,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
 
     pdl_trigger();
     pdl_wait();
-    constexpr PagedCut cut = {R, kRowsUnit, kRowsCost};
+    constexpr PagedCut cut = {R, kRowsUnit, rows_cost(R)};
     const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, reinterpret_cast<int *>(smem));
     PagedWalk walk;
     walk.start(p, plan, cut);
@@ -602,7 +614,8 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
 // row's parts in turn, several in flight, and their sums are added in shared
 // memory. Which warp adds which parts is fixed, so the result does not depend
 // on the order in which anything finished. A call with few rows is all
-// latency here: two dependent reads (the list; maxima and parts together).
+// latency here: two dependent reads (the list; maxima and parts together), some
+// 2.5 us at the end of a call.
 // Value d of row r of a part is at r * row_step + d / 4 * value_step + d % 4.
 constexpr int kMergeWarps = 8, kMergeMost = 1024;
 
