@@ -364,6 +364,18 @@ def test_attend_wide_groups(pkg, heads, cache):
     s.check(s.rows(heads), window=33)
 
 
+@pytest.mark.parametrize("cache", [None, FP8])
+@pytest.mark.parametrize("heads,kv_heads", [(5, 5), (14, 7), (24, 12), (80, 40), (500, 500), (97, 97)])
+def test_attend_numbers_of_key_heads(pkg, heads, kv_heads, cache):
+    """Key heads that divide the grid, leave CTAs idle, are walked one after the other, or outnumber the CTAs; items
+    of one CTA, of a few and of many."""
+    s = Paged(pkg, [1, 4, 0, 2], [700, 90, 33, 4], heads=heads, kv_heads=kv_heads, d=64, dtype=BF16, cache=cache, seed=kv_heads)
+    s.check(s.rows(heads))
+    s.check(s.rows(heads), window=70)
+    long = Paged(pkg, [2], [6000], heads=heads, kv_heads=kv_heads, d=64, dtype=FP16, cache=cache, seed=kv_heads + 1)
+    long.check(long.rows(heads))
+
+
 def test_attend_masked_keys_may_be_anything(pkg):
     """NaN and infinite keys at places that some tokens do not see leave those tokens alone; a value there must be finite."""
     for new in (6, 90):
