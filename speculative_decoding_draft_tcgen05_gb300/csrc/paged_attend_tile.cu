@@ -35,8 +35,9 @@ struct TileShape {
     static constexpr uint32_t O_COL = 256;              // TMEM: scores 0-127 | 128-255, results from 256
 };
 
+template <int STAGES>
 struct TileBars {
-    uint64_t full[10], empty[10];  // ring of tiles
+    uint64_t full[STAGES], empty[STAGES];  // ring of tiles
     uint64_t raw_full[4], raw_empty[4];  // ring of 8-bit tiles
     uint64_t q_full[2];            // a stream's queries are in shared memory
     uint64_t q_empty;              // the piece is done with the queries' place
@@ -298,9 +299,14 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
     constexpr PagedCut cut = {R, U, kTileCost};
     const AttendParams &p = tp.a;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ TileBars bars;
+    __shared__ TileBars<S> bars;
     __shared__ float2 x_ml[128];
-    __shared__ uint8_t q_exp[FP8 ? 256 : 1];  // a query row was scaled by 2^(108 - this)
+    // 8-bit cache: a query row was scaled by 2^(108 - this). Pieces take the two slots in turn, since the streams read a
+    // piece's before its first weights, while the queries' place (q_empty) is free once its last scores are there: in a
+    // piece of one tile that is earlier, and the next piece's queries may come while the streams still finish the piece
+    // before. Two are enough: a slot is written again when the scores of the piece between are complete, and those are
+    // issued after the first weights of the piece that read it.
+    __shared__ uint8_t q_exp[2][FP8 ? 256 : 1];
     uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t q_s = smem_u32(smem), ring = q_s + 2 * SH::TILE;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
         const int i = warp >> 2, row = tid & 127;
         const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
         const uint32_t s_col = tmem + lane_base + 128u * i, o_col = tmem + lane_base + SH::O_COL + D * i;
-        uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
+        uint32_t s_phase = 0, o_phase = 0, x_phase = 0, q_slot = 0;
         int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;
 
         // This thread's row of a piece.
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 if (!(ok = warp_wait(&bars.s_full[i], s_phase, ab))) break;
                 s_phase ^= 1;
                 tc_fence_after_sync();
-                if (FP8 && t == 0) factor *= __uint_as_float((19u + q_exp[c.r]) << 23);
+                if (FP8 && t == 0) factor *= __uint_as_float((19u + q_exp[q_slot][c.r]) << 23);
                 uint32_t sr[128];
                 tmem_load128<FP8>(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
@@ -462,6 +468,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
             const unsigned written = by_ticket ? paged_written(ticket, lane) : 0;  // (on its way while the products end)
             more = walk.next(p, cut);
             if (more) c = row_of(walk.pc);
+            q_slot ^= 1;
             if (e.steps > 0) {
                 if (!(ok = warp_wait(&bars.o_full[i], o_phase, ab))) break;
                 o_phase ^= 1;
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
             // The piece's queries, once the one before is done with their place; rows past the item's are zero.
             auto load_q = [&](const PagedPiece &pc) {
                 if (!(ok = warp_wait(&bars.q_empty, q_phase, ab))) return;
-                q_phase ^= 1;
+                q_phase ^= 1;  // (from 1: the first piece's slot of q_exp is 0)
                 const int r0 = pc.rt * R, rows = min(R, pc.s.n * p.group - r0);
                 constexpr int kQPieces = (128 * (D / 8) + 32 * kLoadWarps - 1) / (32 * kLoadWarps) * (32 * kLoadWarps);
                 constexpr int CH = D / 8;  // 16-byte pieces of a row
@@ -752,7 +759,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                             if (row < 128) {
                                 *at = make_uint4(pack2<CT>(f[0].x * up, f[0].y * up), pack2<CT>(f[1].x * up, f[1].y * up),
                                                  pack2<CT>(f[2].x * up, f[2].y * up), pack2<CT>(f[3].x * up, f[3].y * up));
-                                if (c == 0) q_exp[128 * i + row] = static_cast<uint8_t>(e + 100);
+                                if (c == 0) q_exp[q_phase][128 * i + row] = static_cast<uint8_t>(e + 100);
                             }
                         }
                         fence_async_proxy();
