@@ -136,7 +136,8 @@ dflash_status dflash_paged_append(dflash_paged_handle h, const dflash_paged_cach
  * sum of exp(score), -inf for such a token. out must not overlap q.
  * Sums, maxima and products accumulate in fp32; the softmax weights are
  * rounded to the cache's 16-bit type (fp16 for E4M3 caches) for the matrix
- * product. What is stored at places >= lens[b], and on pages that hold no key
+ * product; in fp16 a weight below 2^-32 of the row's largest counts as zero
+ * there. What is stored at places >= lens[b], and on pages that hold no key
  * that some token of the call sees, is never used and may be anything (those
  * pages need no entry in the table). The values (not the keys) at the other
  * places have to be finite for the tokens that do not see them too: their

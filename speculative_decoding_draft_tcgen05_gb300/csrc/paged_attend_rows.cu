@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                         }
                 }
                 // A row's maximum moves only when it grew by more than 2^8 (fp32 sums and the 16-bit
-                // weights stand a stale one: the weights are at most 256): the accumulator is then
+                // weights stand a stale one): the accumulator is then
                 // hardly ever rescaled. The first unit sets it.
                 bool grew = false;
 #pragma unroll
@@ -439,11 +439,11 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                     }
                 }
 
-                // ---- weights, rounded to the values' 16-bit type for the product; the sum takes them unrounded
+                // ---- weights, rounded to the values' 16-bit type for the product (weight_lift()); the sum takes them unrounded
                 uint32_t pf[MT][4];
 #pragma unroll
                 for (int i = 0; i < NH; ++i) {
-                    const float mm = m[i] == -INFINITY ? 0.f : m[i];
+                    const float mm = m[i] == -INFINITY ? 0.f : m[i] - weight_lift<CT>();
                     if constexpr (NARROW) {
                         sc[0][0][i] = ex2(sc[0][0][i] - mm);
                         sc[0][1][i] = ex2(sc[0][1][i] - mm);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
 #pragma unroll
                 for (int x = LANE0; x < LANE1; x *= 2) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], x);
                 const int r = row_of(i);
-                if ((lane & (LANE1 - LANE0)) == 0) row_ml[warp][r] = make_float2(m[i], l[i]);
+                if ((lane & (LANE1 - LANE0)) == 0) row_ml[warp][r] = make_float2(m[i] - weight_lift<CT>(), l[i]);
 #pragma unroll
                 for (int n = 0; n < OT; ++n) {
                     if constexpr (NARROW) {  // o[0][n][k]: value lane / 4 + 8 (k / 2) of 16 (FP8: 2 (lane / 4) + k / 2), row k % 2

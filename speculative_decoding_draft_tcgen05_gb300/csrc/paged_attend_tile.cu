@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                     }
                     tmem_store_wait();
                 }
-                // weights, rounded to 16 bits for the product; the sum takes them unrounded
-                const float off = m == -INFINITY ? 0.f : m;
+                // weights, rounded to 16 bits for the product (weight_lift()); the sum takes them unrounded
+                const float off = m == -INFINITY ? 0.f : m - weight_lift<CT>();
                 const float2 by = make_float2(factor, factor), less = make_float2(-off, -off);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -455,6 +455,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 l += both.x + both.y;
             }
             if (!ok) break;
+            m -= weight_lift<CT>();
 
             const Row e = c;
             const bool begins = walk.pc.a == 0, split = walk.split(), joined = e.alt && walk.pc.e - walk.pc.a > 1;

@@ -1,10 +1,12 @@
 """The attention block's operators where the order of the kernels' steps, the
 range of the number formats or the limits of the arguments matter. Reference
 and tolerances as in test_gpu_paged.py unless a test says otherwise."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_paged import KINDS, Paged, pkg  # noqa: F401  (pkg is a fixture)
+from test_gpu_paged import FP16, FP8, KINDS, UNIT, Paged, pkg  # noqa: F401  (pkg is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,36 @@ def test_attend_many_pieces_of_a_cta(pkg, new, lens, d, dtype, cache):  # noqa: 
     out = s.check(q)
     for _ in range(5):
         assert torch.equal(s.layer.attend(s.cache, s.batch, q), out)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("heads,new,batch,d", [
+    (2, 1, 228, 64), (2, 8, 228, 128), (8, 4, 228, 64), (8, 8, 152, 128),  # few rows: 1, 8, 16 and 32 an item
+    (2, 40, 76, 64), (2, 40, 76, 128), (8, 90, 76, 64), (8, 90, 76, 128)])  # many: one and two streams' rows
+def test_attend_light_keys_of_a_long_context(pkg, heads, new, batch, d, dtype, cache):  # noqa: F811
+    """100,000 keys of weight e^-18 = 2^-26 beside a few of weight 1, which alone have no value: what the light ones
+    add up to is not lost. As many sequences as the items are walked whole, all over the same pages."""
+    keys, page, kind = 100_000, 64, dtype if cache is None else cache
+    heavy = [0, 16, 32, 48, 128]  # a key for each of the few-row kernel's warps and the many-row kernel's streams
+    pages = -(-keys // page)
+    k, v = torch.zeros(pages, page, 2, d, device="cuda"), torch.full((pages, page, 2, d), 4.0, device="cuda")
+    for x in heavy:
+        k[x // page, x % page, :, 0], v[x // page, x % page] = 12.0, 0.0
+    k, v = k.to(kind), v.to(kind)  # (exact in every type)
+    layer = pkg.PagedAttention(heads=heads, kv_heads=2, head_dim=d, page_size=page, dtype=dtype, cache_dtype=kind, max_batch=batch)
+    b = pkg.PagedBatch(torch.arange(batch + 1, device="cuda", dtype=torch.int32) * new,
+                       torch.full((batch,), keys, device="cuda", dtype=torch.int32),
+                       torch.arange(pages, device="cuda", dtype=torch.int32).expand(batch, -1), max_tokens=new)
+    q = torch.zeros(batch * new, heads, d, device="cuda", dtype=dtype)
+    q[..., 0] = 12.0
+    out = layer.attend(pkg.PagedCache(k, v), b, q, causal=False, scale=0.125)
+    layer.sync_status()
+    light = (keys - len(heavy)) * math.exp(-18.0)
+    want = 4.0 * light / (len(heavy) + light)
+    # fp16 weights are rounded at 2^-14 * 2^-7 of the largest one and below to steps of 2^-24 * 2^-7, above (and in bf16)
+    # to their 11 (8) bits; fp32 scores of 18 are off by 18 * 2^-24 * log2(e) at most, and fp32 sums near 1 by 1e-4 (a
+    # weight of 2^-26 itself is lost in one, a thread adds some thousands); the result is rounded once
+    unit = UNIT[dtype]
+    small = 4.0 * keys * 2.0 ** -32 / len(heavy) if cache is FP8 or dtype is FP16 else unit * want
+    tol = small + 1e-4 * want + unit * want + 2.0 ** -25
+    assert float((out.double() - want).abs().max()) <= tol
