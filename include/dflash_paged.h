@@ -133,7 +133,8 @@ dflash_status dflash_paged_append(dflash_paged_handle h, const dflash_paged_cach
  * <= its own; with window > 0 only those at places > its own - window. Head j
  * reads key/value head j / (heads / kv_heads). A token that sees no key gets
  * zeros. lse [tokens, heads] fp32 (optional): the natural logarithm of the
- * sum of exp(score), -inf for such a token. out must not overlap q.
+ * sum of exp(score), -inf for such a token, NaN (like out) where a score is NaN
+ * or +inf. out must not overlap q.
  * Sums, maxima and products accumulate in fp32; the softmax weights are
  * rounded to the cache's 16-bit type (fp16 for E4M3 caches) for the matrix
  * product; in fp16 a weight below 2^-32 of the row's largest counts as zero

@@ -26,6 +26,13 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+// The natural logarithm of a row's sum, from its maximum (log2) and the sum taken against it: -inf where it sees no key
+// (both are -inf then), NaN where a score is NaN (the maximum passes those over, the sum does not) or +inf.
+__device__ __forceinline__ float row_lse(float max, float sum)
+{
+    return (max + lg2(sum)) * 0.69314718055994531f;
+}
+
 // Four e4m3 values -> two pairs of fp16 (exact).
 __device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t x, uint32_t &lo, uint32_t &hi)
 {

@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                                pack2<QT>(acc[4] * inv, acc[5] * inv), pack2<QT>(acc[6] * inv, acc[7] * inv));
                 if (c == 0 && p.lse)
                     p.lse[static_cast<int64_t>(s.t0 + t) * p.kv_heads * p.group + hd] =
-                        M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                        row_lse(M, L);
             };
             // a warp always takes the same rows, so the CTAs that share an item join them warp by warp
 #pragma unroll
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attend_merge_kernel(const __
                 pack2<QT>(a * inv, b * inv);
             if (tid == 0 && p.lse)
                 p.lse[static_cast<int64_t>(item.x + t) * p.kv_heads * p.group + hd] =
-                    M == -INFINITY ? -INFINITY : (M + lg2(total)) * 0.69314718055994531f;
+                    row_lse(M, total);
         }
         __syncthreads();
     }

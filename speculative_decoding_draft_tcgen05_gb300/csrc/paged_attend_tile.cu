@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 auto store_lse = [&](float M, float L) {
                     if (e.real && p.lse)
                         p.lse[static_cast<int64_t>(e.tok) * p.kv_heads * p.group + e.head] =
-                            M == -INFINITY ? -INFINITY : (M + lg2(L)) * 0.69314718055994531f;
+                            row_lse(M, L);
                 };
                 // Parts are laid out [value / 4][row]: a warp's rows are adjacent, so its accesses are whole lines.
                 auto part_at = [&](int64_t slot, int k) {

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_paged import FP16, FP8, KINDS, UNIT, Paged, pkg  # noqa: F401  (pkg is a fixture)
+from test_gpu_paged import BF16, FP16, FP8, KINDS, UNIT, Paged, pkg  # noqa: F401  (pkg is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,44 @@ def test_attend_light_keys_of_a_long_context(pkg, heads, new, batch, d, dtype, c
     small = 4.0 * keys * 2.0 ** -32 / len(heavy) if cache is FP8 or dtype is FP16 else unit * want
     tol = small + 1e-4 * want + unit * want + 2.0 ** -25
     assert float((out.double() - want).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("new,lens", [
+    ([4, 2], [60, 3]), ([2, 1], [900, 16]), ([8], [9000]),            # few rows: whole items, joined by counters and by the merge
+    ([70, 40], [70, 300]), ([60], [700]), ([200], [900]), ([64], [30000])])  # many rows
+def test_attend_lse_of_rows_that_are_not_numbers(pkg, new, lens, dtype, cache):  # noqa: F811
+    """A row whose every score is NaN has NaN results and a NaN logarithm, not that of a row that sees nothing."""
+    s = Paged(pkg, new, lens, heads=8, kv_heads=2, d=64, dtype=dtype, cache=cache, seed=sum(new))
+    q = s.rows(8)
+
+    def run():
+        lse = torch.full((s.tokens, 8), 7.0, device="cuda")
+        out = s.layer.attend(s.cache, s.batch, q, lse=lse)
+        s.layer.sync_status()
+        return out, lse
+    want, want_lse = run()
+    token, head = s.tokens // 2, 5
+    q[token, head, 3] = float("nan")
+    out, lse = run()
+    assert out[token, head].isnan().all() and lse[token, head].isnan()
+    here = torch.zeros(s.tokens, 8, dtype=torch.bool, device="cuda")
+    here[token, head] = True
+    assert torch.equal(out[~here], want[~here]) and torch.equal(lse[~here], want_lse[~here])
+
+
+@pytest.mark.parametrize("cache", [None, FP8])
+@pytest.mark.parametrize("new,lens", [([8, 1], [5, 64]), ([40, 1], [7, 1]), ([300], [10])])
+def test_attend_rows_that_see_nothing_exactly(pkg, new, lens, cache):  # noqa: F811
+    """Exactly a sequence's first new - length tokens see no key: zeros and -inf there, even for queries that are not
+    numbers, and ordinary results in all other rows."""
+    s = Paged(pkg, new, lens, heads=8, kv_heads=2, d=64, dtype=BF16, cache=cache, seed=3)
+    nothing = torch.cat([torch.arange(n) < n - L for n, L in zip(new, lens)]).cuda()
+    assert nothing.any() and not nothing.all()
+    q = s.rows(8)
+    for x in (q, torch.where(nothing[:, None, None], torch.full_like(q, float("nan")), q)):
+        lse = torch.full((s.tokens, 8), 7.0, device="cuda")
+        out = s.layer.attend(s.cache, s.batch, x, lse=lse)
+        s.layer.sync_status()
+        assert (out[nothing] == 0).all() and (lse[nothing] == -math.inf).all()
+        assert lse[~nothing].isfinite().all() and (out[~nothing] != 0).any(-1).all()
