@@ -74,7 +74,7 @@ typedef struct {
     int64_t table_stride;
     int32_t table_cols;
     int32_t batch;       /* 0 <= batch <= max_batch; 0 launches nothing */
-    int32_t tokens;      /* rows of q, k, v and out: >= cu_tokens[batch] */
+    int32_t tokens;      /* rows of q, k, v and out: >= cu_tokens[batch], <= 2^30, tokens * heads < 2^31 */
     int32_t max_tokens;  /* >= every new[b]; picks kernel and tile, the results do not depend on it */
 } dflash_paged_batch;
 

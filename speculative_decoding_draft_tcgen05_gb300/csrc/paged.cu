@@ -83,6 +83,8 @@ dflash_status check_call(dflash_paged_handle h, const dflash_paged_cache *c, con
         return paged_fail(DFLASH_ERR_INVALID_ARG, "batch must be in [0, max_batch = %lld] (got %lld)", h->cfg.max_batch, b->batch);
     if (b->tokens < 0 || b->max_tokens < 0)
         return paged_fail(DFLASH_ERR_INVALID_ARG, "tokens and max_tokens must be >= 0 (got %lld, %lld)", b->tokens, b->max_tokens);
+    if (b->tokens > 1 << 30)  // (places less a window of up to 2^30 stay in 32 bits)
+        return paged_fail(DFLASH_ERR_INVALID_ARG, "tokens must be at most 2^30 (got %lld)", b->tokens);
     if (static_cast<int64_t>(b->tokens) * h->cfg.heads >= (int64_t(1) << 31))
         return paged_fail(DFLASH_ERR_INVALID_ARG, "tokens * heads must be below 2^31 (got %lld * %lld)", b->tokens, h->cfg.heads);
     if (b->batch > 0 && (!b->cu_tokens || !b->lens || !b->page_table || b->table_cols < 1 || b->table_stride < 0))
@@ -295,7 +297,7 @@ extern "C" dflash_status dflash_paged_attend(dflash_paged_handle h, const dflash
     // CTAs would take the places of those that are still to come (a block of 8 after 2041 keys: 13.5 us a call, 14.3
     // without; 128 single tokens of 64-value heads: 110 us, 86 without).
     auto short_call = [&](int unit, int item_rows, int ctas) {
-        return most_units(unit) * ((most_rows + item_rows - 1) / item_rows) * p.B * p.kv_heads <= ctas;
+        return static_cast<double>(most_units(unit)) * ((most_rows + item_rows - 1) / item_rows) * p.B * p.kv_heads <= ctas;
     };
     // The few-row kernel keeps up to 32 rows of accumulators in registers and streams the keys near the memory's rate
     // (32 ragged sequences of 32 rows: 98 us, 84 with an 8-bit cache; by the other 107 and 115; of 4 rows: 86 and

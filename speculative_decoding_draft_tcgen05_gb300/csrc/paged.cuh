@@ -115,9 +115,9 @@ struct PagedItem {
     int lo, hi, u0, units;
 };
 
-__device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const PagedSeq &s, int rt, PagedCut k)
+__host__ __device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const PagedSeq &s, int rt, PagedCut k)
 {
-    const int r0 = rt * k.R, r1 = min(s.n * p.group, r0 + k.R);
+    const int r0 = rt * k.R, r1 = r0 + min(k.R, s.n * p.group - r0);  // (a sequence has up to 2^31 - 1 rows)
     const int ta = p.by_group.div(r0), tb = p.by_group.div(r1 - 1);
     const int base = s.len - s.n;
     PagedItem it;
@@ -129,9 +129,9 @@ __device__ __forceinline__ PagedItem paged_item(const AttendParams &p, const Pag
     return it;
 }
 
-__device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const PagedSeq &s, int R)
+__host__ __device__ __forceinline__ int paged_row_tiles(const AttendParams &p, const PagedSeq &s, int R)
 {
-    return (s.n * p.group + R - 1) / R;
+    return static_cast<int>((static_cast<uint32_t>(s.n * p.group) + R - 1) / R);
 }
 
 // The items' costs (units + C) of a lane's heads in order (sequence, head, row
@@ -149,34 +149,41 @@ struct PagedPlan {
     int64_t total, begin, end;
     int ctas;      // G
     int lane0, cta;  // the lane's first CTA and this one, numbered lane by lane (an idle CTA beyond them: its block)
-    int b;         // sequence of `begin`
-    int kvh, off;  // the head that it falls into, and the offset within the head
+    int64_t off;   // `begin` within its head
+    int b, kvh;    // its sequence and head
     PagedSeq s;    // the sequence
 };
 
-// n / d, which the 64-bit division (some hundred cycles) is only needed for when n does not fit 32 bits.
-__device__ __forceinline__ int64_t paged_div(int64_t n, int d)
+// n / d, which the 64-bit division (some hundred cycles) is only needed for when they do not fit 32 bits.
+__device__ __forceinline__ int64_t paged_quot(int64_t n, int64_t d)
 {
-    return n >> 32 ? n / d : static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+    return (n | d) >> 32 ? n / d : static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
 }
 
-constexpr int kPlanSeqs = 512;  // sequences whose costs are kept in shared memory
+// Sequences whose costs are kept in shared memory. Beyond it each CTA works them out twice, a thread's sequences one
+// after the other, which the work itself hides: single tokens of 512, 513, 4,096 and 65,536 sequences of 64 keys (32 / 8
+// heads of 128 values, bf16) take 32, 33, 245 and 3,836 us.
+constexpr int kPlanSeqs = 512;
 
-// Cost per key/value head of a sequence, by one thread or by a whole warp.
-__device__ __forceinline__ int paged_cost(const AttendParams &p, const PagedSeq &s, PagedCut k)
+// Cost per key/value head of a sequence, by one thread or by a whole warp. Sums of costs have 64 bits: 2^28 row tiles
+// (tokens * heads < 2^31, 8 rows at least) of 2^25 units are 2^53, and their product with the number of CTAs
+// (paged_sharers()) stays below 2^63.
+__host__ __device__ __forceinline__ int64_t paged_cost(const AttendParams &p, const PagedSeq &s, PagedCut k)
 {
     const int nrt = paged_row_tiles(p, s, k.R);
-    int u = 0;
+    int64_t u = 0;
     for (int rt = 0; rt < nrt; ++rt) u += paged_item(p, s, rt, k).units + k.C;
     return u;
 }
 
-__device__ __forceinline__ int paged_cost_warp(const AttendParams &p, const PagedSeq &s, PagedCut k, int lane)
+__device__ __forceinline__ int64_t paged_cost_warp(const AttendParams &p, const PagedSeq &s, PagedCut k, int lane)
 {
     const int nrt = paged_row_tiles(p, s, k.R);
-    int u = 0;
+    int64_t u = 0;
     for (int rt = lane; rt < nrt; rt += 32) u += paged_item(p, s, rt, k).units + k.C;
-    return __reduce_add_sync(0xFFFFFFFFu, u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    return u;
 }
 
 // This CTA's share of `total`, its lane's costs.
@@ -191,7 +198,7 @@ __device__ __forceinline__ void paged_share(const AttendParams &p, PagedPlan &pl
     plan.ctas = G;
     plan.begin = plan.end = 0;
     if (c < G) {  // total * c / G, in parts that fit
-        const int64_t q = paged_div(total, G);
+        const int64_t q = paged_quot(total, G);
         const int rest = static_cast<int>(total - q * G);
         plan.begin = q * c + static_cast<uint32_t>(rest * c) / static_cast<uint32_t>(G);
         plan.end = q * (c + 1) + static_cast<uint32_t>(rest * (c + 1)) / static_cast<uint32_t>(G);
@@ -211,12 +218,12 @@ __device__ __forceinline__ void paged_report(const AttendParams &p, int b)
 // costs are shared out between the warps, through `cost`; warp 0 returns the
 // plan.
 template <int NT>
-__device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, PagedCut cut, int *cost)
+__device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, PagedCut cut, int64_t *cost)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PagedPlan plan = {};
     PagedSeq s = {0, 0, 0};
-    int head = 0;  // cost per key/value head
+    int64_t head = 0;  // cost per key/value head
     bool many = false;
     if (lane < p.B) {
         s = paged_seq(p, lane);
@@ -230,14 +237,14 @@ __device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, Pag
             if (k % (NT / 32) != warp) continue;
             const int b = __ffs(m) - 1;
             const PagedSeq of = {0, __shfl_sync(0xFFFFFFFFu, s.n, b), __shfl_sync(0xFFFFFFFFu, s.len, b)};
-            const int u = paged_cost_warp(p, of, cut, lane);
+            const int64_t u = paged_cost_warp(p, of, cut, lane);
             if (lane == 0) cost[b] = u;
         }
         __syncthreads();
         if (many) head = cost[lane];
     }
     if (warp > 0) return plan;
-    const int64_t mine = static_cast<int64_t>(head) * p.lane_heads;
+    const int64_t mine = head * p.lane_heads;
     int64_t upto = mine;
     for (int o = 1; o < p.B; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
@@ -248,18 +255,18 @@ __device__ __forceinline__ PagedPlan paged_plan_warps(const AttendParams &p, Pag
     plan.b = max(0, __ffs(at) - 1);  // (sequences without new tokens cost nothing and are passed over)
     plan.s = {__shfl_sync(0xFFFFFFFFu, s.t0, plan.b), __shfl_sync(0xFFFFFFFFu, s.n, plan.b), __shfl_sync(0xFFFFFFFFu, s.len, plan.b)};
     const int64_t off = plan.begin - __shfl_sync(0xFFFFFFFFu, upto - mine, plan.b);
-    const int per_head = max(1, __shfl_sync(0xFFFFFFFFu, head, plan.b));
-    const int head_at = static_cast<int>(paged_div(off, per_head));
-    plan.off = static_cast<int>(off - static_cast<int64_t>(head_at) * per_head);
+    const int64_t per_head = max(int64_t(1), __shfl_sync(0xFFFFFFFFu, head, plan.b));
+    const int head_at = static_cast<int>(paged_quot(off, per_head));
+    plan.off = off - head_at * per_head;
     plan.kvh = head_at * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
     if (blockIdx.x == 0 && lane < p.B) paged_report(p, lane);
     return plan;
 }
 
-// cost: kPlanSeqs ints of shared memory that are free until the plan is made.
+// cost: kPlanSeqs numbers of shared memory that are free until the plan is made.
 // The block meets in here at least once.
 template <int NT>
-__device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
+__device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int64_t *cost)
 {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ PagedPlan plan;
@@ -288,7 +295,7 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
     if (__syncthreads_or(many)) {
         for (int b = warp; b < p.B; b += NT / 32)
             if (cost[b] < 0) {
-                const int u = paged_cost_warp(p, paged_seq(p, b), cut, lane);
+                const int64_t u = paged_cost_warp(p, paged_seq(p, b), cut, lane);
                 __syncwarp();
                 if (lane == 0) cost[b] = u;
             }
@@ -296,7 +303,7 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
     }
     auto head_cost = [&](int b) { return kept ? cost[b] : paged_cost(p, paged_seq(p, b), cut); };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(head_cost(b)) * p.lane_heads;
+    for (int b = b0; b < b1; ++b) mine += head_cost(b) * p.lane_heads;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -314,17 +321,17 @@ __device__ PagedPlan paged_plan(const AttendParams &p, PagedCut cut, int *cost)
     PagedPlan made;
     paged_share(p, made, total);
     if (made.begin < made.end ? (before <= made.begin && made.begin < before + mine) : tid == 0) {
-        int64_t off = made.begin - before;
-        int b = b0, per_head = 1;
+        int64_t off = made.begin - before, per_head = 1;
+        int b = b0;
         if (made.begin < made.end)
             for (; b < b1; ++b) {
                 per_head = head_cost(b);
-                if (off < static_cast<int64_t>(per_head) * p.lane_heads) break;
-                off -= static_cast<int64_t>(per_head) * p.lane_heads;
+                if (off < per_head * p.lane_heads) break;
+                off -= per_head * p.lane_heads;
             }
         made.b = b;
-        const int at = made.begin < made.end ? static_cast<int>(paged_div(off, per_head)) : 0;
-        made.off = static_cast<int>(off - static_cast<int64_t>(at) * per_head);
+        const int at = made.begin < made.end ? static_cast<int>(paged_quot(off, per_head)) : 0;
+        made.off = off - at * per_head;
         made.kvh = at * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
         made.s = paged_seq(p, min(b, p.B - 1));
         plan = made;
@@ -364,7 +371,7 @@ struct PagedWalk {
         nrt = paged_row_tiles(p, pc.s, k.R);
         pc.kvh = plan.kvh;
         pc.rt = 0;
-        int rem = plan.off;
+        int64_t rem = plan.off;
         for (int from = 0; nrt > 1; from += 32) {  // the row tile that holds cost `rem` of the head, 32 at a time
             const int u = from + lane < nrt ? paged_item(p, pc.s, from + lane, k).units + k.C : 0;
             int upto = u;
@@ -400,11 +407,11 @@ struct PagedWalk {
             pc.kvh += p.lanes;
             if (pc.kvh >= p.kv_heads) {
                 pc.kvh %= p.lanes;
-                do {
-                    ++pc.b;
+                do {  // there are items left (unless the lengths change while the kernel runs)
+                    if (++pc.b >= p.B) return more = false;
                     pc.s = paged_seq(p, pc.b);
                     nrt = paged_row_tiles(p, pc.s, k.R);
-                } while (nrt == 0);  // ends: there are items left
+                } while (nrt == 0);
             }
         }
         pc.it = paged_item(p, pc.s, pc.rt, k);
@@ -415,11 +422,6 @@ struct PagedWalk {
     // Whether another CTA has a part of the piece's item.
     __device__ __forceinline__ bool split() const { return pc.a > 0 || pc.e < pc.it.units; }
 };
-
-__device__ __forceinline__ int64_t paged_quot(int64_t n, int64_t d)
-{
-    return (n | d) >> 32 ? n / d : static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
-}
 
 // The CTAs that share the piece's item: the first, and how many. Boundary c
 // lies inside the item (after its first unit, before its last one's end) if

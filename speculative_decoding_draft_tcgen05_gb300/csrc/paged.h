@@ -41,7 +41,8 @@ struct PrepParams {
 cudaError_t launch_prep(const PrepParams &p, int head_dim, int dtype, cudaStream_t s);
 
 // ---- attention ----
-// Division of 0 <= n < 2^31 by a constant of the launch.
+// Division of 0 <= n < 2^31 by a constant of the launch (a product and a shift: Granlund and Montgomery, "Division by
+// invariant integers using multiplication").
 struct FastDiv {
     uint32_t d = 1, mul = 1, shift = 0;
     FastDiv() = default;
@@ -51,10 +52,10 @@ struct FastDiv {
         mul = static_cast<uint32_t>((((uint64_t(1) << shift) - by) << 32) / by + 1);
     }
 #ifdef __CUDACC__
-    __device__ __forceinline__ int div(int n) const
+    __host__ __device__ __forceinline__ int div(int n) const
     {
-        const uint32_t u = static_cast<uint32_t>(n);
-        return static_cast<int>((__umulhi(u, mul) + u) >> shift);
+        const uint32_t u = static_cast<uint32_t>(n), high = static_cast<uint32_t>((static_cast<uint64_t>(u) * mul) >> 32);
+        return static_cast<int>((high + u) >> shift);
     }
 #endif
 };

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
     pdl_trigger();
     pdl_wait();
     constexpr PagedCut cut = {R, kRowsUnit, rows_cost(R)};
-    const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, reinterpret_cast<int *>(smem));
+    const PagedPlan plan = paged_plan<kRowsThreads>(p, cut, reinterpret_cast<int64_t *>(smem));
     PagedWalk walk;
     walk.start(p, plan, cut);
     int4 merge0 = make_int4(0, 0, 0, 0), merge1 = merge0;

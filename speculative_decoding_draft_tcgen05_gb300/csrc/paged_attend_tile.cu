@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
     pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
-    const PagedPlan plan = paged_plan<tile_threads(FP8)>(p, cut, reinterpret_cast<int *>(smem));  // holds block barriers
+    const PagedPlan plan = paged_plan<tile_threads(FP8)>(p, cut, reinterpret_cast<int64_t *>(smem));  // holds block barriers
     tc_fence_after_sync();
     const uint32_t tmem = bars.tmem;
     int *const ab = &bars.abort_flag;
