@@ -82,6 +82,15 @@ constexpr float weight_lift()
     return std::is_same<CT, __half>::value ? 7.f : 0.f;
 }
 
+// Exponent of a query row's largest magnitude, for products in fp16 (8-bit caches): the row is scaled by 2^(8 - e), so
+// that magnitude comes to [2^8, 2^9) and bf16 queries of any size fit. Values below 2^-22 of it lose bits to fp16's
+// smallest step, at most 2^-33 of it each. (Zero, subnormal and infinite rows get the nearest e whose powers of two and
+// their inverses are ordinary numbers.)
+__device__ __forceinline__ int query_exponent(float top)
+{
+    return max(-118, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+}
+
 // One sequence of the batch: first row, new tokens, length in the cache.
 // Everything is clamped to what the call's arrays hold.
 struct PagedSeq {

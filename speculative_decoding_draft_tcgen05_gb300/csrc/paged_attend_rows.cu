@@ -248,8 +248,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                                                          (s.t0 + t) * p.q_ts + (pc.kvh * p.group + g) * p.q_hs + 8 * c);
                 }
                 if constexpr (FP8) {
-                    // The products run in fp16: a power of two per row brings the row's largest
-                    // value to [2^8, 2^9), so bf16 queries of any size fit (and f16 ones stay exact).
+                    // the products run in fp16: a power of two per row (query_exponent())
                     float f[8];
                     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                     float top = 0.f;
@@ -262,8 +261,7 @@ __global__ void __launch_bounds__(kRowsThreads, R <= 16 ? 3 : 2) attend_rows_ker
                     }
 #pragma unroll
                     for (int o = QCH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal
-                    e = max(-100, min(100, e));
+                    const int e = query_exponent(top);
                     const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
                     if (c == 0) q_undo[r] = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
                     // of every 16 values 0, 1, 4, 5, 8, .. are k = 0 .. 7 of the product and the others 8 .. 15 (see the scores)

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileBars<S> bars;
     __shared__ float2 x_ml[128];
-    // 8-bit cache: a query row was scaled by 2^(108 - this). Pieces take the two slots in turn, since the streams read a
+    // 8-bit cache: a query row was scaled by 2^(126 - this). Pieces take the two slots in turn, since the streams read a
     // piece's before its first weights, while the queries' place (q_empty) is free once its last scores are there: in a
     // piece of one tile that is earlier, and the next piece's queries may come while the streams still finish the piece
     // before. Two are enough: a slot is written again when the scores of the piece between are complete, and those are
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                 if (!(ok = warp_wait(&bars.s_full[i], s_phase, ab))) break;
                 s_phase ^= 1;
                 tc_fence_after_sync();
-                if (FP8 && t == 0) factor *= __uint_as_float((19u + q_exp[q_slot][c.r]) << 23);
+                if (FP8 && t == 0) factor *= __uint_as_float((1u + q_exp[q_slot][c.r]) << 23);
                 uint32_t sr[128];
                 tmem_load128<FP8>(s_col, sr);
                 if (!(key0 > most_after && key0 + U - 1 <= least_upto)) {
@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                     }
                 }
                 if constexpr (FP8) {
-                    // In their place, by the thread that copied them: to fp16 with the row's largest value in
-                    // [2^8, 2^9), by a power of two, so that queries of any size fit (a row's lanes are neighbours).
+                    // In their place, by the thread that copied them: to fp16 with a power of two per row
+                    // (query_exponent(); a row's lanes are neighbours).
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     for (int i = 0; i < tiles; ++i) {
 #pragma unroll 2
@@ -754,13 +754,12 @@ __global__ void __launch_bounds__(tile_threads(FP8), 1) attend_tile_kernel(const
                             for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
 #pragma unroll
                             for (int o = CH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal
-                            e = max(-100, min(100, e));
+                            const int e = query_exponent(top);
                             const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
                             if (row < 128) {
                                 *at = make_uint4(pack2<CT>(f[0].x * up, f[0].y * up), pack2<CT>(f[1].x * up, f[1].y * up),
                                                  pack2<CT>(f[2].x * up, f[2].y * up), pack2<CT>(f[3].x * up, f[3].y * up));
-                                if (c == 0) q_exp[q_phase][128 * i + row] = static_cast<uint8_t>(e + 100);
+                                if (c == 0) q_exp[q_phase][128 * i + row] = static_cast<uint8_t>(e + 118);
                             }
                         }
                         fence_async_proxy();

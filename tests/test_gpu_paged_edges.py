@@ -104,3 +104,18 @@ def test_attend_rows_that_see_nothing_exactly(pkg, new, lens, cache):  # noqa: F
         s.layer.sync_status()
         assert (out[nothing] == 0).all() and (lse[nothing] == -math.inf).all()
         assert lse[~nothing].isfinite().all() and (out[~nothing] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 90])
+@pytest.mark.parametrize("e", [-126, -118, -101, -99, 99, 107, 108, 120, 125])
+def test_attend_queries_of_any_size(pkg, e, new):  # noqa: F811
+    """bf16 queries of 2^e over an 8-bit cache, with scales that bring the scores back to ordinary sizes."""
+    s = Paged(pkg, [new], [333], heads=4, kv_heads=2, d=64, dtype=BF16, cache=FP8, seed=new)
+    for x in (s.k, s.v):
+        x.copy_((0.125 * torch.randn(x.shape, device="cuda", generator=s.g)).to(FP8))
+    q = (s.rows(4).clamp(-1.9, 1.9).double() * 2.0 ** e).to(BF16)
+    # (scale * k_scale has to be an ordinary number; bf16 queries below 2^-126 keep few bits, which the reference reads as they are)
+    k_scale, scale = 2.0 ** (-60 if e > 0 else 60), 2.0 ** ((60 if e > 0 else -60) - e)
+    s.cache.c.k_scale, s.ks = k_scale, k_scale
+    s.cache.c.v_scale, s.vs = 1.0, 1.0
+    s.check(q, scale=scale)
