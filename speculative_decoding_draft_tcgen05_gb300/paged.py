@@ -229,6 +229,21 @@ def dflash_paged_destroy(handle):
     check(L.dflash_paged_destroy(handle), "dflash_paged_destroy")
 
 
+def _empty_for(q, stream):
+    """A tensor like q for a call on `stream` (None: the current one): memory that no earlier work of another stream may
+    still touch, and that is not handed out again before the current stream's work up to then is done."""
+    torch = _torch()
+    if stream is not None:
+        here = torch.cuda.current_stream(q.device)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != here.cuda_stream:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, q.device)):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out.record_stream(here)
+            return out
+    return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+
+
 class PagedAttention:
     """Owns a handle (convenience only)."""
 
@@ -244,7 +259,7 @@ class PagedAttention:
 
     def attend(self, cache, batch, q, out=None, *, lse=None, causal=True, window=0, scale=None, stream=None):
         if out is None:
-            out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _empty_for(q, stream)
         st = (_calls or _load_calls()).attend(self.h, cache, batch, q, out, lse, causal, window, scale, stream)
         if st:
             _binding()[1](st, "dflash_paged_attend")

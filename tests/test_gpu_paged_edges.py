@@ -119,3 +119,31 @@ def test_attend_queries_of_any_size(pkg, e, new):  # noqa: F811
     s.cache.c.k_scale, s.ks = k_scale, k_scale
     s.cache.c.v_scale, s.vs = 1.0, 1.0
     s.check(q, scale=scale)
+
+
+def test_attend_makes_its_output_for_the_stream_of_the_call(pkg):  # noqa: F811
+    """Without `out`, a call on another stream writes memory that no pending work of the current stream holds, and that
+    is not handed out again while the current stream still reads it."""
+    s = Paged(pkg, [8, 5], [300, 40], heads=8, kv_heads=2, d=64, dtype=BF16, seed=4)
+    q = s.rows(8)
+    want = s.layer.attend(s.cache, s.batch, q)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        x = torch.empty_like(q)
+        torch.cuda._sleep(100_000_000)
+        x.fill_(7)                       # pending on the current stream when its memory is given back
+        del x
+        out = s.layer.attend(s.cache, s.batch, q, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out = s.layer.attend(s.cache, s.batch, q, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(100_000_000)
+        got = out.clone()                # pending when the output is given back
+        del out
+        with torch.cuda.stream(side):
+            other = [torch.full_like(q, 7) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and len(other) == 4
+    assert torch.equal(s.layer.attend(s.cache, s.batch, q, stream=torch.cuda.current_stream()), want)
