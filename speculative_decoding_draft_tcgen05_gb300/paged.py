@@ -225,8 +225,12 @@ def dflash_paged_sync_status(handle, stream=None):
 
 
 def dflash_paged_destroy(handle):
+    """Frees the handle; calls with it are refused from then on."""
     L, check, _ = _binding()
-    check(L.dflash_paged_destroy(handle), "dflash_paged_destroy")
+    at = handle
+    if isinstance(handle, PagedHandle):
+        at, handle.value, handle.spec = handle.value, None, (0,) + handle.spec[1:]
+    check(L.dflash_paged_destroy(at), "dflash_paged_destroy")
 
 
 def _empty_for(q, stream):
@@ -270,8 +274,7 @@ class PagedAttention:
 
     def close(self):
         if self.h is not None:
-            dflash_paged_destroy(self.h)
-            self.h = None
+            dflash_paged_destroy(self.h)  # (stays, empty: calls raise)
 
     def __enter__(self):
         return self

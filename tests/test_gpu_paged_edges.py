@@ -147,3 +147,27 @@ def test_attend_makes_its_output_for_the_stream_of_the_call(pkg):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(got, want) and len(other) == 4
     assert torch.equal(s.layer.attend(s.cache, s.batch, q, stream=torch.cuda.current_stream()), want)
+
+
+def test_destroyed_handles_are_refused(pkg):  # noqa: F811
+    s = Paged(pkg, [4, 4], [30, 40], heads=8, kv_heads=2, d=64, dtype=BF16, seed=1)
+    q, k, v = s.rows(8), s.rows(2), s.rows(2)
+    h = pkg.dflash_paged_init(heads=8, kv_heads=2, head_dim=64, page_size=16, dtype=BF16, max_batch=2)
+    out = torch.empty_like(q)
+    pkg.dflash_paged_attend(h, s.cache, s.batch, q, out)
+    want = out.clone()
+    pkg.dflash_paged_destroy(h)
+    out.fill_(7)
+    for call in (lambda: pkg.dflash_paged_attend(h, s.cache, s.batch, q, out),
+                 lambda: pkg.dflash_paged_append(h, s.cache, s.batch, k, v), lambda: pkg.dflash_paged_sync_status(h)):
+        with pytest.raises(pkg.DflashError) as e:
+            call()
+        assert e.value.status == pkg.DFLASH_ERR_INVALID_ARG
+    pkg.dflash_paged_destroy(h)     # nothing left to free
+    pkg.dflash_paged_destroy(None)
+    assert (out == 7).all() and torch.equal(s.layer.attend(s.cache, s.batch, q), want)
+    s.layer.close()
+    for call in (lambda: s.layer.attend(s.cache, s.batch, q, out), lambda: s.layer.append(s.cache, s.batch, k, v)):
+        with pytest.raises(pkg.DflashError):
+            call()
+    s.layer.close()
