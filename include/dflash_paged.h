@@ -109,9 +109,10 @@ dflash_status dflash_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t
                                   const int32_t *positions, void *stream);
 
 /* Checks the shapes and allocates the workspace that attention over split
- * sequences needs (the only allocation; 40 MB with head_dim 128). One handle serves all
- * layers of a model; its calls must not overlap on the GPU (order them on one
- * stream). Errors: INVALID_ARG, UNSUPPORTED (also: not an sm_103 GPU), CUDA. */
+ * sequences needs (the only allocation; 40 MB with head_dim 128), cleared on
+ * `stream`, which it waits for. One handle serves all layers of a model; its
+ * calls must not overlap on the GPU (order them on one stream, any).
+ * Errors: INVALID_ARG, UNSUPPORTED (also: not an sm_103 GPU), CUDA. */
 dflash_status dflash_paged_init(const dflash_paged_config *cfg, void *stream, dflash_paged_handle *out);
 
 /* Writes k and v [tokens, kv_heads, head_dim] of the batch's new tokens to

@@ -193,7 +193,9 @@ extern "C" dflash_status dflash_paged_init(const dflash_paged_config *cfg, void 
     c->merge = reinterpret_cast<int4 *>(at + o_bytes + ml_bytes);
     c->ticket = reinterpret_cast<unsigned *>(at + o_bytes + ml_bytes + merge_bytes);
     c->err = reinterpret_cast<int *>(at + o_bytes + ml_bytes + merge_bytes + ticket_bytes);
-    if (cudaMemsetAsync(c->ticket, 0, ticket_bytes + 256, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    // (waited for: the first call may be on another stream)
+    if (cudaMemsetAsync(c->ticket, 0, ticket_bytes + 256, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaFree(c->block);
         delete c;
         return paged_fail(DFLASH_ERR_CUDA, "clearing the workspace failed");

@@ -171,3 +171,18 @@ def test_destroyed_handles_are_refused(pkg):  # noqa: F811
         with pytest.raises(pkg.DflashError):
             call()
     s.layer.close()
+
+
+def test_new_handles_are_ready_for_any_stream(pkg):  # noqa: F811
+    """A handle made behind pending work serves a call on another stream at once (items joined by its counters)."""
+    s = Paged(pkg, [2, 1], [900, 16], heads=8, kv_heads=2, d=64, dtype=BF16, seed=4)
+    q = s.rows(8)
+    want = s.layer.attend(s.cache, s.batch, q)
+    side, out = torch.cuda.Stream(), torch.full_like(q, 7)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    layer = pkg.PagedAttention(heads=8, kv_heads=2, head_dim=64, page_size=16, dtype=BF16, max_batch=2)
+    layer.attend(s.cache, s.batch, q, out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    layer.sync_status()
