@@ -99,7 +99,8 @@ typedef struct dflash_paged_ctx *dflash_paged_handle;
  * k_out (either pair may be NULL; in place is allowed, other overlaps are
  * not). dtype BF16 or FP16, head_dim 64, 128 or 256, tokens * heads < 2^31.
  * positions [tokens] int32 (may be NULL with rotary_dim = 0). No handle, no
- * workspace; a position outside the table is clamped silently here.
+ * workspace; launched on the current device, which holds all tensors; a position
+ * outside the table is clamped silently here.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 dflash_status dflash_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
                                   int64_t qo_token_stride, int64_t qo_head_stride, const void *k,

@@ -104,6 +104,13 @@ dflash_status check_call(dflash_paged_handle h, const dflash_paged_cache *c, con
 
 }  // namespace
 
+// The current device (-1: none), for the binding, which compares it with the tensors' device.
+extern "C" int dflash_paged_current_device(void)
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 extern "C" dflash_status dflash_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
                                              int64_t qo_token_stride, int64_t qo_head_stride, const void *k,
                                              int64_t k_token_stride, int64_t k_head_stride, void *k_out,

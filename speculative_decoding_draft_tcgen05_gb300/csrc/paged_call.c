@@ -1,10 +1,11 @@
 /* Argument marshalling of the three entry points that a step calls once per
  * layer (include/dflash_paged.h), for the Python binding: checks the tensors,
  * takes their addresses and strides, finds the stream and makes the call, with
- * the interpreter's lock released. It does nothing that the binding could not
- * do through ctypes; it takes about half the time, and the GPU's work on one
- * block of a single sequence is shorter than either. Knows tensors only by
- * their Python attributes. */
+ * the interpreter's lock released. The tensors of a call, its handle and the
+ * current device, which the launch goes to, have to be the same device. It does
+ * nothing that the binding could not do through ctypes; it takes about half the
+ * time, and the GPU's work on one block of a single sequence is shorter than
+ * either. Knows tensors only by their Python attributes. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -25,10 +26,11 @@ typedef dflash_status (*attend_fn)(dflash_paged_handle, const dflash_paged_cache
 static norm_rope_fn call_norm_rope;
 static append_fn call_append;
 static attend_fn call_attend;
+static int (*current_device)(void);
 static PyObject *raw_stream;                 /* device index -> handle of its current stream */
 static PyObject *t_int32, *t_float32;        /* torch dtypes */
 static PyObject *t_bf16, *t_fp16;
-static PyObject *s_dtype, *s_shape, *s_is_cuda, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_spec,
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_spec,
     *s_cuda_stream;
 
 typedef struct {
@@ -42,13 +44,13 @@ static int is_none(PyObject *o)
     return o == NULL || o == Py_None;
 }
 
-static int flag(PyObject *t, PyObject *name) /* a truth value attribute */
+/* The call's device (-1: not known yet) is also that of `name`. */
+static int same_device(long index, long *dev, const char *name)
 {
-    PyObject *o = PyObject_GetAttr(t, name);
-    if (!o) return -1;
-    const int is = PyObject_IsTrue(o);
-    Py_DECREF(o);
-    return is;
+    if (*dev < 0) *dev = index;
+    if (*dev == index) return 0;
+    PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the call's other tensors or its handle on cuda:%ld", name, index, *dev);
+    return -1;
 }
 
 static int has_dtype(PyObject *t, PyObject *dtype, const char *name)
@@ -85,14 +87,18 @@ static int sizes(PyObject *t, int dims, const int64_t *want, int64_t *n, const c
     return bad ? -1 : 0;
 }
 
-static int address(PyObject *t, void **p, const char *name)
+static int address(PyObject *t, long *dev, void **p, const char *name)
 {
-    const int cuda = flag(t, s_is_cuda);
-    if (cuda <= 0) {
-        if (cuda == 0) PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
+    PyObject *o = PyObject_CallMethodNoArgs(t, s_get_device);
+    if (!o) return -1;
+    const long index = PyLong_AsLong(o);
+    Py_DECREF(o);
+    if (index < 0) {
+        if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
         return -1;
     }
-    PyObject *o = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (same_device(index, dev, name) < 0) return -1;
+    o = PyObject_CallMethodNoArgs(t, s_data_ptr);
     if (!o) return -1;
     *p = PyLong_AsVoidPtr(o);
     Py_DECREF(o);
@@ -100,9 +106,10 @@ static int address(PyObject *t, void **p, const char *name)
 }
 
 /* Rows [tokens, heads, head_dim] with a contiguous last dimension. */
-static int get_rows(PyObject *t, PyObject *dtype, const int64_t *want, rows *r, const char *name)
+static int get_rows(PyObject *t, PyObject *dtype, const int64_t *want, long *dev, rows *r, const char *name)
 {
-    if (has_dtype(t, dtype, name) < 0 || sizes(t, 3, want, r->n, name) < 0 || address(t, &r->p, name) < 0) return -1;
+    if (has_dtype(t, dtype, name) < 0 || sizes(t, 3, want, r->n, name) < 0 || address(t, dev, &r->p, name) < 0)
+        return -1;
     PyObject *o = PyObject_CallMethodNoArgs(t, s_stride);
     if (!o) return -1;
     if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3) {
@@ -124,12 +131,12 @@ static int get_rows(PyObject *t, PyObject *dtype, const int64_t *want, rows *r, 
 }
 
 /* A contiguous tensor of the given dtype and sizes, or NULL for None. */
-static int get_plain(PyObject *t, PyObject *dtype, int dims, const int64_t *want, void **p, const char *name)
+static int get_plain(PyObject *t, PyObject *dtype, int dims, const int64_t *want, long *dev, void **p, const char *name)
 {
     int64_t n[2];
     *p = NULL;
     if (is_none(t)) return 0;
-    if (has_dtype(t, dtype, name) < 0 || sizes(t, dims, want, n, name) < 0 || address(t, p, name) < 0) return -1;
+    if (has_dtype(t, dtype, name) < 0 || sizes(t, dims, want, n, name) < 0 || address(t, dev, p, name) < 0) return -1;
     PyObject *o = PyObject_CallMethodNoArgs(t, s_is_contiguous);
     if (!o) return -1;
     const int is = PyObject_IsTrue(o);
@@ -138,11 +145,11 @@ static int get_plain(PyObject *t, PyObject *dtype, int dims, const int64_t *want
     return is > 0 ? 0 : -1;
 }
 
-static int get_stream(PyObject *stream, PyObject *t, void **s)
+static int get_stream(PyObject *stream, long dev, void **s)
 {
     PyObject *o;
     if (is_none(stream)) {
-        PyObject *d = PyObject_CallMethodNoArgs(t, s_get_device);
+        PyObject *d = PyLong_FromLong(dev);
         if (!d) return -1;
         o = PyObject_CallOneArg(raw_stream, d);
         Py_DECREF(d);
@@ -168,12 +175,12 @@ static PyObject *spec_of(PyObject *o, Py_ssize_t n, const char *name)
     return s;
 }
 
-/* QkTransform.spec: (address of the C structure, weights' dtype or None, weights' size). */
-static int get_transform(PyObject *o, PyObject *dtype, int64_t head_dim, const dflash_qk_transform **tr)
+/* QkTransform.spec: (address of the C structure, weights' dtype or None, weights' size, device or -1 without tensors). */
+static int get_transform(PyObject *o, PyObject *dtype, int64_t head_dim, long *dev, const dflash_qk_transform **tr)
 {
     *tr = NULL;
     if (is_none(o)) return 0;
-    PyObject *s = spec_of(o, 3, "transform");
+    PyObject *s = spec_of(o, 4, "transform");
     if (!s) return -1;
     PyObject *wd = PyTuple_GET_ITEM(s, 1);
     int bad = 0;
@@ -182,16 +189,20 @@ static int get_transform(PyObject *o, PyObject *dtype, int64_t head_dim, const d
                      PyTuple_GET_ITEM(s, 2));
         bad = 1;
     }
+    const long index = PyLong_AsLong(PyTuple_GET_ITEM(s, 3));
+    if (!bad && index >= 0) bad = same_device(index, dev, "transform") < 0;
     *tr = (const dflash_qk_transform *)PyLong_AsVoidPtr(PyTuple_GET_ITEM(s, 0));
     Py_DECREF(s);
     return bad || PyErr_Occurred() ? -1 : 0;
 }
 
 /* A handle, cache and batch that fit together. handle.spec: (address, dtype, cache dtype, heads, kv_heads, head_dim,
- * cache shape); cache.spec: (address of the C structure, dtype, shape); batch.spec: (address of the C structure,). */
+ * cache shape, device); cache.spec: (address of the C structure, dtype, shape, device); batch.spec: (address of the C
+ * structure, device). */
 typedef struct {
     PyObject *dtype; /* borrowed from the handle */
     int64_t heads, kv_heads, head_dim;
+    long dev; /* the handle's */
     dflash_paged_handle h;
     const dflash_paged_cache *cache;
     dflash_paged_batch *batch;
@@ -200,9 +211,9 @@ typedef struct {
 static int get_call(PyObject *handle, PyObject *cache, PyObject *batch, call *c)
 {
     int ok = 0;
-    PyObject *h = spec_of(handle, 7, "handle"), *k = NULL, *b = NULL;
-    if (h) k = spec_of(cache, 3, "cache");
-    if (k) b = spec_of(batch, 1, "batch");
+    PyObject *h = spec_of(handle, 8, "handle"), *k = NULL, *b = NULL;
+    if (h) k = spec_of(cache, 4, "cache");
+    if (k) b = spec_of(batch, 2, "batch");
     if (b) {
         c->h = (dflash_paged_handle)PyLong_AsVoidPtr(PyTuple_GET_ITEM(h, 0));
         c->dtype = PyTuple_GET_ITEM(h, 1); /* (kept alive by torch) */
@@ -211,7 +222,9 @@ static int get_call(PyObject *handle, PyObject *cache, PyObject *batch, call *c)
         c->head_dim = PyLong_AsLongLong(PyTuple_GET_ITEM(h, 5));
         c->cache = (const dflash_paged_cache *)PyLong_AsVoidPtr(PyTuple_GET_ITEM(k, 0));
         c->batch = (dflash_paged_batch *)PyLong_AsVoidPtr(PyTuple_GET_ITEM(b, 0));
-        ok = !PyErr_Occurred();
+        c->dev = PyLong_AsLong(PyTuple_GET_ITEM(h, 7));
+        const long at[2] = {PyLong_AsLong(PyTuple_GET_ITEM(k, 3)), PyLong_AsLong(PyTuple_GET_ITEM(b, 1))};
+        ok = !PyErr_Occurred() && same_device(at[0], &c->dev, "cache") == 0 && same_device(at[1], &c->dev, "batch") == 0;
         if (ok) {
             const int same = PyTuple_GET_ITEM(k, 1) == PyTuple_GET_ITEM(h, 2)
                                  ? PyObject_RichCompareBool(PyTuple_GET_ITEM(k, 2), PyTuple_GET_ITEM(h, 6), Py_EQ)
@@ -228,6 +241,14 @@ static int get_call(PyObject *handle, PyObject *cache, PyObject *batch, call *c)
     return ok ? 0 : -1;
 }
 
+/* Without a handle, whose device the library compares with the current one, that is done here. */
+static int launch_device(long dev)
+{
+    const int now = current_device();
+    if (now != dev) PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%ld, the current device is cuda:%d", dev, now);
+    return now == dev ? 0 : -1;
+}
+
 /* norm_rope(q, k, q_out, k_out, transform, positions, stream) -> status */
 static PyObject *norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
@@ -235,21 +256,23 @@ static PyObject *norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (n != 7) return PyErr_Format(PyExc_TypeError, "norm_rope takes 7 arguments, got %zd", n);
     const int has_q = !is_none(a[0]), has_k = !is_none(a[1]);
     if (!has_q && !has_k) return PyErr_Format(PyExc_ValueError, "q or k must be given");
-    PyObject *x = has_q ? a[0] : a[1], *dt = PyObject_GetAttr(x, s_dtype);
+    PyObject *dt = PyObject_GetAttr(has_q ? a[0] : a[1], s_dtype);
     if (!dt) return NULL;
     rows q = {0}, qo = {0}, k = {0}, ko = {0};
     const dflash_qk_transform *tr = NULL;
     void *pos = NULL, *st = NULL;
+    long dev = -1;
     int bad = 0;
     int64_t want[3] = {-1, -1, -1};
-    if (has_q) bad = get_rows(a[0], dt, want, &q, "q") < 0 || get_rows(a[2], dt, q.n, &qo, "q_out") < 0;
+    if (has_q) bad = get_rows(a[0], dt, want, &dev, &q, "q") < 0 || get_rows(a[2], dt, q.n, &dev, &qo, "q_out") < 0;
     if (!bad && has_k) {
         if (has_q) want[0] = q.n[0], want[2] = q.n[2];
-        bad = get_rows(a[1], dt, want, &k, "k") < 0 || get_rows(a[3], dt, k.n, &ko, "k_out") < 0;
+        bad = get_rows(a[1], dt, want, &dev, &k, "k") < 0 || get_rows(a[3], dt, k.n, &dev, &ko, "k_out") < 0;
     }
     const int64_t tokens = has_q ? q.n[0] : k.n[0], head_dim = has_q ? q.n[2] : k.n[2];
-    bad = bad || get_transform(a[4], dt, head_dim, &tr) < 0 || get_plain(a[5], t_int32, 1, &tokens, &pos, "positions") < 0 ||
-          get_stream(a[6], x, &st) < 0;
+    bad = bad || get_transform(a[4], dt, head_dim, &dev, &tr) < 0 ||
+          get_plain(a[5], t_int32, 1, &tokens, &dev, &pos, "positions") < 0 || launch_device(dev) < 0 ||
+          get_stream(a[6], dev, &st) < 0;
     const int32_t code = dt == t_bf16 ? DFLASH_BF16 : (dt == t_fp16 ? DFLASH_FP16 : -1);
     Py_DECREF(dt);
     if (bad) return NULL;
@@ -274,14 +297,15 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const dflash_qk_transform *tr = NULL;
     void *pos = NULL, *st = NULL;
     int64_t want[3] = {-1, c.kv_heads, c.head_dim};
-    if (get_rows(a[3], c.dtype, want, &k, "k") < 0 || get_rows(a[4], c.dtype, k.n, &v, "v") < 0 ||
-        get_transform(a[5], c.dtype, c.head_dim, &tr) < 0)
+    if (get_rows(a[3], c.dtype, want, &c.dev, &k, "k") < 0 || get_rows(a[4], c.dtype, k.n, &c.dev, &v, "v") < 0 ||
+        get_transform(a[5], c.dtype, c.head_dim, &c.dev, &tr) < 0)
         return NULL;
     if (!is_none(a[6])) {
         const int64_t as[3] = {k.n[0], c.heads, c.head_dim};
-        if (get_rows(a[6], c.dtype, as, &q, "q") < 0 || get_rows(a[7], c.dtype, as, &qo, "q_out") < 0) return NULL;
+        if (get_rows(a[6], c.dtype, as, &c.dev, &q, "q") < 0 || get_rows(a[7], c.dtype, as, &c.dev, &qo, "q_out") < 0)
+            return NULL;
     }
-    if (get_plain(a[8], t_int32, 1, k.n, &pos, "positions") < 0 || get_stream(a[9], a[3], &st) < 0) return NULL;
+    if (get_plain(a[8], t_int32, 1, k.n, &c.dev, &pos, "positions") < 0 || get_stream(a[9], c.dev, &st) < 0) return NULL;
     if (k.n[0] > INT32_MAX) return PyErr_Format(PyExc_ValueError, "too many tokens");
     dflash_paged_batch b = *c.batch;
     b.tokens = (int32_t)k.n[0];
@@ -303,8 +327,8 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t n)
     rows q = {0}, out = {0};
     void *lse = NULL, *st = NULL;
     const int64_t want[3] = {-1, c.heads, c.head_dim};
-    if (get_rows(a[3], c.dtype, want, &q, "q") < 0 || get_rows(a[4], c.dtype, q.n, &out, "out") < 0 ||
-        get_plain(a[5], t_float32, 2, q.n, &lse, "lse") < 0 || get_stream(a[9], a[3], &st) < 0)
+    if (get_rows(a[3], c.dtype, want, &c.dev, &q, "q") < 0 || get_rows(a[4], c.dtype, q.n, &c.dev, &out, "out") < 0 ||
+        get_plain(a[5], t_float32, 2, q.n, &c.dev, &lse, "lse") < 0 || get_stream(a[9], c.dev, &st) < 0)
         return NULL;
     const int causal = PyObject_IsTrue(a[6]);
     const long long window = PyLong_AsLongLong(a[7]);
@@ -322,18 +346,19 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(status);
 }
 
-/* setup(norm_rope, append, attend: addresses; raw_stream; int32, float32, bfloat16, float16) */
+/* setup(norm_rope, append, attend, current_device: addresses; raw_stream; int32, float32, bfloat16, float16) */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
     (void)self;
-    PyObject *f[3], *o[5];
-    if (!PyArg_ParseTuple(args, "OOOOOOOO", &f[0], &f[1], &f[2], &o[0], &o[1], &o[2], &o[3], &o[4])) return NULL;
-    void *p[3];
-    for (int i = 0; i < 3; ++i) p[i] = PyLong_AsVoidPtr(f[i]);
+    PyObject *f[4], *o[5];
+    if (!PyArg_ParseTuple(args, "OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &o[0], &o[1], &o[2], &o[3], &o[4])) return NULL;
+    void *p[4];
+    for (int i = 0; i < 4; ++i) p[i] = PyLong_AsVoidPtr(f[i]);
     if (PyErr_Occurred()) return NULL;
     call_norm_rope = (norm_rope_fn)p[0];
     call_append = (append_fn)p[1];
     call_attend = (attend_fn)p[2];
+    current_device = (int (*)(void))p[3];
     PyObject **to[5] = {&raw_stream, &t_int32, &t_float32, &t_bf16, &t_fp16};
     for (int i = 0; i < 5; ++i) {
         Py_INCREF(o[i]);
@@ -355,7 +380,7 @@ PyMODINIT_FUNC PyInit__paged_call(void)
     struct {
         PyObject **to;
         const char *name;
-    } names[] = {{&s_dtype, "dtype"}, {&s_shape, "shape"}, {&s_is_cuda, "is_cuda"}, {&s_stride, "stride"},
+    } names[] = {{&s_dtype, "dtype"}, {&s_shape, "shape"}, {&s_stride, "stride"},
                  {&s_data_ptr, "data_ptr"}, {&s_is_contiguous, "is_contiguous"}, {&s_get_device, "get_device"},
                  {&s_spec, "spec"}, {&s_cuda_stream, "cuda_stream"}};
     for (size_t i = 0; i < sizeof names / sizeof *names; ++i)

@@ -87,7 +87,7 @@ def _load_calls():
     if raw is None:
         raw = lambda index: t.cuda.current_stream(index).cuda_stream  # noqa: E731
     at = [ctypes.cast(getattr(L, f), ctypes.c_void_p).value
-          for f in ("dflash_qk_norm_rope", "dflash_paged_append", "dflash_paged_attend")]
+          for f in ("dflash_qk_norm_rope", "dflash_paged_append", "dflash_paged_attend", "dflash_paged_current_device")]
     _paged_call.setup(*at, raw, t.int32, t.float32, t.bfloat16, t.float16)
     _calls = _paged_call
     return _calls
@@ -104,6 +104,14 @@ def _int32(t, shape, name):
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr()
+
+
+def _one_device(**tensors):
+    """The index of the device that all the given tensors (None: left out) are on; -1 without any."""
+    at = {name: t.get_device() for name, t in tensors.items() if t is not None}
+    if len(set(at.values())) > 1:
+        raise ValueError("tensors on different devices: " + ", ".join(f"{n} on cuda:{i}" for n, i in at.items()))
+    return next(iter(at.values()), -1)
 
 
 class QkTransform:
@@ -133,7 +141,8 @@ class QkTransform:
             q_weight=None if q_weight is None else q_weight.data_ptr(),
             k_weight=None if k_weight is None else k_weight.data_ptr(), eps=eps)
         w = self.weights[0] if self.weights else None
-        self.spec = (ctypes.addressof(self.c), None if w is None else w.dtype, 0 if w is None else w.shape[0])
+        self.spec = (ctypes.addressof(self.c), None if w is None else w.dtype, 0 if w is None else w.shape[0],
+                     _one_device(table=self.table, q_weight=q_weight, k_weight=k_weight))
 
 
 class PagedCache:
@@ -155,7 +164,7 @@ class PagedCache:
         self.c = dflash_paged_cache(k=k.data_ptr(), v=v.data_ptr(), num_pages=k.shape[0], page_stride=page,
                                     slot_stride=slot, head_stride=head if k.shape[2] > 1 else 0, k_scale=k_scale,
                                     v_scale=v_scale)
-        self.spec = (ctypes.addressof(self.c), k.dtype, tuple(k.shape[1:]))
+        self.spec = (ctypes.addressof(self.c), k.dtype, tuple(k.shape[1:]), _one_device(k=k, v=v))
 
 
 class PagedBatch:
@@ -171,7 +180,7 @@ class PagedBatch:
                                     page_table=_int32(page_table, (batch, None), "page_table"),
                                     table_stride=page_table.stride(0), table_cols=page_table.shape[1], batch=batch,
                                     tokens=0, max_tokens=max_tokens)
-        self.spec = (ctypes.addressof(self.c),)
+        self.spec = (ctypes.addressof(self.c), _one_device(cu_tokens=cu_tokens, lens=lens, page_table=page_table))
 
 
 def dflash_qk_norm_rope(q, k, q_out, k_out, transform, positions=None, stream=None):
@@ -198,7 +207,7 @@ def dflash_paged_init(*, heads, kv_heads, head_dim, page_size, dtype, cache_dtyp
     check(L.dflash_paged_init(ctypes.byref(cfg), get_stream(stream), ctypes.cast(ctypes.byref(h), ctypes.POINTER(ctypes.c_void_p))),
           "dflash_paged_init")
     h.spec = (h.value, dtype, dtype if cache_dtype is None else cache_dtype, heads, kv_heads, head_dim,
-              (page_size, kv_heads, head_dim))
+              (page_size, kv_heads, head_dim), _torch().cuda.current_device())
     return h
 
 
