@@ -57,7 +57,7 @@ typedef struct {
     void *k, *v;
     int64_t num_pages;  /* < 2^31 */
     int64_t page_stride, slot_stride, head_stride;
-    float k_scale, v_scale;  /* > 0; E4M3 caches only (1 is taken otherwise) */
+    float k_scale, v_scale;  /* >= 2^-126, finite; E4M3 caches only (1 is taken otherwise) */
 } dflash_paged_cache;
 
 /* The batch of a call. Sequence b has the new tokens cu_tokens[b] ..

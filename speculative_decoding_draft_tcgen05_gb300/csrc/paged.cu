@@ -97,8 +97,9 @@ dflash_status check_call(dflash_paged_handle h, const dflash_paged_cache *c, con
     for (int64_t s : {c->page_stride, c->slot_stride, c->head_stride})
         if (s < 0 || s % unit != 0)
             return paged_fail(DFLASH_ERR_INVALID_ARG, "cache strides must be multiples of %lld elements (got %lld)", unit, s);
-    if (h->cfg.cache_dtype == DFLASH_E4M3 && !(c->k_scale > 0.f && c->v_scale > 0.f && !isinf(c->k_scale) && !isinf(c->v_scale)))
-        return paged_fail(DFLASH_ERR_INVALID_ARG, "an 8-bit cache needs finite k_scale and v_scale > 0");
+    // (ordinary numbers: the reciprocal of a smaller one may be infinite)
+    if (h->cfg.cache_dtype == DFLASH_E4M3 && !(c->k_scale > 0.f && c->v_scale > 0.f && isnormal(c->k_scale) && isnormal(c->v_scale)))
+        return paged_fail(DFLASH_ERR_INVALID_ARG, "an 8-bit cache needs ordinary fp32 numbers > 0 as k_scale and v_scale");
     return DFLASH_OK;
 }
 

@@ -186,3 +186,22 @@ def test_new_handles_are_ready_for_any_stream(pkg):  # noqa: F811
     side.synchronize()
     assert torch.equal(out, want)
     layer.sync_status()
+
+
+def test_scales_whose_reciprocal_is_infinite_are_refused(pkg):  # noqa: F811
+    s = Paged(pkg, [2], [20], heads=4, kv_heads=2, d=64, dtype=BF16, cache=FP8, seed=1, poison=False)
+    q, k, v = s.rows(4), torch.zeros_like(s.rows(2)), torch.zeros_like(s.rows(2))
+    for name in ("k_scale", "v_scale"):
+        for bad in (1e-40, 0.0, -1.0, math.inf, math.nan):
+            good = getattr(s.cache.c, name)
+            setattr(s.cache.c, name, bad)
+            for call in (lambda: s.layer.append(s.cache, s.batch, k, v), lambda: s.layer.attend(s.cache, s.batch, q, scale=1e30)):
+                with pytest.raises(pkg.DflashError) as e:
+                    call()
+                assert e.value.status == pkg.DFLASH_ERR_INVALID_ARG
+            setattr(s.cache.c, name, good)
+    s.cache.c.k_scale = s.cache.c.v_scale = 2.0 ** -126
+    s.layer.append(s.cache, s.batch, k, v)
+    s.layer.sync_status()
+    at = s.table[0, 1].long()
+    assert (s.k[at, 2:4].float() == 0).all() and (s.v[at, 2:4].float() == 0).all()
