@@ -135,10 +135,13 @@ constexpr int kRowsPad = 8;  // floats between merge rows
 // matrix instructions and accumulators that rows of 16 would take.
 //
 // The floor is HBM: 2 * D * 2 bytes per key against 4 * D * rows operations,
-// 32 op/byte at 32 rows, which mma.sync sustains; the tensor memory path would
-// leave 3/4 or more of its 128-row tiles empty here. What keeps it from the
-// floor is the chain of each warp's step (copy wait, scores, weights, values)
-// with 8 or 12 warps an SM, and the start of each piece. Heads of 128 values,
+// 32 op/byte at 32 rows, which mma.sync sustains; in tensor memory the queries
+// as 128-row tiles would leave 3/4 or more of them empty (keys as the rows and
+// queries as the columns would not; that form was not built). What keeps it
+// from the floor is the chain of each warp's step (copy wait, scores, weights,
+// values) with 8 or 12 warps an SM, and the start of each piece: over an 8-bit
+// cache with 32 rows issue slots are 38 %, the tensor pipe 36 % and shared
+// memory 34 % busy, and fixed-latency waits lead a warp's stalls. Heads of 128 values,
 // 8 of them, a GB300 that copies 6.8 TB/s:
 //   128 sequences, 1 token x 4 heads, 200 to 3800 keys   16 bit 154 us 6.6 TB/s, 8 bit 88 us 5.8 TB/s
 //   32 sequences, 8 tokens x 4 heads, 500 to 7000 keys   16 bit  98 us 5.4 TB/s, 8 bit 84 us 3.2 TB/s

@@ -277,10 +277,12 @@ __device__ __forceinline__ int stream_steps(int n, bool alt, int i)
 // Bound by the tensor cores for many rows, with the exponentials (one per
 // score) close behind; by HBM for few. 2048 tokens x 32 heads of 128 values (8 key/value heads) after 14336:
 // 293 us, 1.76 PFLOP/s, called a few times, 326 us, 1.58 PFLOP/s, where the power
-// limit holds (a plain product: 1.90 and 1.70); with an 8-bit cache 335 us; 8
+// limit holds (a plain product: 1.90 and 1.70), 346 us with an 8-bit cache; 8
 // tokens x 40 heads over 131065 keys 93 us, 5.8 TB/s; seven windowed chunks of 300
 // to 1100 tokens, 16 heads of 64 values, 44 us, 0.35 PFLOP/s: few, short items
-// whose starts are not hidden.
+// whose starts and ends are not hidden (of a CTA's cycles 7 % are the plan, 16
+// to 24 % waits for a piece's first scores, 17 to 19 % the read-out of results
+// and the joins, 50 to 55 % the steps themselves).
 // ---------------------------------------------------------------------------
 struct TileParams {
     AttendParams a;
