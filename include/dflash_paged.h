@@ -36,7 +36,8 @@ extern "C" {
 typedef enum {
     DFLASH_BF16 = 0,
     DFLASH_FP16 = 1,
-    DFLASH_E4M3 = 2  /* 8-bit cache: a stored value x stands for x * scale */
+    DFLASH_E4M3 = 2, /* 8-bit cache: a stored value x stands for x * scale */
+    DFLASH_FP32 = 3  /* outputs of dflash_linear.h, logits of dflash_logits.h; not here */
 } dflash_dtype;
 
 /* Shapes fixed for the lifetime of a handle. Supported: heads a multiple of

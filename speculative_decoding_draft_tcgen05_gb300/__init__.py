@@ -87,6 +87,7 @@ def lib() -> ctypes.CDLL:
             L.dflash_conv2_destroy.argtypes = [P]
             L.dflash_last_error.restype = ctypes.c_char_p
             paged.declare(L)
+            step.declare(L)
             for f in ("dflash_select_init", "dflash_select_run", "dflash_verify_prefix", "dflash_select_step_host",
                       "dflash_select_sync_status", "dflash_select_profile", "dflash_select_profile_read",
                       "dflash_select_destroy", "dflash_lmhead_topk_noalloc", "dflash_select_run_sampled",
@@ -523,7 +524,10 @@ def dflash_selftest_wait_timeout(device_status, stream=None):
            "dflash_selftest_wait_timeout")
 
 
-from . import paged  # noqa: E402
+from . import paged, step  # noqa: E402
 from .paged import (DFLASH_BF16, DFLASH_E4M3, DFLASH_FP16, PagedAttention, PagedBatch, PagedCache,  # noqa: E402,F401
                     QkTransform, dflash_paged_append, dflash_paged_attend, dflash_paged_config, dflash_paged_destroy,
                     dflash_paged_init, dflash_paged_sync_status, dflash_qk_norm_rope)
+from .step import (DFLASH_FP32, Linear, LogitsRules, PagePool, dflash_linear_config,  # noqa: E402,F401
+                   dflash_linear_destroy, dflash_linear_init, dflash_linear_run, dflash_linear_sync_status,
+                   dflash_logits_adjust, dflash_logits_rules, dflash_page_pool, dflash_pages_extend, dflash_pages_trim)

@@ -102,6 +102,25 @@ dflash_status host_make_tmap(CUtensorMap *tm, const void *ptr, int64_t rows, int
     return make_tmap(tm, ptr, rows, cols, box_rows);
 }
 
+// 16-bit values [rows, cols], rows `stride` values apart, tiles of 64 columns x
+// box_rows rows, 128B swizzle; what lies past either end reads as zero.
+dflash_status host_make_tmap_rows(CUtensorMap *tm, const void *ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a [%lld, %lld] tensor", static_cast<int>(r),
+                    static_cast<long long>(rows), static_cast<long long>(cols));
+    return ok();
+}
+
 // Values [pages, slots of a page, heads, head_dim] (strides in values,
 // head_dim contiguous) as the 4D map (value, slot, head, page). 16-bit values:
 // boxes of 64 values x box_rows slots, 128B swizzle; 8-bit ones: boxes of

@@ -243,18 +243,23 @@ def dflash_paged_destroy(handle):
 
 
 def _empty_for(q, stream):
-    """A tensor like q for a call on `stream` (None: the current one): memory that no earlier work of another stream may
-    still touch, and that is not handed out again before the current stream's work up to then is done."""
+    """A tensor like q for a call on `stream`."""
+    return _empty_like_for(q, q.shape, q.dtype, stream)
+
+
+def _empty_like_for(q, shape, dtype, stream):
+    """A tensor on q's device for a call on `stream` (None: the current one): memory that no earlier work of another
+    stream may still touch, and that is not handed out again before the current stream's work up to then is done."""
     torch = _torch()
     if stream is not None:
         here = torch.cuda.current_stream(q.device)
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if handle != here.cuda_stream:
             with torch.cuda.stream(torch.cuda.ExternalStream(handle, q.device)):
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                out = torch.empty(shape, dtype=dtype, device=q.device)
             out.record_stream(here)
             return out
-    return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    return torch.empty(shape, dtype=dtype, device=q.device)
 
 
 class PagedAttention:
