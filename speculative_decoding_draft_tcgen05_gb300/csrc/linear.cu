@@ -1,20 +1,30 @@
 // y = residual + act(x W^T + bias) on the tcgen05 tensor cores.
 //
-// The weights are the products' M: 128 rows of W (256 over a CTA pair) are the
-// lanes of TMEM, and a tile of NT rows of x its columns, so that a single
-// token wastes 15 columns and not 127 lanes. k is streamed by TMA in stages of
-// 64 or 128 columns.
+// The weights are the products' M: up to 128 rows of W per CTA are the lanes of
+// TMEM, and a tile of NT rows of x its columns, so that a single token wastes
+// 15 columns and not 127 lanes. k is streamed by TMA in stages of one to four
+// boxes of 64 columns.
 //
-// Few rows are bound by the stream of W: each weight is read once, from as many
-// CTAs as there are (a tile's k split over a cluster of up to 8, whose CTAs
-// join their sums through distributed shared memory in the order of their
-// ranks, so that results do not depend on timing). Many rows are bound by the
-// tensor cores: persistent CTA pairs on tiles of 256 x NT with two accumulators
-// in TMEM, so that a tile's epilogue runs beside the next one's products.
+// Few rows are bound by the stream of W, each weight read once. One SM takes in
+// some 60 GB/s from HBM whatever it has in flight, so all of them have to
+// stream: a CTA takes as few weight rows (F, a multiple of 8) as gives every SM
+// its share, and a cluster of up to 8 CTAs can split a tile's k; they join their
+// sums through distributed shared memory in the order of their ranks, so that
+// results do not depend on timing. The products' other lanes then hold what
+// happens to lie behind the tile, and nobody reads them. Many rows are bound by
+// the tensor cores: persistent CTA pairs on tiles of 256 x NT with two
+// accumulators in TMEM, so that a tile's epilogue runs beside the next one's
+// products.
+//
+// The tensor cores' fp32 accumulator truncates: over k = 2560 its error is
+// 2.7e-6 of the result (2-norm). Results in 16 bits do not notice; for results
+// in 32 bits the accumulator is read every 512 columns and summed in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <math.h>
 #include <stdio.h>
 
+#include <atomic>
 #include <new>
 #include <type_traits>
 
@@ -28,16 +38,19 @@ dflash_status host_fail(dflash_status st, const char *msg);
 dflash_status host_make_tmap_rows(CUtensorMap *tm, const void *ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows);
 
 struct LinearParams {
-    CUtensorMap tm_w, tm_x;  // boxes of 64 columns x 128 rows, and x the tile's rows of one CTA
+    CUtensorMap tm_w, tm_x;  // boxes of 64 columns x F rows of W, and the rows of x that one CTA loads of a tile
     const void *bias, *residual;
     void *y;
     int64_t residual_stride, y_stride;
     int rows, n;
-    int NT;              // rows of x per tile
+    int F, NT;           // weight rows of a CTA, rows of x of a tile
     int boxes, stages;   // 64-column boxes per stage, stages of the ring
-    int KB;              // stages that k takes
+    int KB, seg;         // stages that k takes; that one accumulator takes
+    int kb_part, kb_more;  // stages of a part of k, and how many parts have one more
     int tiles_f, tiles_t, band;
-    int split;           // CTAs that share a tile's k
+    int split;           // CTAs (pairs) that share a tile's k
+    int owned;           // rows of x of a split tile that one of them joins, at most
+    int apart;           // their sums have a place of their own, else in the ring
     int act;
     int vec;             // y and residual: 4 values at a time
     int *err;
@@ -45,24 +58,30 @@ struct LinearParams {
 
 namespace {
 
-constexpr int kThreads = 320;  // TMA, products, 2 x 4 epilogue warps
-constexpr int kTileF = 128;    // weight rows of one CTA
+constexpr int kThreads = 320;  // TMA, products, 8 epilogue warps
+constexpr int kLanes = 128;    // of TMEM: the most weight rows of a CTA
 constexpr int kBox = 64;       // columns of a box: 128 bytes
-constexpr uint32_t kWBox = kTileF * kBox * 2;
-constexpr uint32_t kStaging = 16 * kTileF * 4;  // 16 rows of a tile's results, for each epilogue group
 constexpr int kMaxSplit = 8;
+constexpr int kMaxSum = 192;   // rows of x of a tile whose results are summed in registers
 
 struct Layout {
-    uint32_t stage, staging, bars, total;
+    uint32_t w, stage, bars, extra, total;
 };
 
-__host__ __device__ inline Layout layout(int NT, int boxes, int stages, bool pair, int split)
+constexpr uint32_t kTurn = 16 * 32 * 4;  // 16 rows of 32 results, turned from a lane per column to a lane per four
+
+__host__ __device__ inline Layout layout(int F, int NT, int boxes, int stages, bool pair, int split, int owned, int apart)
 {
     Layout l;
-    l.stage = static_cast<uint32_t>(boxes) * (kWBox + static_cast<uint32_t>(pair ? NT / 2 : NT) * kBox * 2);
-    l.staging = static_cast<uint32_t>(stages) * l.stage;
-    l.bars = l.staging + (split > 1 ? 0 : 2 * kStaging);  // (a split tile's sums go to the ring)
-    l.total = l.bars + 8u * (2u * stages + 5u) + 8u;  // full, empty, tfull, tempty, drain; TMEM's address, abort flag
+    l.w = static_cast<uint32_t>(F) * kBox * 2;
+    l.stage = static_cast<uint32_t>(boxes) * (l.w + static_cast<uint32_t>(pair ? NT / 2 : NT) * kBox * 2);
+    l.bars = static_cast<uint32_t>(stages) * l.stage;
+    l.extra = l.bars + ((8u * (2u * stages + 5u) + 8u + 127u) & ~127u);  // full, empty, tfull, tempty, drain; TMEM, abort flag
+    // the epilogue warps' turning places, or what the parts of a split tile send: [part][row][128]
+    l.total = l.extra + (split == 1 ? 8 * kTurn : apart ? static_cast<uint32_t>(split * owned) * kLanes * 4 : 0u);
+    // the products read 128 rows from a box's start on
+    const uint32_t read = static_cast<uint32_t>(stages > 0 ? stages - 1 : 0) * l.stage + static_cast<uint32_t>(boxes - 1) * l.w + kLanes * kBox * 2;
+    if (l.total < read) l.total = read;
     return l;
 }
 
@@ -73,51 +92,127 @@ __host__ __device__ inline int tmem_columns(int NT)
     return c;
 }
 
-__device__ __forceinline__ void group_sync(int id)
+// One lane of the calling warp.
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+    return is;
 }
 
-// Whether any of the group's 128 threads says so.
-__device__ __forceinline__ bool group_any(int id, bool pred)
+// The issuing instructions below act on lanes with who != 0. Whole warps run the code around them: a branch for one
+// lane would cost a chain of moves to uniform registers per product (100 clocks; as it is, the tensor cores' time).
+template <bool kPair>
+__device__ __forceinline__ void umma_if(uint32_t who, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    uint32_t r;
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(who)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(who)
+            : "memory");
+}
+
+// An arrival on `bar` (a pair: on that barrier of both CTAs of `both`) when the products so far are over.
+template <bool kPair>
+__device__ __forceinline__ void commit_if(uint32_t who, uint32_t bar, uint16_t both)
+{
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
+            "h"(both), "r"(who)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+            "r"(who)
+            : "memory");
+}
+
+// A box to this CTA's shared memory, its bytes counted on `bar` (a pair: a barrier of either CTA).
+template <bool kPair>
+__device__ __forceinline__ void load_if(uint32_t who, uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint64_t policy)
+{
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}\n" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy), "r"(who)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;\n\t}\n" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy), "r"(who)
+            : "memory");
+}
+
+__device__ __forceinline__ void expect_if(uint32_t who, uint32_t bar, uint32_t bytes)
+{
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %2, 0;\n\t"
-        "bar.red.or.pred q, %1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"(id), "r"(static_cast<uint32_t>(pred))
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+        "r"(bytes), "r"(who)
         : "memory");
-    return r != 0;
 }
 
-__device__ __forceinline__ float4 ld_peer(uint32_t addr)
+// A whole warp's wait (a pair's barriers are also arrived on by the other CTA).
+template <bool kPair>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    const bool got = kPair ? mbar_wait_cluster(bar, parity, abort_flag) : mbar_wait(bar, parity, abort_flag);
+    return __all_sync(0xFFFFFFFFu, got);
+}
+
+__device__ __forceinline__ void st_peer(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Exponentials and quotients by the fast forms: their error is a few 2^-22 of |z| (that of exp(-z) counts only where
 // it is not small against 1, and then |z| is not large), below fp32's of a product's sum.
-__device__ __forceinline__ float activate(float z, int act)
+template <int N>
+__device__ __forceinline__ void activate(float (&z)[N], int act)
 {
     switch (act) {
     case DFLASH_ACT_RELU:
-        return z < 0.f ? 0.f : z;
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
+        break;
     case DFLASH_ACT_SILU:
-        return __fdividef(z, 1.f + __expf(-z));
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = __fdividef(z[i], 1.f + __expf(-z[i]));
+        break;
     case DFLASH_ACT_GELU:
-        return 0.5f * z * (1.f + erff(z * 0.70710678f));
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678f));
+        break;
     case DFLASH_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-        return __fdividef(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            z[i] = __fdividef(z[i], 1.f + __expf(-1.5957691f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+        break;
     default:
-        return z;
+        break;
     }
 }
 
@@ -143,23 +238,22 @@ struct alignas(sizeof(Y) * 4) Four {
     Y v[4];
 };
 
-// Results of a row of y: features n0 .. n0 + 127 of the 128 in `src` (shared memory or a sum of it), by one warp.
-// A lane has four adjacent features where rows allow (vec), else every 32nd.
+// A row of a tile's results by one warp, four adjacent features a lane.
 template <typename T, typename Y>
 struct RowStore {
     const LinearParams &p;
-    const int lane, n0;
+    const int lane, n0, n1;  // features n0 .. n1 - 1
     float bias[4];
     bool whole;  // all four of the lane's features exist and go as one
 
-    __device__ __forceinline__ int feature(int i) const { return n0 + (p.vec ? lane * 4 + i : lane + 32 * i); }
+    __device__ __forceinline__ int feature(int i) const { return n0 + lane * 4 + i; }
 
-    __device__ __forceinline__ RowStore(const LinearParams &p_, int lane_, int n0_) : p(p_), lane(lane_), n0(n0_)
+    __device__ __forceinline__ RowStore(const LinearParams &p_, int lane_, int n0_, int n1_) : p(p_), lane(lane_), n0(n0_), n1(n1_)
     {
-        whole = p.vec && n0 + lane * 4 + 3 < p.n;
+        whole = p.vec && n0 + lane * 4 + 3 < n1;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            bias[i] = p.bias && feature(i) < p.n ? to_f(static_cast<const T *>(p.bias)[feature(i)]) : 0.f;
+            bias[i] = p.bias && feature(i) < n1 ? to_f(static_cast<const T *>(p.bias)[feature(i)]) : 0.f;
     }
 
     // this lane's values of the residual's row
@@ -171,33 +265,31 @@ struct RowStore {
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (feature(i) < p.n) r.v[i] = at[feature(i)];
+                if (feature(i) < n1) r.v[i] = at[feature(i)];
         }
     }
 
     __device__ __forceinline__ void store(int row, const float (&acc)[4], const Four<Y> &r) const
     {
+        float z[4] = {acc[0] + bias[0], acc[1] + bias[1], acc[2] + bias[2], acc[3] + bias[3]};
+        activate(z, p.act);
         Four<Y> o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float z = activate(acc[i] + bias[i], p.act);
-            if (p.residual) z += to_f(r.v[i]);
-            o.v[i] = from_f<Y>(z);
-        }
+        for (int i = 0; i < 4; ++i) o.v[i] = from_f<Y>(p.residual ? z[i] + to_f(r.v[i]) : z[i]);
         Y *at = static_cast<Y *>(p.y) + static_cast<int64_t>(row) * p.y_stride;
         if (whole) {
             *reinterpret_cast<Four<Y> *>(at + n0 + lane * 4) = o;
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (feature(i) < p.n) at[feature(i)] = o.v[i];
+                if (feature(i) < n1) at[feature(i)] = o.v[i];
         }
     }
 };
 
-// kPair: a cluster of two CTAs computes a tile of 256 weight rows (cta_group::2 products issued by the even CTA):
-// each holds 128 weight rows and half of the tile's rows of x, and has the results of its 128 weight rows.
-// Otherwise a cluster of p.split CTAs (1: none) shares the stages of one tile.
+// kPair: two CTAs compute a tile of 2 F weight rows (cta_group::2 products issued by the even CTA): each holds F weight
+// rows and half of the tile's rows of x, and has the results of its weight rows. A cluster of p.split CTAs or pairs
+// shares the stages of one tile.
 template <bool kPair, typename T, typename Y>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p)
 {
@@ -206,48 +298,81 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzled tiles start on 1024 bytes
     uint8_t *const gbase = smem_raw + (base - raw);
 
-    const int NT = p.NT, S = p.stages, BX = p.boxes;
-    const int XR = kPair ? NT / 2 : NT;
-    const int split = kPair ? 1 : p.split;
-    const Layout lay = layout(NT, BX, S, kPair, split);
-    const uint32_t w_bytes = static_cast<uint32_t>(BX) * kWBox;
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int NT = p.NT, S = p.stages, BX = p.boxes, F = p.F;
+    const int XR = NT / kCtas;
+    const int split = p.split;
+    const Layout lay = layout(F, NT, BX, S, kPair, split, p.owned, p.apart);
+    const uint32_t w_bytes = static_cast<uint32_t>(BX) * lay.w, x_bytes = static_cast<uint32_t>(XR) * kBox * 2;
     const uint32_t bar_full = base + lay.bars, bar_empty = bar_full + 8u * S;
     const uint32_t bar_tfull = bar_empty + 8u * S, bar_tempty = bar_tfull + 16u, bar_drain = bar_tempty + 16u;
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(gbase + lay.bars + 8u * (2u * S + 5u));
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = kPair || split > 1 ? cluster_ctarank() : 0u;
-    const int team = static_cast<int>(blockIdx.x) / (kPair ? 2 : split);  // the cluster's index, and how many there are
-    const int teams = static_cast<int>(gridDim.x) / (kPair ? 2 : split);
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const bool clustered = kPair || split > 1;
+    const uint32_t rank = clustered ? cluster_ctarank() : 0u;
+    const uint32_t half = kPair ? rank & 1u : 0u;    // of a pair
+    const uint32_t part = kPair ? rank >> 1 : rank;  // of a tile's k
+    int team, teams;                                 // the cluster's index, and how many there are
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(team));
+    asm("mov.u32 %0, %%nclusterid.x;" : "=r"(teams));
 
     // work items: tiles team, team + teams, .. (a split tile: one), in bands of `band` feature tiles, within which
     // the row tiles follow one another: CTAs that run together share both operands' tiles in L2
     const int items = p.tiles_f * p.tiles_t;
     auto tile_of = [&](int item, int &tf, int &tt) {
+        if (p.tiles_t == 1) {
+            tf = item;
+            tt = 0;
+            return;
+        }
         const int per = p.band * p.tiles_t, b = item / per, in = item - b * per;
         const int width = min(p.band, p.tiles_f - b * p.band);
         tt = in / width;
         tf = b * p.band + in - tt * width;
     };
+    auto first_feature = [&](int tf) { return (tf * kCtas + static_cast<int>(half)) * F; };
     // this CTA's stages of a tile
-    const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(p.KB) * rank / split);
-    const int kb1 = kPair ? p.KB : static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / split);
-    const int my_items = (items - team + teams - 1) / teams;
+    const int per = p.kb_part + (static_cast<int>(part) < p.kb_more ? 1 : 0);
+    const int kb0 = static_cast<int>(part) * p.kb_part + min(static_cast<int>(part), p.kb_more);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(bar_full + 8u * s, 1);
-            mbar_init(bar_empty + 8u * s, 1);
+    uint64_t pol_w = 0, pol_x = 0;
+    uint32_t who = 0;
+    const uint32_t full0 = kPair ? mapa_shared(bar_full, rank & ~1u) : bar_full;  // where the pair's bytes are counted
+    const uint32_t tx = kCtas * lay.stage;
+    auto load_w = [&](int s, int row, int kb) {
+        if (half == 0) expect_if(who, bar_full + 8u * s, tx);
+        for (int b = 0; b < BX; ++b)
+            load_if<kPair>(who, base + s * lay.stage + b * lay.w, &p.tm_w, (kb * BX + b) * kBox, row, full0 + 8u * s, pol_w);
+    };
+    auto load_x = [&](int s, int row, int kb) {
+        for (int b = 0; b < BX; ++b)
+            load_if<kPair>(who, base + s * lay.stage + w_bytes + b * x_bytes, &p.tm_x, (kb * BX + b) * kBox, row, full0 + 8u * s, pol_x);
+    };
+    const int pre = min(per, S);  // stages whose loads of W come first of all
+    int tf0, tt0;
+    tile_of(team, tf0, tt0);
+    if (warp == 0) {
+        who = elect_one();
+        if (who) {
+            for (int s = 0; s < S; ++s) {
+                mbar_init(bar_full + 8u * s, 1);
+                mbar_init(bar_empty + 8u * s, 1);
+            }
+            for (int a = 0; a < 2; ++a) {
+                mbar_init(bar_tfull + 8u * a, 1);
+                mbar_init(bar_tempty + 8u * a, 8 * kCtas);  // an arrival per epilogue warp (of both CTAs)
+            }
+            mbar_init(bar_drain, 1);
+            *abort_flag = 0;
+            fence_mbar_init();
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(bar_tfull + 8u * a, 1);
-            mbar_init(bar_tempty + 8u * a, kPair ? 16 : 8);  // an arrival per epilogue warp (of both CTAs)
-        }
-        mbar_init(bar_drain, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-        tma_prefetch_desc(&p.tm_w);
-        tma_prefetch_desc(&p.tm_x);
+        __syncwarp();
+        pol_w = p.tiles_t == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        pol_x = p.tiles_t == 1 ? l2_policy_evict_last() : l2_policy_evict_normal();
+        // W is constant from the handle's creation on: its first loads overlap the previous kernel on the stream
+        if constexpr (!kPair)
+            for (int i = 0; i < pre; ++i) load_w(i, first_feature(tf0), kb0 + i);
     }
     const uint32_t tmem_cols = static_cast<uint32_t>(tmem_columns(NT));
     if (warp == 1) {
@@ -261,253 +386,277 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (kPair) cluster_sync_all();  // the even CTA's barriers are initialised before any use
+    if (clustered) cluster_sync_all();  // the even CTA's barriers exist, and every CTA's shared memory
     tc_fence_after_sync();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_holder);
-    // What is above overlaps the previous kernel on the stream, and so do the first loads of W, which is constant from
-    // the handle's creation on. x, residual and y are touched after that kernel has finished.
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_holder), 0);
+    if (kPair && warp == 0)
+        for (int i = 0; i < pre; ++i) load_w(i, first_feature(tf0), kb0 + i);
+    // x, residual and y are touched after the previous kernel has finished
     pdl_trigger();
-    if (!(warp == 0 && lane == 0)) pdl_wait();
+    pdl_wait();
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
-        if (lane == 0) {
-            const uint64_t pol_w = p.tiles_t == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-            const uint64_t pol_x = p.tiles_t == 1 ? l2_policy_evict_last() : l2_policy_evict_normal();
-            const uint32_t tx = kPair ? 2u * lay.stage : lay.stage;  // a pair counts both CTAs' bytes on the even one's barrier
-            auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint64_t pol) {
-                if constexpr (kPair)
-                    tma_load_2d_pair(dst, tm, x, y, mapa_shared(bar, 0), pol);
-                else
-                    tma_load_2d(dst, tm, x, y, bar, pol);
-            };
-            auto load_w = [&](int it, int tf, int kb) {
-                const int s = it % S;
-                if (rank == 0 || !kPair) mbar_arrive_expect_tx(bar_full + 8u * s, tx);
-                const int row = kPair ? (tf * 2 + static_cast<int>(rank)) * kTileF : tf * kTileF;
-                for (int b = 0; b < BX; ++b)
-                    load(base + s * lay.stage + b * kWBox, &p.tm_w, (kb * BX + b) * kBox, row, bar_full + 8u * s, pol_w);
-            };
-            auto load_x = [&](int it, int tt, int kb) {
-                const int s = it % S;
-                const int row = tt * NT + (kPair ? static_cast<int>(rank) * XR : 0);
-                for (int b = 0; b < BX; ++b)
-                    load(base + s * lay.stage + w_bytes + b * (XR * kBox * 2), &p.tm_x, (kb * BX + b) * kBox, row,
-                         bar_full + 8u * s, pol_x);
-            };
-            const int per = kb1 - kb0;
-            int tf, tt, it = 0;
-            tile_of(team, tf, tt);
-            const int pre = my_items > 0 ? min(per, S) : 0;
-            for (int i = 0; i < pre; ++i) load_w(i, tf, kb0 + i);
-            pdl_wait();
-            for (; it < pre; ++it) load_x(it, tt, kb0 + it);
-            bool ok = true;
-            for (int i = 0; ok && i < my_items; ++i) {
-                tile_of(team + i * teams, tf, tt);
-                for (int k = i == 0 ? pre : 0; k < per; ++k, ++it) {
-                    if (!mbar_wait(bar_empty + 8u * (it % S), (static_cast<uint32_t>(it / S) & 1u) ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    load_w(it, tf, kb0 + k);
-                    load_x(it, tt, kb0 + k);
+        bool ok = true;
+        int s = 0, it = 0;
+        uint32_t ph = 1;  // of the stage's emptiness
+        for (; it < pre; ++it) load_x(it, tt0 * NT + static_cast<int>(half) * XR, kb0 + it);
+        s = pre;
+        if (s == S) s = 0, ph ^= 1u;
+        for (int i = team; ok && i < items; i += teams) {
+            int tf, tt;
+            tile_of(i, tf, tt);
+            for (int k = i == team ? pre : 0; k < per; ++k, ++it) {
+                // (the ring's first round is empty; from then on a stage is free when its products are over)
+                ok = warp_wait<false>(bar_empty + 8u * s, ph, abort_flag);
+                if (!ok) break;
+                load_w(s, first_feature(tf), kb0 + k);
+                load_x(s, tt * NT + static_cast<int>(half) * XR, kb0 + k);
+                if (++s == S) s = 0, ph ^= 1u;
+            }
+        }
+        if (!ok) {
+            if (who) atomicOr(p.err, DEV_ERR_TIMEOUT);
+            // what has been issued lands before the CTA can end
+            if (half == 0) {
+                for (int j = it > S ? it - S : 0; j < it; ++j)
+                    mbar_wait(bar_full + 8u * (j % S), static_cast<uint32_t>(j / S) & 1u, abort_flag, false);
+            } else {  // (counted on the even CTA's barriers: a copy lands within microseconds)
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 100000ull) {
                 }
             }
-            if (!ok) {
-                atomicOr(p.err, DEV_ERR_TIMEOUT);
-                // what has been issued lands before the CTA can end
-                if (rank == 0 || !kPair) {
-                    for (int j = it > S ? it - S : 0; j < it; ++j)
-                        mbar_wait(bar_full + 8u * (j % S), static_cast<uint32_t>(j / S) & 1u, abort_flag, false);
-                } else {  // (counted on the even CTA's barriers: a copy lands within microseconds)
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 100000ull) {
-                    }
-                }
-            }
+            __syncwarp();
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products (a pair: the even CTA's)
-        if (lane == 0 && (rank == 0 || !kPair)) {
+        if (half == 0) {
+            who = elect_one();
             constexpr bool kHalf = std::is_same_v<T, __half>;
-            const uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kTileF : kTileF, NT) & (kHalf ? ~((1u << 7) | (1u << 10)) : ~0u);
-            int it = 0;
+            const uint32_t idesc = idesc_bf16_f32(kCtas * kLanes, NT) & (kHalf ? ~((1u << 7) | (1u << 10)) : ~0u);
+            const uint16_t both = static_cast<uint16_t>(3u << (rank & ~1u));
+            // a descriptor's low bits are the address in units of 16 bytes: stepping it is an addition
+            const uint64_t w0 = smem_desc_sw128(base), x0 = smem_desc_sw128(base + w_bytes);
+            int s = 0, n = 0;
+            uint32_t ph = 0;
             bool ok = true;
-            for (int i = 0; ok && i < my_items; ++i) {
-                const int a = i & 1;
-                const uint32_t u = static_cast<uint32_t>(i >> 1);
-                ok = kPair ? mbar_wait_cluster(bar_tempty + 8u * a, (u & 1u) ^ 1u, abort_flag)
-                           : mbar_wait(bar_tempty + 8u * a, (u & 1u) ^ 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
-                for (int k = kb0; k < kb1; ++k, ++it) {
-                    const int s = it % S;
-                    const uint32_t ph = static_cast<uint32_t>(it / S) & 1u;
-                    ok = kPair ? mbar_wait_cluster(bar_full + 8u * s, ph, abort_flag)
-                               : mbar_wait(bar_full + 8u * s, ph, abort_flag);
+            for (int i = team; ok && i < items; i += teams) {
+                for (int k0 = 0; ok && k0 < per; k0 += p.seg, ++n) {
+                    const int a = n & 1;
+                    ok = warp_wait<kPair>(bar_tempty + 8u * a, (static_cast<uint32_t>(n >> 1) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t sw = base + s * lay.stage, sx = sw + w_bytes;
-                    for (int b = 0; b < BX; ++b) {
+                    const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
+                    const int k1 = min(per, k0 + p.seg);
+                    uint32_t more = 0;  // the accumulator holds something
+                    for (int k = k0; k < k1; ++k) {
+                        ok = warp_wait<kPair>(bar_full + 8u * s, ph, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t at = static_cast<uint32_t>(s) * (lay.stage >> 4);
+                        for (int b = 0; b < BX; ++b) {
+                            const uint64_t wd = w0 + at + b * (lay.w >> 4), xd = x0 + at + b * (x_bytes >> 4);
 #pragma unroll
-                        for (int j = 0; j < kBox / 16; ++j) {
-                            const uint64_t wd = smem_desc_sw128(sw + b * kWBox + 32u * j);
-                            const uint64_t xd = smem_desc_sw128(sx + b * (XR * kBox * 2) + 32u * j);
-                            const uint32_t acc = (k > kb0 || b > 0 || j > 0) ? 1u : 0u;
-                            if constexpr (kPair)
-                                umma_bf16_pair(d, wd, xd, idesc, acc);
-                            else
-                                umma_bf16(d, wd, xd, idesc, acc);
+                            for (int j = 0; j < kBox / 16; ++j) {
+                                umma_if<kPair>(who, d, wd + 2 * j, xd + 2 * j, idesc, more);
+                                more = 1;
+                            }
                         }
+                        commit_if<kPair>(who, bar_empty + 8u * s, both);
+                        if (++s == S) s = 0, ph ^= 1u;
                     }
-                    if constexpr (kPair)
-                        umma_commit_pair(bar_empty + 8u * s, 3);
-                    else
-                        umma_commit(bar_empty + 8u * s);
+                    if (ok) commit_if<kPair>(who, bar_tfull + 8u * a, both);
                 }
-                if (!ok) break;
-                if constexpr (kPair)
-                    umma_commit_pair(bar_tfull + 8u * a, 3);
-                else
-                    umma_commit(bar_tfull + 8u * a);
             }
-            if (!ok) atomicOr(p.err, DEV_ERR_TIMEOUT);
+            if (!ok && who) atomicOr(p.err, DEV_ERR_TIMEOUT);
             // every product is over before TMEM is released
-            if constexpr (kPair)
-                umma_commit_pair(bar_drain, 1);
-            else
-                umma_commit(bar_drain);
+            commit_if<kPair>(who, bar_drain, static_cast<uint16_t>(1u << rank));
             mbar_wait(bar_drain, 0, abort_flag, false);
+            __syncwarp();
         }
-    } else if (split == 1) {
-        // ---------------------------------------------------------------- epilogue: two groups of four warps take turns
-        // at a tile's 16-row chunks: TMEM (a feature per lane) -> shared memory -> rows of y
-        const int g = (warp - 2) >> 2, gw = (warp - 2) & 3, q = warp & 3;
-        float *const stage = reinterpret_cast<float *>(gbase + lay.staging + g * kStaging);
-        for (int i = 0; i < my_items; ++i) {
+    } else {
+        // ---------------------------------------------------------------- epilogue: a thread has a weight row's results;
+        // the two warps of a lane quadrant take turns at a tile's chunks of 16 rows of x
+        const int g = (warp - 2) >> 2, q = warp & 3, f = q * 32 + lane;
+        // results in 32 bits are summed in registers over the accumulators
+        constexpr bool kSum = std::is_same_v<Y, float>;
+        constexpr int kChunks = kMaxSum / 32;  // of a warp, at most
+        float *const turn = reinterpret_cast<float *>(gbase + lay.extra + (warp - 2) * kTurn);
+        const uint32_t mail = base + (p.apart ? lay.extra : 0u);  // where the parts of a split tile arrive
+        const int tr = lane >> 3, tc = (lane & 7) * 4;            // turned: rows tr + 4 t, features tc .. tc + 3
+        int n = 0;
+        bool ok = true;
+        for (int i = team; ok && i < items; i += teams) {
             int tf, tt;
-            tile_of(team + i * teams, tf, tt);
-            const int a = i & 1;
-            const uint32_t u = static_cast<uint32_t>(i >> 1);
-            const int n0 = kPair ? (tf * 2 + static_cast<int>(rank)) * kTileF : tf * kTileF;
-            const RowStore<T, Y> out(p, lane, n0);
-            const int row0 = tt * NT, valid = min(NT, p.rows - row0);
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
-            bool waited = false, ok = true;
-            for (int c = g * 16; c < valid || !waited; c += 32) {
-                Four<Y> r[4];
-                if (p.residual) {
+            tile_of(i, tf, tt);
+            const int n0 = first_feature(tf), feature = n0 + f;
+            const int end = min(p.n, n0 + F);  // behind the CTA's last feature
+            const int row0 = tt * NT, valid = q * 32 < F ? min(NT, p.rows - row0) : 0;
+            const float bias = p.bias && feature < end ? to_f(static_cast<const T *>(p.bias)[feature]) : 0.f;
+            const bool whole = p.vec && n0 + q * 32 + tc + 3 < end;
+            const int64_t col = n0 + q * 32 + tc;
+            // the residual of a chunk: as it is turned (four values of four rows), or the thread's own column
+            auto fetch = [&](int c, Four<Y> (&r)[4]) {
+                if (!p.residual || split > 1) return;
+                const Y *const res = static_cast<const Y *>(p.residual) + static_cast<int64_t>(row0 + c) * p.residual_stride;
+                if (p.vec) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (c + gw + 4 * t < valid) out.fetch(row0 + c + gw + 4 * t, r[t]);
-                }
-                if (!waited) {
-                    const bool got = kPair ? mbar_wait_cluster(bar_tfull + 8u * a, u & 1u, abort_flag)
-                                           : mbar_wait(bar_tfull + 8u * a, u & 1u, abort_flag);
-                    ok = !group_any(1 + g, !got);
-                    waited = true;
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    if (c >= valid) break;  // (a tile of one chunk: the other group's)
-                }
-                float v[16];
-                __syncwarp();
-                tmem_load16(taddr + static_cast<uint32_t>(c), v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) stage[j * kTileF + q * 32 + lane] = v[j];
-                group_sync(1 + g);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int j = gw + 4 * t;
-                    if (c + j < valid) {
-                        float z[4];
-                        if (p.vec) {
-                            const float4 f = *reinterpret_cast<const float4 *>(stage + j * kTileF + lane * 4);
-                            z[0] = f.x, z[1] = f.y, z[2] = f.z, z[3] = f.w;
+                    for (int t = 0; t < 4; ++t) {
+                        const Y *const at = res + (tr + 4 * t) * p.residual_stride + col;
+                        if (c + tr + 4 * t >= valid) continue;
+                        if (whole) {
+                            r[t] = *reinterpret_cast<const Four<Y> *>(at);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) z[e] = stage[j * kTileF + lane + 32 * e];
+                            for (int e = 0; e < 4; ++e)
+                                if (col + e < end) r[t].v[e] = at[e];
                         }
-                        out.store(row0 + c + j, z, r[t]);
+                    }
+                } else if (feature < end) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < valid) r[j >> 2].v[j & 3] = res[j * p.residual_stride + feature];
+                }
+            };
+            auto finish = [&](int c, float (&v)[16], const Four<Y> (&r)[4]) {
+                if (split > 1) {  // to the CTA that joins the row
+                    int slot = c / split, owner = c - slot * split;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (c + j < valid)
+                            st_peer(mapa_shared(mail, static_cast<uint32_t>(owner * kCtas) + half) +
+                                        static_cast<uint32_t>(((static_cast<int>(part) * p.owned + slot) * kLanes + f) * 4),
+                                    v[j]);
+                        if (++owner == split) owner = 0, ++slot;
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += bias;
+                activate(v, p.act);
+                Y *const y = static_cast<Y *>(p.y) + static_cast<int64_t>(row0 + c) * p.y_stride;
+                if (p.vec) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) turn[j * 32 + lane] = v[j];
+                    __syncwarp();
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const float4 z = *reinterpret_cast<const float4 *>(turn + (tr + 4 * t) * 32 + tc);
+                        const float w[4] = {z.x, z.y, z.z, z.w};
+                        Four<Y> o;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o.v[e] = from_f<Y>(p.residual ? w[e] + to_f(r[t].v[e]) : w[e]);
+                        Y *const at = y + (tr + 4 * t) * p.y_stride + col;
+                        if (c + tr + 4 * t >= valid) continue;
+                        if (whole) {
+                            *reinterpret_cast<Four<Y> *>(at) = o;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (col + e < end) at[e] = o.v[e];
+                        }
+                    }
+                } else if (feature < end) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < valid) y[j * p.y_stride + feature] = from_f<Y>(p.residual ? v[j] + to_f(r[j >> 2].v[j & 3]) : v[j]);
+                }
+            };
+            auto release = [&](int a) {  // the accumulator goes back to the products' warp
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair)
+                        mbar_arrive_remote(mapa_shared(bar_tempty + 8u * a, rank & ~1u));
+                    else
+                        mbar_arrive(bar_tempty + 8u * a);
+                }
+            };
+            auto column = [&](int a) { return tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT); };
+            if constexpr (kSum) {
+                float acc[kChunks][16];
+                for (int k0 = 0; ok && k0 < per; k0 += p.seg, ++n) {
+                    const int a = n & 1;
+                    ok = warp_wait<kPair>(bar_tfull + 8u * a, static_cast<uint32_t>(n >> 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int ci = 0; ci < kChunks; ++ci) {
+                        const int c = (2 * ci + g) * 16;
+                        if (c < valid) {
+                            float v[16];
+                            tmem_load16(column(a) + static_cast<uint32_t>(c), v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[ci][j] = k0 == 0 ? v[j] : acc[ci][j] + v[j];
+                        }
+                    }
+                    release(a);
+                }
+                if (split > 1 && !p.apart) cluster_sync_all();  // no CTA's ring is in use
+                if (!ok) break;
+#pragma unroll
+                for (int ci = 0; ci < kChunks; ++ci) {
+                    const int c = (2 * ci + g) * 16;
+                    if (c < valid) {
+                        Four<Y> r[4];
+                        fetch(c, r);
+                        finish(c, acc[ci], r);
                     }
                 }
-                group_sync(1 + g);
-            }
-            if (!ok) break;
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {  // the accumulator goes back to the products' warp
-                if constexpr (kPair)
-                    mbar_arrive_remote(mapa_shared(bar_tempty + 8u * a, 0));
-                else
-                    mbar_arrive(bar_tempty + 8u * a);
-            }
-        }
-    } else if constexpr (!kPair) {
-        // ---------------------------------------------------------------- a split tile: sums to shared memory (the ring
-        // is free: every product that read it is over)
-        const int g = (warp - 2) >> 2, q = warp & 3;
-        const bool got = mbar_wait(bar_tfull, 0, abort_flag);
-        __syncwarp();
-        if (__all_sync(0xFFFFFFFFu, got)) {
-            tc_fence_after_sync();
-            int tf, tt;
-            tile_of(team, tf, tt);
-            const int valid = min(NT, p.rows - tt * NT);
-            float *const sums = reinterpret_cast<float *>(gbase);
-            for (int c = g * 16; c < valid; c += 32) {
-                float v[16];
-                tmem_load16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c), v);
+            } else {
+                const int a = n & 1;
+                Four<Y> r[4];
+                if (g * 16 < valid) fetch(g * 16, r);
+                ok = warp_wait<kPair>(bar_tfull + 8u * a, static_cast<uint32_t>(n >> 1) & 1u, abort_flag);
+                ++n;
+                if (split > 1 && !p.apart) cluster_sync_all();  // no CTA's ring is in use
+                if (!ok) break;
+                tc_fence_after_sync();
+                for (int c = g * 16; c < valid; c += 32) {
+                    float v[16];
+                    tmem_load16(column(a) + static_cast<uint32_t>(c), v);
+                    Four<Y> next[4];
+                    if (c + 32 < valid) fetch(c + 32, next);
+                    finish(c, v, r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sums[(c + j) * kTileF + q * 32 + lane] = v[j];
+                    for (int t = 0; t < 4; ++t) r[t] = next[t];
+                }
+                release(a);
             }
         }
-        tc_fence_before_sync();
     }
-
+    if (warp < 2 && split > 1 && !p.apart) {
+        __syncwarp();
+        cluster_sync_all();
+    }
     __syncwarp();
-    if constexpr (kPair) {
-        cluster_sync_all();  // the pair's products, copies and arrivals are over
-    } else if (split > 1) {
-        cluster_sync_all();  // every CTA's sums are in its shared memory
+
+    if (split > 1) {
+        // the CTAs that share a tile share its rows too: a warp a row, summed in the order of the parts
+        const int n0 = first_feature(tf0), valid = min(NT, p.rows - tt0 * NT), end = min(p.n, n0 + F);
+        const int slot0 = warp - 2, row0 = static_cast<int>(part) + slot0 * split;
+        const RowStore<T, Y> out(p, lane, n0, end);
+        Four<Y> r;
+        if (p.residual && warp >= 2 && row0 < valid) out.fetch(tt0 * NT + row0, r);
+        cluster_sync_all();  // everything has arrived, and products, copies and arrivals are over
         if (warp >= 2) {
-            // each CTA joins its share of the tile's rows, a warp a row, in the order of the ranks
-            int tf, tt;
-            tile_of(team, tf, tt);
-            const int valid = min(NT, p.rows - tt * NT);
-            const RowStore<T, Y> out(p, lane, tf * kTileF);
-            uint32_t peer[kMaxSplit];
-#pragma unroll
-            for (int s = 0; s < kMaxSplit; ++s) peer[s] = s < split ? mapa_shared(base, s) : 0u;
-            for (int j = static_cast<int>(rank) + split * (warp - 2); j < valid; j += split * 8) {
-                Four<Y> r;
-                if (p.residual) out.fetch(tt * NT + j, r);
+            const float *const mine = reinterpret_cast<const float *>(gbase + (p.apart ? lay.extra : 0u)) + lane * 4;
+            for (int slot = slot0; static_cast<int>(part) + slot * split < valid; slot += 8) {
+                const int row = tt0 * NT + static_cast<int>(part) + slot * split;
+                if (p.residual && slot != slot0) out.fetch(row, r);
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < kMaxSplit; ++s) {
-                    if (s >= split) continue;
-                    if (p.vec) {
-                        const float4 f = ld_peer(peer[s] + static_cast<uint32_t>(j * kTileF + lane * 4) * 4u);
-                        z[0] += f.x, z[1] += f.y, z[2] += f.z, z[3] += f.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float f;
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                         : "=f"(f)
-                                         : "r"(peer[s] + static_cast<uint32_t>(j * kTileF + lane + 32 * e) * 4u)
-                                         : "memory");
-                            z[e] += f;
-                        }
+                for (int s = 0; s < kMaxSplit; ++s)
+                    if (s < split) {
+                        const float4 v = *reinterpret_cast<const float4 *>(mine + (s * p.owned + slot) * kLanes);
+                        z[0] += v.x, z[1] += v.y, z[2] += v.z, z[3] += v.w;
                     }
-                }
-                out.store(tt * NT + j, z, r);
+                out.store(row, z, r);
             }
         }
-        __syncwarp();
-        cluster_sync_all();  // no CTA ends while another reads its sums
+    } else if constexpr (kPair) {
+        cluster_sync_all();  // the pair's products, copies and arrivals are over
     } else {
         __syncthreads();
     }
@@ -521,72 +670,93 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
 }
 
-// How a call is cut: tiles of NT rows, by CTA pairs or by clusters of `split` CTAs.
+// How a call is cut: tiles of NT rows by F weight rows of a CTA, or of both CTAs of a pair, `split` of which share k.
 struct Plan {
-    int pair, NT, split, boxes, stages, grid;  // grid: clusters
+    int pair, F, NT, split, boxes, stages, grid;  // grid: clusters
+    int apart = 0;   // a split tile's sums have a place of their own
+    int owned() const { return (NT + split - 1) / split; }
 };
 
 struct Machine {
-    int sms = 0, smem = 0;              // SMs, dynamic shared memory of a block
-    int pairs = 0;                      // CTA pairs that run at a time
-    int clusters[2][kMaxSplit + 1] = {};  // clusters of that many CTAs with all of an SM's shared memory, or half of it, each
+    int sms = 0, smem = 0;                // SMs, dynamic shared memory of a block
+    int clusters[2][kMaxSplit + 1] = {};  // clusters of that many CTAs that run at a time: of single CTAs, of pairs
 };
-
-constexpr int kHalfSmem = 113 * 1024;  // two blocks fit an SM
 
 int smem_of(const Plan &pl)
 {
-    return static_cast<int>(layout(pl.NT, pl.boxes, pl.stages, pl.pair, pl.split).total) + 1024;  // (alignment)
+    return static_cast<int>(layout(pl.F, pl.NT, pl.boxes, pl.stages, pl.pair, pl.split, pl.owned(), pl.apart).total) + 1024;  // (alignment)
 }
 
-// The ring: as many stages as shared memory holds or the CTA's share of k takes. False if the plan does not fit.
+// The ring's stages. False if the plan does not fit.
 bool fit_stages(Plan &pl, int KB64, const Machine &m)
 {
-    pl.boxes = 1;
-    pl.stages = 0;
-    const int fixed = smem_of(pl), stage = static_cast<int>(layout(pl.NT, 1, 1, pl.pair, pl.split).stage);
-    int most = (m.smem - fixed) / (stage + 16);
     const int need = (KB64 + pl.split - 1) / pl.split;
-    if (most >= 8 && need >= 8) {  // fewer, larger stages: half the barriers
-        pl.boxes = 2;
-        most /= 2;
-    }
+    const int box = static_cast<int>(layout(pl.F, pl.NT, 1, 1, pl.pair, pl.split, 0, 0).stage);
+    // stages of up to 4 boxes and 32 KB: fewer barriers, and longer pieces of W's rows
+    pl.boxes = 1;
+    while (pl.boxes < 4 && 2 * pl.boxes * box <= 40 * 1024 && 4 * pl.boxes <= need) pl.boxes *= 2;
     const int KB = (KB64 + pl.boxes - 1) / pl.boxes;
+    const int stage = pl.boxes * box;
+    if (KB < pl.split) return false;
+    // a split tile's sums have a place of their own where that is small, else in the ring
+    const int sums = pl.split > 1 ? pl.split * pl.owned() * kLanes * 4 : 0;
+    pl.apart = pl.split > 1 && sums <= 36 * 1024;
+    pl.stages = 0;
+    int most = (m.smem - smem_of(pl)) / (stage + 16);
     int use = (KB + pl.split - 1) / pl.split;
     if (use > most) use = most;
-    // (a split tile's sums take NT * 512 bytes of the ring)
-    while (pl.split > 1 && use * pl.boxes * stage < pl.NT * kTileF * 4) ++use;
+    while (pl.split > 1 && !pl.apart && use * stage < sums) ++use;
     pl.stages = use;
-    return use >= 1 && use <= most && KB >= pl.split;
+    return use >= 1 && smem_of(pl) <= m.smem;
 }
 
-Plan choose(int64_t rows, int64_t n, int64_t k, const Machine &m)
+// A plan's time in microseconds but for a constant: a fit to 3,000 plans of 35 shapes (1 to 12,000 rows, n 128 to
+// 151,936, k 512 to 16,000), by which the chosen plan is 2 % slower than the fastest on average and 12 % at most.
+double cost(const Plan &pl, int64_t rows, int64_t n, int64_t k, int KB64, int64_t items)
+{
+    const int ctas = pl.pair ? 2 : 1;
+    const double rounds = pl.split > 1 ? 1 : static_cast<double>((items + pl.grid - 1) / pl.grid);
+    const double steps = static_cast<double>((KB64 + pl.split - 1) / pl.split);  // of 64 columns
+    const double xr = static_cast<double>(pl.NT / ctas < rows ? pl.NT / ctas : rows);
+    const double valid = static_cast<double>(pl.NT < rows ? pl.NT : rows);
+    // a step: its products, which follow one another, and what the SM takes in for them, in L4
+    const double mma = pl.NT * 0.001 > 0.127 ? pl.NT * 0.001 : 0.127;
+    const double in = pl.F / 940.0 + xr / 615.0;
+    const double step = sqrt(sqrt(mma * mma * mma * mma + in * in * in * in));
+    const double chain = rounds * steps * step, hbm = static_cast<double>(n) * k * 2 / 9e6;
+    // the epilogue of the last tile; with a short k also those that the next tile's products do not cover
+    const double epilogue = 0.0113 * valid, late = 1.36 * epilogue - steps * step;
+    double t = sqrt(chain * chain + hbm * hbm) + 0.0084 * pl.grid * pl.split * ctas + (pl.pair ? 1.25 : 0);
+    t += pl.split > 1 ? 0.375 + 0.026 * pl.split + 0.147 * ((pl.NT < rows ? pl.NT : static_cast<int>(rows)) + pl.split - 1) / pl.split + 0.5 * epilogue
+                      : epilogue;
+    return late > 0 ? t + late * (rounds - 1) : t;
+}
+
+Plan choose(int64_t rows, int64_t n, int64_t k, bool sum, const Machine &m)
 {
     const int KB64 = static_cast<int>((k + kBox - 1) / kBox);
     Plan best = {};
     double best_t = 0;
+    const int widest = sum ? kMaxSum : 256;
+    const int most = static_cast<int>(rows < widest ? (rows + 15) / 16 * 16 : widest);
     for (int pair = 0; pair < 2; ++pair) {
-        if (pair && (rows <= 64 || m.pairs < 1)) continue;
-        const int F = pair ? 2 * kTileF : kTileF;
-        const int64_t tf = (n + F - 1) / F;
-        for (int split = 1; split <= (pair ? 1 : kMaxSplit); ++split) {
-            const int most = static_cast<int>(rows < 256 ? (rows + 15) / 16 * 16 : 256);
+        const int ctas = pair ? 2 : 1;
+        if (pair && rows <= 32) continue;
+        for (int split = 1; split * ctas <= kMaxSplit; ++split) {
+            const int slots = m.clusters[pair][split * ctas];
+            if (slots < 1 || split > KB64) continue;
             for (int NT = most; NT >= 16; NT -= 16) {
-                Plan pl = {pair, NT, split, 1, 0, 0};
-                const int64_t items = tf * ((rows + pl.NT - 1) / pl.NT);
-                if (!fit_stages(pl, KB64, m)) continue;
-                const int slots = pair ? m.pairs : m.clusters[split > 1 && smem_of(pl) <= kHalfSmem][split];
-                if (slots < 1 || (split > 1 && items > slots)) continue;
-                pl.grid = static_cast<int>(items < slots ? items : slots);
-                const double rounds = static_cast<double>((items + slots - 1) / slots);
-                // clocks: a 64-column step's products, its loads from L2, everybody's share of HBM
-                const double mma = pl.NT, l2 = (kTileF + (pair ? pl.NT / 2 : pl.NT)) * 128 / 100.0;
-                const double hbm = (static_cast<double>(n) * k + static_cast<double>(rows) * k) * 2 / 3500.0;
-                const double steps = static_cast<double>((KB64 + split - 1) / split) * rounds;
-                double t = steps * (mma > l2 ? mma : l2);
-                if (hbm > t) t = hbm;
-                t += 1500 + pl.NT * 12 + (split > 1 ? 2500 : 0);
-                if (best_t == 0 || t < best_t) best = pl, best_t = t;
+                if (NT < most && rows <= 64) break;       // (more rows per weight cost nothing there)
+                if (rows > 512 && NT < 64) break;
+                for (int F = kLanes; F >= (rows <= 256 ? 16 : kLanes); F -= 8) {
+                    Plan pl = {pair, F, NT, split, 1, 0, 0};
+                    const int64_t items = (n + F * ctas - 1) / (F * ctas) * ((rows + NT - 1) / NT);
+                    if (split > 1 && items > slots) break;
+                    if (!fit_stages(pl, KB64, m)) continue;
+                    pl.grid = static_cast<int>(items < slots ? items : slots);
+                    const double t = cost(pl, rows, n, k, KB64, items);
+                    if (best_t == 0 || t < best_t) best = pl, best_t = t;
+                }
             }
         }
     }
@@ -616,7 +786,7 @@ template <typename T, typename Y>
 cudaError_t launch(const Plan &pl, const LinearParams &p, cudaStream_t s)
 {
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config(pl.grid, pl.pair ? 2 : pl.split, smem_of(pl), s, attr);
+    const cudaLaunchConfig_t cfg = config(pl.grid, (pl.pair ? 2 : 1) * pl.split, smem_of(pl), s, attr);
     return pl.pair ? cudaLaunchKernelEx(&cfg, linear_kernel<true, T, Y>, p) : cudaLaunchKernelEx(&cfg, linear_kernel<false, T, Y>, p);
 }
 
@@ -627,16 +797,16 @@ cudaError_t prepare(Machine &m)
     cudaError_t e = set_max_dynamic_smem(linear_kernel<true, T, Y>, m.smem);
     if (e == cudaSuccess) e = set_max_dynamic_smem(linear_kernel<false, T, Y>, m.smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = config(1, 2, m.smem, nullptr, attr);
-    e = cudaOccupancyMaxActiveClusters(&m.pairs, linear_kernel<true, T, Y>, &cfg);
-    if (e != cudaSuccess) return e;
     m.clusters[0][1] = m.sms;
-    for (int half = 0; half < 2; ++half)
-        for (int size = 2; size <= kMaxSplit; ++size) {
-            cfg = config(1, size, half ? kHalfSmem : m.smem, nullptr, attr);
-            if (cudaOccupancyMaxActiveClusters(&m.clusters[half][size], linear_kernel<false, T, Y>, &cfg) != cudaSuccess) {
+    for (int pair = 0; pair < 2; ++pair)
+        for (int size = 2; size <= kMaxSplit; size += pair + 1) {
+            const cudaLaunchConfig_t cfg = config(1, size, m.smem, nullptr, attr);
+            int *const to = &m.clusters[pair][size];
+            e = pair ? cudaOccupancyMaxActiveClusters(to, linear_kernel<true, T, Y>, &cfg)
+                     : cudaOccupancyMaxActiveClusters(to, linear_kernel<false, T, Y>, &cfg);
+            if (e != cudaSuccess) {
                 cudaGetLastError();
-                m.clusters[half][size] = 0;  // (such a cluster is not used)
+                *to = 0;  // (such a cluster is not used)
             }
         }
     return cudaSuccess;
@@ -679,9 +849,39 @@ struct dflash_linear_ctx {
     dfl::Machine m;
     int dev = 0;
     const void *W = nullptr, *bias = nullptr;
-    CUtensorMap tm_w;
+    CUtensorMap tm_w[dfl::kLanes / 8];  // by F / 8 - 1
     int *err = nullptr;
+    // the last call's rows and plan (rows << 32 | F / 8 << 16 | NT / 16 << 8 | split << 4 | pair): a step calls its layers
+    // with the same rows again, and looking through the plans takes some microseconds
+    std::atomic<uint64_t> plan{0};
 };
+
+namespace dfl {
+namespace {
+
+Plan plan_for(dflash_linear_ctx *h, int64_t rows)
+{
+    const uint64_t last = h->plan.load(std::memory_order_relaxed);
+    const int64_t n = h->cfg.n, k = h->cfg.k;
+    if (last >> 32 == static_cast<uint64_t>(rows)) {
+        Plan pl = {static_cast<int>(last & 15), static_cast<int>(last >> 16 & 255) * 8, static_cast<int>(last >> 8 & 255) * 16,
+                   static_cast<int>(last >> 4 & 15), 1, 0, 0};
+        const int ctas = pl.pair ? 2 : 1, slots = h->m.clusters[pl.pair][pl.split * ctas];
+        const int64_t items = (n + pl.F * ctas - 1) / (pl.F * ctas) * ((rows + pl.NT - 1) / pl.NT);
+        fit_stages(pl, static_cast<int>((k + kBox - 1) / kBox), h->m);
+        pl.grid = static_cast<int>(items < slots ? items : slots);
+        return pl;
+    }
+    const Plan pl = choose(rows, n, k, h->cfg.out_dtype == DFLASH_FP32, h->m);
+    if (pl.grid > 0)
+        h->plan.store(static_cast<uint64_t>(rows) << 32 | static_cast<uint64_t>(pl.F / 8) << 16 | static_cast<uint64_t>(pl.NT / 16) << 8 |
+                          static_cast<uint64_t>(pl.split) << 4 | static_cast<uint64_t>(pl.pair),
+                      std::memory_order_relaxed);
+    return pl;
+}
+
+}  // namespace
+}  // namespace dfl
 
 using dfl::linear_fail;
 
@@ -728,7 +928,8 @@ extern "C" dflash_status dflash_linear_init(const dflash_linear_config *cfg, con
                                  : dfl::prepare<__nv_bfloat16, __nv_bfloat16>(c->m));
     dflash_status st = DFLASH_OK;
     if (e == cudaSuccess) {
-        st = dfl::host_make_tmap_rows(&c->tm_w, W, cfg->n, cfg->k, cfg->n > 1 ? cfg->w_stride : (cfg->k + 7) / 8 * 8, dfl::kTileF);
+        for (int i = 0; st == DFLASH_OK && i < dfl::kLanes / 8; ++i)
+            st = dfl::host_make_tmap_rows(&c->tm_w[i], W, cfg->n, cfg->k, cfg->n > 1 ? cfg->w_stride : (cfg->k + 7) / 8 * 8, 8 * (i + 1));
         if (st != DFLASH_OK) {
             delete c;
             return st;
@@ -780,12 +981,12 @@ extern "C" dflash_status dflash_linear_run(dflash_linear_handle h, const void *x
          dfl::overlap(residual, rows, residual_stride * size, n * size, y, rows, y_stride * size, n * size)))
         return linear_fail(DFLASH_ERR_INVALID_ARG, "y must not overlap x, the weights, or a residual other than y itself");
 
-    const dfl::Plan pl = dfl::choose(rows, n, k, h->m);
-    if ((n + 127) / 128 * ((rows + pl.NT - 1) / pl.NT) >= (int64_t(1) << 31))
-        return linear_fail(DFLASH_ERR_INVALID_ARG, "too many tiles: %lld rows of %lld values", rows, n);
+    const dfl::Plan pl = dfl::plan_for(h, rows);
     if (pl.grid < 1) return linear_fail(DFLASH_ERR_UNSUPPORTED, "no tiling fits this device's shared memory");
+    if ((n + pl.F - 1) / pl.F * ((rows + pl.NT - 1) / pl.NT) >= (int64_t(1) << 31))
+        return linear_fail(DFLASH_ERR_INVALID_ARG, "too many tiles: %lld rows of %lld values", rows, n);
     dfl::LinearParams p;
-    p.tm_w = h->tm_w;
+    p.tm_w = h->tm_w[pl.F / 8 - 1];
     dflash_status st = dfl::host_make_tmap_rows(&p.tm_x, x, rows, k, x_stride, pl.pair ? pl.NT / 2 : pl.NT);
     if (st != DFLASH_OK) return st;
     p.bias = h->bias;
@@ -799,11 +1000,18 @@ extern "C" dflash_status dflash_linear_run(dflash_linear_handle h, const void *x
     p.boxes = pl.boxes;
     p.stages = pl.stages;
     p.KB = static_cast<int>((k + dfl::kBox * pl.boxes - 1) / (dfl::kBox * pl.boxes));
-    const int F = pl.pair ? 2 * dfl::kTileF : dfl::kTileF;
+    // (results in 32 bits: an accumulator takes 512 columns)
+    p.seg = h->cfg.out_dtype == DFLASH_FP32 ? 8 / pl.boxes : p.KB;
+    p.F = pl.F;
+    const int F = pl.pair ? 2 * pl.F : pl.F;
     p.tiles_f = static_cast<int>((n + F - 1) / F);
     p.tiles_t = static_cast<int>((rows + pl.NT - 1) / pl.NT);
     p.band = 8;
     p.split = pl.split;
+    p.kb_part = p.KB / pl.split;
+    p.kb_more = p.KB % pl.split;
+    p.owned = pl.owned();
+    p.apart = pl.apart;
     p.act = h->cfg.activation;
     const uintptr_t four = 4 * size;
     p.vec = !dfl::misaligned(y, four) && (rows == 1 || y_stride % 4 == 0) &&
