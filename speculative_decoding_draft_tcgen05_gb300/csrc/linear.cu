@@ -53,6 +53,7 @@ struct LinearParams {
     int apart;           // their sums have a place of their own, else in the ring
     int act;
     int vec;             // y and residual: 4 values at a time
+    int ahead;           // the residual's rows start on 16 bytes: they are brought to L2 while the products run
     int *err;
 };
 
@@ -62,13 +63,14 @@ constexpr int kThreads = 320;  // TMA, products, 8 epilogue warps
 constexpr int kLanes = 128;    // of TMEM: the most weight rows of a CTA
 constexpr int kBox = 64;       // columns of a box: 128 bytes
 constexpr int kMaxSplit = 8;
-constexpr int kMaxSum = 192;   // rows of x of a tile whose results are summed in registers
+constexpr int kMaxSum = 128;   // rows of x of a tile whose results are summed in registers
 
 struct Layout {
     uint32_t w, stage, bars, extra, total;
 };
 
-constexpr uint32_t kTurn = 16 * 32 * 4;  // 16 rows of 32 results, turned from a lane per column to a lane per four
+constexpr int kRows = 32;                   // rows of x that an epilogue warp finishes at a time
+constexpr uint32_t kTurn = kRows * 32 * 4;  // of 32 results each, turned from a lane per column to a lane per four
 
 __host__ __device__ inline Layout layout(int F, int NT, int boxes, int stages, bool pair, int split, int owned, int apart)
 {
@@ -232,11 +234,101 @@ __device__ __forceinline__ T from_f(float v)
     else return __float2bfloat16_rn(v);
 }
 
-// Four values of type Y, as they lie in memory.
+// Four values of type Y as they lie in memory: whole words, taken apart only where they are used (a load whose value is
+// taken apart at once holds up the loads behind it).
 template <typename Y>
 struct alignas(sizeof(Y) * 4) Four {
-    Y v[4];
+    uint32_t w[sizeof(Y)];
+
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (std::is_same_v<Y, float>) {
+            return __uint_as_float(w[i]);
+        } else {
+            const uint16_t h = static_cast<uint16_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+            if constexpr (std::is_same_v<Y, __half>) return __half2float(__ushort_as_half(h));
+            else return __uint_as_float(static_cast<uint32_t>(h) << 16);
+        }
+    }
+    __device__ __forceinline__ void put(int i, Y y)
+    {
+        if constexpr (std::is_same_v<Y, float>) {
+            w[i] = __float_as_uint(y);
+        } else {
+            uint16_t h;
+            if constexpr (std::is_same_v<Y, __half>) h = __half_as_ushort(y);
+            else h = __bfloat16_as_ushort(y);
+            w[i >> 1] = i & 1 ? (w[i >> 1] & 0xFFFFu) | static_cast<uint32_t>(h) << 16 : (w[i >> 1] & 0xFFFF0000u) | h;
+        }
+    }
+    // what the n values at `at` are, or four of them as one
+    __device__ __forceinline__ void load(const Y *at, bool whole, int n)
+    {
+        if (whole) {
+            *this = *reinterpret_cast<const Four *>(at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) put(i, at[i]);
+        }
+    }
+    __device__ __forceinline__ void store(Y *at, bool whole, int n) const
+    {
+        if (whole) {
+            *reinterpret_cast<Four *>(at) = *this;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) at[i] = from_f<Y>(get(i));
+        }
+    }
 };
+
+template <typename Y>
+__device__ __forceinline__ Four<Y> pack(float4 z)
+{
+    Four<Y> o;
+    if constexpr (std::is_same_v<Y, float>) {
+        o.w[0] = __float_as_uint(z.x), o.w[1] = __float_as_uint(z.y), o.w[2] = __float_as_uint(z.z), o.w[3] = __float_as_uint(z.w);
+    } else if constexpr (std::is_same_v<Y, __half>) {
+        const __half2 a = __floats2half2_rn(z.x, z.y), b = __floats2half2_rn(z.z, z.w);
+        o.w[0] = *reinterpret_cast<const uint32_t *>(&a), o.w[1] = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(z.x, z.y), b = __floats2bfloat162_rn(z.z, z.w);
+        o.w[0] = *reinterpret_cast<const uint32_t *>(&a), o.w[1] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return o;
+}
+
+// 32 consecutive columns of this thread's TMEM lane, or the first 16 of them.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32], bool all)
+{
+    uint32_t r[32];
+#define DFL_LD16(at, i)                                                                                                  \
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "    \
+                 "%14, %15}, [%16];\n"                                                                                    \
+                 : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),            \
+                   "=r"(r[i + 6]), "=r"(r[i + 7]), "=r"(r[i + 8]), "=r"(r[i + 9]), "=r"(r[i + 10]), "=r"(r[i + 11]),      \
+                   "=r"(r[i + 12]), "=r"(r[i + 13]), "=r"(r[i + 14]), "=r"(r[i + 15])                                    \
+                 : "r"(at)                                                                                               \
+                 : "memory")
+    __syncwarp();
+    DFL_LD16(taddr, 0);
+    if (all) {
+        DFL_LD16(taddr + 16u, 16);
+    } else {
+#pragma unroll
+        for (int i = 16; i < 32; ++i) r[i] = 0u;
+    }
+#undef DFL_LD16
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // (what is loaded is read after the wait)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        v[i] = __uint_as_float(r[i]);
+    }
+}
 
 // A row of a tile's results by one warp, four adjacent features a lane.
 template <typename T, typename Y>
@@ -259,31 +351,19 @@ struct RowStore {
     // this lane's values of the residual's row
     __device__ __forceinline__ void fetch(int row, Four<Y> &r) const
     {
-        const Y *at = static_cast<const Y *>(p.residual) + static_cast<int64_t>(row) * p.residual_stride;
-        if (whole) {
-            r = *reinterpret_cast<const Four<Y> *>(at + n0 + lane * 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (feature(i) < n1) r.v[i] = at[feature(i)];
-        }
+        r.load(static_cast<const Y *>(p.residual) + static_cast<int64_t>(row) * p.residual_stride + feature(0), whole, n1 - feature(0));
     }
 
     __device__ __forceinline__ void store(int row, const float (&acc)[4], const Four<Y> &r) const
     {
         float z[4] = {acc[0] + bias[0], acc[1] + bias[1], acc[2] + bias[2], acc[3] + bias[3]};
         activate(z, p.act);
-        Four<Y> o;
+        if (p.residual) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o.v[i] = from_f<Y>(p.residual ? z[i] + to_f(r.v[i]) : z[i]);
-        Y *at = static_cast<Y *>(p.y) + static_cast<int64_t>(row) * p.y_stride;
-        if (whole) {
-            *reinterpret_cast<Four<Y> *>(at + n0 + lane * 4) = o;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (feature(i) < n1) at[feature(i)] = o.v[i];
+            for (int i = 0; i < 4; ++i) z[i] += r.get(i);
         }
+        pack<Y>(make_float4(z[0], z[1], z[2], z[3]))
+            .store(static_cast<Y *>(p.y) + static_cast<int64_t>(row) * p.y_stride + feature(0), whole, n1 - feature(0));
     }
 };
 
@@ -476,91 +556,99 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
     } else {
         // ---------------------------------------------------------------- epilogue: a thread has a weight row's results;
-        // the two warps of a lane quadrant take turns at a tile's chunks of 16 rows of x
+        // the two warps of a lane quadrant take turns at 32 of a tile's rows of x
         const int g = (warp - 2) >> 2, q = warp & 3, f = q * 32 + lane;
         // results in 32 bits are summed in registers over the accumulators
         constexpr bool kSum = std::is_same_v<Y, float>;
-        constexpr int kChunks = kMaxSum / 32;  // of a warp, at most
+        constexpr int kSteps = kMaxSum / (2 * kRows);  // of a warp, at most
         float *const turn = reinterpret_cast<float *>(gbase + lay.extra + (warp - 2) * kTurn);
         const uint32_t mail = base + (p.apart ? lay.extra : 0u);  // where the parts of a split tile arrive
         const int tr = lane >> 3, tc = (lane & 7) * 4;            // turned: rows tr + 4 t, features tc .. tc + 3
         int n = 0;
         bool ok = true;
+        // A tile's residual, 32 rows a warp: whole rows of it to L2, since what the warps fetch of a row (64 bytes) is less
+        // than HBM serves well (8192 rows, n = 10240, k = 2560: 350 us without)
+        auto bring = [&](int i) {
+            int tf, tt;
+            tile_of(i, tf, tt);
+            const int n0 = first_feature(tf), row = tt * NT + (warp - 2) * 32 + lane;
+            const uint32_t bytes = static_cast<uint32_t>(max(0, min(p.n, n0 + F) - n0)) * sizeof(Y) & ~15u;
+            if ((warp - 2) * 32 + lane < NT && row < p.rows && bytes > 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const Y *>(p.residual) +
+                                                                                static_cast<int64_t>(row) * p.residual_stride + n0),
+                             "r"(bytes)
+                             : "memory");
+        };
+        if (p.ahead && team < items) bring(team);
         for (int i = team; ok && i < items; i += teams) {
             int tf, tt;
             tile_of(i, tf, tt);
+            if (p.ahead && i + teams < items) bring(i + teams);
             const int n0 = first_feature(tf), feature = n0 + f;
             const int end = min(p.n, n0 + F);  // behind the CTA's last feature
             const int row0 = tt * NT, valid = q * 32 < F ? min(NT, p.rows - row0) : 0;
             const float bias = p.bias && feature < end ? to_f(static_cast<const T *>(p.bias)[feature]) : 0.f;
             const bool whole = p.vec && n0 + q * 32 + tc + 3 < end;
             const int64_t col = n0 + q * 32 + tc;
-            // the residual of a chunk: as it is turned (four values of four rows), or the thread's own column
-            auto fetch = [&](int c, Four<Y> (&r)[4]) {
+            // the residual of 32 rows: as it is turned (four values of eight rows), or the thread's own column
+            auto fetch = [&](int c, Four<Y> (&r)[8]) {
                 if (!p.residual || split > 1) return;
                 const Y *const res = static_cast<const Y *>(p.residual) + static_cast<int64_t>(row0 + c) * p.residual_stride;
                 if (p.vec) {
+                    const Y *const at = res + tr * p.residual_stride + col;
+                    const int rows = valid - c - tr;  // (this lane's rows are 4 t < rows)
+                    if (whole) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const Y *const at = res + (tr + 4 * t) * p.residual_stride + col;
-                        if (c + tr + 4 * t >= valid) continue;
-                        if (whole) {
-                            r[t] = *reinterpret_cast<const Four<Y> *>(at);
-                        } else {
+                        for (int t = 0; t < 8; ++t)
+                            if (4 * t < rows) r[t].load(at + 4 * t * p.residual_stride, true, 4);
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (col + e < end) r[t].v[e] = at[e];
-                        }
+                        for (int t = 0; t < 8; ++t)
+                            if (4 * t < rows) r[t].load(at + 4 * t * p.residual_stride, false, end - static_cast<int>(col));
                     }
                 } else if (feature < end) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < valid) r[j >> 2].v[j & 3] = res[j * p.residual_stride + feature];
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < valid) r[j >> 2].put(j & 3, res[j * p.residual_stride + feature]);
                 }
             };
-            auto finish = [&](int c, float (&v)[16], const Four<Y> (&r)[4]) {
+            auto finish = [&](int c, float (&v)[32], const Four<Y> (&r)[8]) {
                 if (split > 1) {  // to the CTA that joins the row
                     int slot = c / split, owner = c - slot * split;
+                    const uint32_t to = mail + static_cast<uint32_t>((static_cast<int>(part) * p.owned * kLanes + f) * 4);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (c + j < valid)
-                            st_peer(mapa_shared(mail, static_cast<uint32_t>(owner * kCtas) + half) +
-                                        static_cast<uint32_t>(((static_cast<int>(part) * p.owned + slot) * kLanes + f) * 4),
-                                    v[j]);
-                        if (++owner == split) owner = 0, ++slot;
+                    for (int h = 0; h < 32; h += 8) {
+                        if (c + h >= valid) break;
+#pragma unroll
+                        for (int j = h; j < h + 8; ++j) {
+                            if (c + j < valid)
+                                st_peer(mapa_shared(to + static_cast<uint32_t>(slot * kLanes * 4), static_cast<uint32_t>(owner * kCtas) + half), v[j]);
+                            if (++owner == split) owner = 0, ++slot;
+                        }
                     }
                     return;
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += bias;
+                for (int j = 0; j < 32; ++j) v[j] += bias;
                 activate(v, p.act);
                 Y *const y = static_cast<Y *>(p.y) + static_cast<int64_t>(row0 + c) * p.y_stride;
                 if (p.vec) {
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) turn[j * 32 + lane] = v[j];
+                    for (int j = 0; j < 32; ++j) turn[j * 32 + lane] = v[j];
                     __syncwarp();
+                    Y *const y0 = y + tr * p.y_stride + col;
+                    const int rows = valid - c - tr;  // (this lane's rows are 4 t < rows)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float4 z = *reinterpret_cast<const float4 *>(turn + (tr + 4 * t) * 32 + tc);
-                        const float w[4] = {z.x, z.y, z.z, z.w};
-                        Four<Y> o;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o.v[e] = from_f<Y>(p.residual ? w[e] + to_f(r[t].v[e]) : w[e]);
-                        Y *const at = y + (tr + 4 * t) * p.y_stride + col;
-                        if (c + tr + 4 * t >= valid) continue;
-                        if (whole) {
-                            *reinterpret_cast<Four<Y> *>(at) = o;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (col + e < end) at[e] = o.v[e];
-                        }
+                    for (int t = 0; t < 8; ++t) {
+                        float4 z = *reinterpret_cast<const float4 *>(turn + (tr + 4 * t) * 32 + tc);
+                        if (p.residual) z.x += r[t].get(0), z.y += r[t].get(1), z.z += r[t].get(2), z.w += r[t].get(3);
+                        if (4 * t < rows) pack<Y>(z).store(y0 + 4 * t * p.y_stride, whole, end - static_cast<int>(col));
                     }
                 } else if (feature < end) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < valid) y[j * p.y_stride + feature] = from_f<Y>(p.residual ? v[j] + to_f(r[j >> 2].v[j & 3]) : v[j]);
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < valid) y[j * p.y_stride + feature] = from_f<Y>(p.residual ? v[j] + r[j >> 2].get(j & 3) : v[j]);
                 }
             };
             auto release = [&](int a) {  // the accumulator goes back to the products' warp
@@ -575,20 +663,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             };
             auto column = [&](int a) { return tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT); };
             if constexpr (kSum) {
-                float acc[kChunks][16];
+                float acc[kSteps][32];
                 for (int k0 = 0; ok && k0 < per; k0 += p.seg, ++n) {
                     const int a = n & 1;
                     ok = warp_wait<kPair>(bar_tfull + 8u * a, static_cast<uint32_t>(n >> 1) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int ci = 0; ci < kChunks; ++ci) {
-                        const int c = (2 * ci + g) * 16;
+                    for (int ci = 0; ci < kSteps; ++ci) {
+                        const int c = (2 * ci + g) * kRows;
                         if (c < valid) {
-                            float v[16];
-                            tmem_load16(column(a) + static_cast<uint32_t>(c), v);
+                            float v[32];
+                            tmem_load32(column(a) + static_cast<uint32_t>(c), v, c + 16 < NT);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[ci][j] = k0 == 0 ? v[j] : acc[ci][j] + v[j];
+                            for (int j = 0; j < 32; ++j) acc[ci][j] = k0 == 0 ? v[j] : acc[ci][j] + v[j];
                         }
                     }
                     release(a);
@@ -596,31 +684,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (split > 1 && !p.apart) cluster_sync_all();  // no CTA's ring is in use
                 if (!ok) break;
 #pragma unroll
-                for (int ci = 0; ci < kChunks; ++ci) {
-                    const int c = (2 * ci + g) * 16;
+                for (int ci = 0; ci < kSteps; ++ci) {
+                    const int c = (2 * ci + g) * kRows;
                     if (c < valid) {
-                        Four<Y> r[4];
+                        Four<Y> r[8];
                         fetch(c, r);
                         finish(c, acc[ci], r);
                     }
                 }
             } else {
                 const int a = n & 1;
-                Four<Y> r[4];
-                if (g * 16 < valid) fetch(g * 16, r);
+                Four<Y> r[8];
+                if (g * kRows < valid) fetch(g * kRows, r);
                 ok = warp_wait<kPair>(bar_tfull + 8u * a, static_cast<uint32_t>(n >> 1) & 1u, abort_flag);
                 ++n;
                 if (split > 1 && !p.apart) cluster_sync_all();  // no CTA's ring is in use
                 if (!ok) break;
                 tc_fence_after_sync();
-                for (int c = g * 16; c < valid; c += 32) {
-                    float v[16];
-                    tmem_load16(column(a) + static_cast<uint32_t>(c), v);
-                    Four<Y> next[4];
-                    if (c + 32 < valid) fetch(c + 32, next);
+                for (int c = g * kRows; c < valid; c += 2 * kRows) {
+                    float v[32];
+                    tmem_load32(column(a) + static_cast<uint32_t>(c), v, c + 16 < NT);
+                    Four<Y> next[8];
+                    if (c + 2 * kRows < valid) fetch(c + 2 * kRows, next);
                     finish(c, v, r);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) r[t] = next[t];
+                    for (int t = 0; t < 8; ++t) r[t] = next[t];
                 }
                 release(a);
             }
@@ -1016,6 +1104,7 @@ extern "C" dflash_status dflash_linear_run(dflash_linear_handle h, const void *x
     const uintptr_t four = 4 * size;
     p.vec = !dfl::misaligned(y, four) && (rows == 1 || y_stride % 4 == 0) &&
             (!residual || (!dfl::misaligned(residual, four) && (rows == 1 || residual_stride % 4 == 0)));
+    p.ahead = residual && pl.split == 1 && !dfl::misaligned(residual, 16) && (rows == 1 || residual_stride * size % 16 == 0);
     p.err = h->err;
     const auto s = static_cast<cudaStream_t>(stream);
     const bool half = h->cfg.dtype == DFLASH_FP16, wide = size == 4;
