@@ -1,16 +1,20 @@
 // The target's logits under penalties for repeated tokens, biases and a mask;
 // from them softmax, the best token, or the logits.
 //
-// A cluster of C CTAs takes some positions of one sequence; each CTA has a
-// slice of the vocabulary. What depends on the sequence alone is laid out once
-// in shared memory, a word per token of the slice: how often it has occurred,
-// and its place in the list of biases. Then one pass over the slice per
-// position finds the best token and, relative to the running maximum, the sum
-// of the exponentials; the CTAs exchange those through distributed shared
-// memory, and a second pass, whose logits come from L2, writes the
-// probabilities. So HBM sees the logits once and the outputs once, which is
-// what bounds a large batch; a small one is bound by the chain history ->
-// table -> logits -> exchange.
+// A cluster of C CTAs takes some positions of one sequence; its CTAs take turns
+// at pieces of 2048 tokens, so that the frequent ones, which vocabularies have
+// at their beginning, are everybody's. A CTA's logits come to shared memory by
+// bulk copies: all of them under way at once (loads into registers, a step
+// ahead, kept 20 KB an SM under way and took twice as long), and read once from
+// HBM for both passes over them. Few tokens have occurred or have a bias (a
+// percent), so they are a list, laid out once per sequence from a table of
+// occurrences in shared memory, a thread an entry, and left out of the passes
+// over all the others: the first finds the best token and, relative to each
+// thread's running maximum, the sum of the exponentials; the warps of all CTAs
+// exchange those through distributed shared memory, with one cluster barrier;
+// the second writes the probabilities. HBM sees the logits and the outputs
+// once, which is what bounds a large batch; a small one is bound by the chain
+// history -> table -> list -> exchange.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdio.h>
@@ -28,12 +32,14 @@ dflash_status host_fail(dflash_status st, const char *msg);
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 8;                  // tokens of a lane in a step
-constexpr int kStep = kThreads * kPer;   // tokens of a CTA in a step
+constexpr int kLogStep = 11;
+constexpr int kStep = 1 << kLogStep;     // tokens of a CTA in a step
+static_assert(kStep == kThreads * kPer, "a step is a piece");
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kInPrompt = 0x80000000u;
+constexpr int kMaxList = 2048;           // tokens of a CTA on its list; with more it goes by the bits
 
 struct LogitsParams {
     const void *logits;
@@ -43,8 +49,9 @@ struct LogitsParams {
     int64_t seq_stride, row_stride, out_seq_stride, out_row_stride;
     int64_t vocab;
     int batch, rows, group, groups;  // positions of a cluster, clusters of a sequence
-    int slice;                       // tokens of a CTA, a multiple of 256
-    int C;
+    int slice;                       // tokens of a CTA, a multiple of kStep
+    int most, wide;                  // entries that a CTA's list can have; 32 bits an entry of a table, not 16
+    int C, log_c;
     dflash_logits_rules r;
     const int32_t *draft;
     int64_t draft_stride;
@@ -53,19 +60,11 @@ struct LogitsParams {
     int counted, biased;             // there are tokens (or drafts) that penalties count; there are biases
 };
 
-struct Best {
+struct alignas(16) Best {
     float m, s;   // maximum and sum of exp((x - m) / tau)
     float v;      // the largest x that is a number, and the lowest token that has it
     int id;
 };
-
-template <typename T>
-__device__ __forceinline__ float to_f(T v)
-{
-    if constexpr (std::is_same_v<T, float>) return v;
-    else if constexpr (std::is_same_v<T, __half>) return __half2float(v);
-    else return __bfloat162float(v);
-}
 
 template <typename T>
 __device__ __forceinline__ T from_f(float v)
@@ -75,28 +74,21 @@ __device__ __forceinline__ T from_f(float v)
     else return __float2bfloat16_rn(v);
 }
 
+// One of the two 16-bit values of a word.
 template <typename T>
-struct alignas(16) Vec {
-    T v[16 / sizeof(T)];
-};
+__device__ __forceinline__ float half_of(uint32_t w, int high)
+{
+    if constexpr (std::is_same_v<T, __half>)
+        return __half2float(__ushort_as_half(static_cast<uint16_t>(high ? w >> 16 : w)));
+    else
+        return __uint_as_float(high ? w & 0xFFFF0000u : w << 16);
+}
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// (m, s) of two parts; scale = log2(e) / tau
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, float scale)
-{
-    const float top = fmaxf(m, m2);
-    if (top == -INFINITY) {  // (a NaN in s or s2 stays: m is then not its maximum)
-        s += s2;
-        return;
-    }
-    s = (m == top ? s : s * exp2_fast((m - top) * scale)) + (m2 == top ? s2 : s2 * exp2_fast((m2 - top) * scale));
-    m = top;
 }
 
 __device__ __forceinline__ void join_best(float &v, int &id, float v2, int id2)
@@ -107,343 +99,588 @@ __device__ __forceinline__ void join_best(float &v, int &id, float v2, int id2)
     }
 }
 
-template <typename T, bool kVec>
-struct Slice {
-    const LogitsParams &p;
-    const uint32_t *counts, *bias;   // shared memory (or unused)
-    int64_t v0, v1;                  // the CTA's tokens
-    float rho, alpha, beta;
-    const float *bias_values;        // the sequence's
+// Over the warp: the maximum and the sum relative to it (a sum that is no number stays one), the best token.
+__device__ __forceinline__ void reduce(Best &q, float scale, bool sum, bool best)
+{
+    if (sum) {
+        const float m = ordered_to_f32(__reduce_max_sync(0xFFFFFFFFu, f32_to_ordered(q.m)));  // (never NaN)
+        q.s = q.m == m ? q.s : q.s * exp2_fast((q.m - m) * scale);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) q.s += __shfl_xor_sync(0xFFFFFFFFu, q.s, o);
+        q.m = m;
+    }
+    if (best) {
+        const float v = ordered_to_f32(__reduce_max_sync(0xFFFFFFFFu, f32_to_ordered(q.v)));
+        q.id = __reduce_min_sync(0xFFFFFFFFu, q.v == v ? q.id : 0x7FFFFFFF);
+        q.v = v;
+    }
+}
 
-    // Token j of this lane's step at `at` (the warp's first token).
-    __device__ __forceinline__ int64_t token(int64_t at, int lane, int j) const
+// Shared memory in words: a position's logits; the mask's bits; bits of the tokens on the list (marks) and of those with a
+// bias (listed); the list; a table of what has occurred, which the list is made from; places in the list of biases. Entries of
+// a table are 32 bits (wide) or 16: the highest says that the token is in the prompt, the others how often it has occurred
+// behind it. (Two positions' logits, one on its way beside the other, left room for fewer CTAs: 230 us against 115 for 256
+// positions of 151,936 tokens after 8000.)
+struct Room {
+    int logits, bits, list, counts, bias, total;
+};
+
+__host__ __device__ inline Room room_of(int slice, int size, int most, bool counted, bool biased, bool wide)
+{
+    Room r = {slice / 4 * size, slice / 32, 0, 0, 0, 0};
+    r.total = r.logits + r.bits;
+    if (!counted && !biased) return r;
+    const int table = wide ? slice : slice / 2;
+    r.list = ((most < kMaxList ? most : kMaxList) + 3) / 4 * (wide ? 8 : 4);
+    r.counts = counted ? table : 0;
+    r.bias = biased ? table : 0;
+    r.total += 2 * r.bits + r.list + r.bias + r.counts;
+    return r;
+}
+
+// A CTA's tokens on the list. Tokens go by their index in the CTA's own.
+struct Marked {
+    uint32_t *marks, *listed, *list, *counts, *bias;
+    bool wide;
+
+    __device__ __forceinline__ uint32_t get(const uint32_t *table, int at) const
     {
-        return kVec ? at + lane * kPer + j : at + j * 32 + lane;
+        return wide ? table[at] : table[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
+    }
+    __device__ __forceinline__ bool bit(const uint32_t *bits, int at) const { return bits[at >> 5] >> (at & 31) & 1u; }
+
+    // One more token that has occurred (fewer than 2^15 without `wide`, so that no count runs over).
+    __device__ __forceinline__ void occurred(int at, bool prompt) const
+    {
+        if (wide) {
+            if (prompt) atomicOr(counts + at, 0x80000000u);
+            else atomicAdd(counts + at, 1u);
+        } else {
+            const int sh = 16 * (at & 1);
+            if (prompt) atomicOr(counts + (at >> 1), 0x8000u << sh);
+            else atomicAdd(counts + (at >> 1), 1u << sh);
+        }
+    }
+    // how often, of an entry that is not 0
+    __device__ __forceinline__ float times(uint32_t entry) const { return static_cast<float>(entry & (wide ? 0x7FFFFFFFu : 0x7FFFu)); }
+
+    __device__ __forceinline__ void has_bias(int at, uint32_t place) const  // the last one counts
+    {
+        atomicOr(listed + (at >> 5), 1u << (at & 31));
+        if (wide) {
+            atomicMax(bias + at, place);
+            return;
+        }
+        uint32_t *const word = bias + (at >> 1);
+        const int sh = 16 * (at & 1);
+        for (uint32_t old = *word; (old >> sh & 0xFFFFu) < place;) {
+            const uint32_t was = atomicCAS(word, old, (old & ~(0xFFFFu << sh)) | place << sh);
+            if (was == old) break;
+            old = was;
+        }
     }
 
-    __device__ __forceinline__ void load(const T *row, int64_t at, int lane, float (&x)[kPer]) const
+    // which of 8 tokens from `at` on have occurred, a bit each
+    __device__ __forceinline__ uint32_t occurrences(int at) const
+    {
+        uint32_t m = 0;
+        if (wide) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m |= (counts[at + j] != 0u) << j;
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4 *>(counts + (at >> 1));
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            if (v[0] | v[1] | v[2] | v[3]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m |= ((v[j >> 1] >> (16 * (j & 1)) & 0xFFFFu) != 0u) << j;
+            }
+        }
+        return m;
+    }
+
+    __device__ __forceinline__ void put(int e, int at, uint32_t count) const
+    {
+        if (wide) list[2 * e] = static_cast<uint32_t>(at), list[2 * e + 1] = count;
+        else list[e] = static_cast<uint32_t>(at) | count << 16;
+    }
+    __device__ __forceinline__ int token(int e) const { return static_cast<int>(wide ? list[2 * e] : list[e] & 0xFFFFu); }
+    __device__ __forceinline__ uint32_t count(int e) const { return wide ? list[2 * e + 1] : list[e] >> 16; }
+};
+
+// A lane's 8 tokens of a step as they are loaded. kVec: adjacent ones, by 16 bytes; else every 32nd.
+template <typename T, bool kVec>
+struct Raw {
+    static constexpr int kWords = kVec && sizeof(T) == 2 ? 4 : 8;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ float get(int j) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        else if constexpr (kVec) return half_of<T>(w[j >> 1], j & 1);
+        else return half_of<T>(w[j], 0);
+    }
+
+    // at: the index of the lane's first token
+    __device__ __forceinline__ void load(const T *logits, int at)
     {
         if constexpr (kVec) {
-            const int64_t t = at + lane * kPer;
-            if (t < v1) {  // (v1 is a multiple of 8 where rows are)
-                constexpr int N = 16 / sizeof(T);
+            const uint4 *const from = reinterpret_cast<const uint4 *>(logits + at);
 #pragma unroll
-                for (int i = 0; i < kPer / N; ++i) {
-                    const Vec<T> q = *reinterpret_cast<const Vec<T> *>(row + t + i * N);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) x[i * N + j] = to_f(q.v[j]);
-                }
-                return;
+            for (int q = 0; q < kWords / 4; ++q) {
+                const uint4 x = from[q];
+                w[4 * q] = x.x, w[4 * q + 1] = x.y, w[4 * q + 2] = x.z, w[4 * q + 3] = x.w;
             }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) x[j] = -INFINITY;
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                const int64_t t = at + j * 32 + lane;
-                x[j] = t < v1 ? to_f(row[t]) : -INFINITY;
+                if constexpr (sizeof(T) == 4) w[j] = reinterpret_cast<const uint32_t *>(logits)[at + j * 32];
+                else w[j] = reinterpret_cast<const uint16_t *>(logits)[at + j * 32];
             }
         }
     }
 
-    // The rules on one value of a token that has occurred.
-    __device__ __forceinline__ float repeated(float x, uint32_t word) const
+    // a bit each for the lane's tokens
+    static __device__ __forceinline__ uint32_t bits(const uint32_t *from, int at)
     {
-        x = x > 0.f ? __fdiv_rn(x, rho) : __fmul_rn(x, rho);
-        const uint32_t c = word & ~kInPrompt;
-        if (c) x = __fsub_rn(__fsub_rn(x, __fmul_rn(beta, static_cast<float>(c))), alpha);
-        return x;
+        if constexpr (kVec) return reinterpret_cast<const uint8_t *>(from)[at >> 3];
+        uint32_t r = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) r |= (from[(at >> 5) + j] >> (at & 31) & 1u) << j;
+        return r;
     }
 
-    __device__ __forceinline__ void adjust(const int32_t *mask, int64_t at, int lane, float (&x)[kPer]) const
+    // the values; -inf for those that `keep` leaves out
+    __device__ __forceinline__ void values(uint32_t keep, float2 (&x)[kPer / 2]) const
     {
-        const int local = static_cast<int>(at - v0);
-        if (counts) {
-            uint32_t w[kPer], any = 0;
-            if constexpr (kVec) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(counts + local + lane * kPer);
-                const uint4 b = *reinterpret_cast<const uint4 *>(counts + local + lane * kPer + 4);
-                w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-            } else {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) w[j] = counts[local + j * 32 + lane];
-            }
+        for (int j = 0; j < kPer / 2; ++j) x[j] = make_float2(get(2 * j), get(2 * j + 1));
+        if (keep != 0xFFu) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) any |= w[j];
-            if (any) {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (w[j]) x[j] = repeated(x[j], w[j]);
-            }
-        }
-        if (bias) {
-            uint32_t w[kPer], any = 0;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                w[j] = bias[kVec ? local + lane * kPer + j : local + j * 32 + lane];
-                any |= w[j];
-            }
-            if (any) {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (w[j]) x[j] = __fadd_rn(x[j], bias_values[w[j] - 1]);
-            }
-        }
-        if (mask) {
-            if constexpr (kVec) {
-                const int64_t t = at + lane * kPer;
-                const uint32_t bits = t < v1 ? static_cast<uint32_t>(mask[t >> 5]) >> (t & 31) : 0u;
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (!((bits >> j) & 1u)) x[j] = -INFINITY;
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int64_t t = at + j * 32;  // (a multiple of 32: one word for the warp)
-                    const uint32_t bits = t < v1 ? static_cast<uint32_t>(mask[t >> 5]) : 0u;
-                    if (!((bits >> lane) & 1u)) x[j] = -INFINITY;
-                }
+            for (int j = 0; j < kPer / 2; ++j) {
+                x[j].x = keep >> (2 * j) & 1u ? x[j].x : -INFINITY;
+                x[j].y = keep >> (2 * j + 1) & 1u ? x[j].y : -INFINITY;
             }
         }
     }
 };
 
+// Two fp32 operations by one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <bool kVec, typename Y>
+__device__ __forceinline__ void store8(Y *to, int v, int vocab, const float2 (&y)[kPer / 2])
+{
+    if constexpr (kVec) {
+        if (v >= vocab) return;
+        if constexpr (sizeof(Y) == 4) {
+            *reinterpret_cast<float4 *>(to + v) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+            *reinterpret_cast<float4 *>(to + v + 4) = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+        } else {
+            alignas(16) Y o[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer / 2; ++j) o[2 * j] = from_f<Y>(y[j].x), o[2 * j + 1] = from_f<Y>(y[j].y);
+            *reinterpret_cast<uint4 *>(to + v) = *reinterpret_cast<const uint4 *>(o);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (v + j * 32 < vocab) to[v + j * 32] = from_f<Y>(j & 1 ? y[j >> 1].y : y[j >> 1].x);
+    }
+}
+
+// x = exp2((x + less) * scale)
+__device__ __forceinline__ void exponentials(float2 (&x)[kPer / 2], float2 less, float2 scale)
+{
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) {
+        x[j] = mul2(add2(x[j], less), scale);
+        x[j] = make_float2(exp2_fast(x[j].x), exp2_fast(x[j].y));
+    }
+}
+
 struct Shared {
-    Best warp[kWarps];
-    Best peer[2][kMaxCluster];
-    Best all;
+    Best peer[2][kMaxCluster * kWarps];
+    uint64_t full;  // a position's logits have arrived
+    int abort_flag;
+    int warp_n[kWarps];
+    int n;  // entries of the list
 };
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitsParams p)
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitsParams p)
 {
     extern __shared__ uint4 smem[];
     __shared__ Shared s;
-    pdl_trigger();
-    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = p.C;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool tables = p.counted || p.biased;
+    const Room room = room_of(p.slice, sizeof(T), p.most, p.counted, p.biased, p.wide);
+    uint32_t *const words = reinterpret_cast<uint32_t *>(smem);
+    T *const logits = reinterpret_cast<T *>(words);
+    uint32_t *const mask = words + room.logits;
+    Marked mk;
+    mk.marks = mask + room.bits;
+    mk.listed = mk.marks + room.bits;
+    mk.list = mk.listed + room.bits;
+    mk.bias = mk.list + room.list;
+    mk.counts = mk.bias + room.bias;
+    mk.wide = p.wide;
+    if (tables) {
+        auto clear = [&](uint32_t *from, int n) {
+            for (int i = tid; i < n / 4; i += kThreads) reinterpret_cast<uint4 *>(from)[i] = make_uint4(0, 0, 0, 0);
+        };
+        if (p.counted) clear(mk.counts, room.counts);
+        if (p.biased) {
+            clear(mk.listed, room.bits);
+            clear(mk.bias, room.bias);
+        }
+    }
+    if (tid == 0) {
+        mbar_init(smem_u32(&s.full), 1);
+        s.abort_flag = 0;
+        s.n = 0;
+        fence_mbar_init();
+    }
     const int b = static_cast<int>(blockIdx.x) / p.groups, g = static_cast<int>(blockIdx.x) % p.groups;
     const int t0 = g * p.group, t1 = min(p.rows, t0 + p.group);
-    uint32_t *const counts = reinterpret_cast<uint32_t *>(smem);
-    uint32_t *const bias = counts + (p.counted ? p.slice : 0);
-
-    Slice<T, kVec> sl = {p, p.counted ? counts : nullptr, p.biased ? bias : nullptr, 0, 0, 1.f, 0.f, 0.f, nullptr};
-    sl.v0 = min(static_cast<int64_t>(rank) * p.slice, p.vocab);
-    sl.v1 = min(sl.v0 + p.slice, p.vocab);
-    const int width = static_cast<int>(sl.v1 - sl.v0);
-    if (p.r.repetition) sl.rho = p.r.repetition[b];
-    if (p.r.presence) sl.alpha = p.r.presence[b];
-    if (p.r.frequency) sl.beta = p.r.frequency[b];
-    const float tau = p.r.temperature ? p.r.temperature[b] : 1.f;
-
-    // what has occurred, and the biases' places
-    const int words = ((p.counted ? p.slice : 0) + (p.biased ? p.slice : 0)) / 4;
-    for (int i = tid; i < words; i += kThreads) smem[i] = make_uint4(0, 0, 0, 0);
-    if (words) __syncthreads();
-    auto place = [&](int32_t token) {  // the slice's index of a token, or -1
-        const int64_t at = static_cast<int64_t>(token) - sl.v0;
-        return at >= 0 && at < width ? static_cast<int>(at) : -1;
-    };
-    const int32_t *const draft = p.draft ? p.draft + b * p.draft_stride : nullptr;
-    if (p.counted) {
-        if (p.r.tokens) {
-            const int32_t *const tokens = p.r.tokens + b * p.r.token_stride;
-            const int len = min(max(p.r.lens[b], 0), p.r.token_cols);
-            const int prompt = p.r.prompt_lens ? p.r.prompt_lens[b] : 0;
-            for (int i0 = tid; i0 < len; i0 += 4 * kThreads) {
-                int32_t w[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) w[u] = i0 + u * kThreads < len ? tokens[i0 + u * kThreads] : -1;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int at = place(w[u]);
-                    if (at < 0) continue;
-                    if (i0 + u * kThreads < prompt)
-                        atomicOr(counts + at, kInPrompt);
-                    else
-                        atomicAdd(counts + at, 1u);
+    // the CTA's tokens: pieces rank, rank + C, .. of kStep
+    const int vocab = static_cast<int>(p.vocab), pieces = (vocab + kStep - 1) >> kLogStep;
+    const int mine = (pieces - rank + C - 1) >> p.log_c;
+    auto token_of = [&](int at) { return ((((at >> kLogStep) << p.log_c) + rank) << kLogStep) + (at & (kStep - 1)); };
+    // this lane's first token and its index, and from one step to the next
+    const int at0 = warp * (32 * kPer) + (kVec ? lane * kPer : lane), first = (rank << kLogStep) + at0, stride = C << kLogStep;
+    auto row_at = [&](int t) { return static_cast<const T *>(p.logits) + b * p.seq_stride + t * p.row_stride; };
+    // A position's logits on their way to shared memory (where nobody reads the last one's any more).
+    auto bring = [&](int t) {
+        const T *const row = row_at(t);
+        if (kVec) {
+            if (tid == 0) {
+                const uint32_t bar = smem_u32(&s.full);
+                uint32_t bytes = 0;
+                for (int i = 0; i < mine; ++i) bytes += static_cast<uint32_t>(min(kStep, vocab - token_of(i * kStep)) * sizeof(T));
+                mbar_arrive_expect_tx(bar, bytes);
+                for (int i = 0; i < mine; ++i) {
+                    const int v = token_of(i * kStep);
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                     smem_u32(logits + i * kStep)),
+                                 "l"(row + v), "r"(static_cast<uint32_t>(min(kStep, vocab - v) * sizeof(T))), "r"(bar)
+                                 : "memory");
                 }
             }
-        }
-        if (draft && tid < t0) {
-            for (int i = tid; i < t0; i += kThreads) {
-                const int at = place(draft[i]);
-                if (at >= 0) atomicAdd(counts + at, 1u);
+        } else {  // rows that do not start on 16 bytes
+            for (int i = 0; i < mine; ++i) {
+                const int v = token_of(i * kStep) + tid;
+                T x[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (v + j * kThreads < vocab) x[j] = row[v + j * kThreads];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (v + j * kThreads < vocab) logits[i * kStep + tid + j * kThreads] = x[j];
             }
         }
-    }
-    if (p.biased) {
-        const int32_t *const ids = p.r.bias_ids + b * p.r.bias_stride;
-        sl.bias_values = p.r.bias_values + b * p.r.bias_stride;
-        for (int i = tid; i < p.r.bias_count; i += kThreads) {
-            const int at = place(ids[i]);
-            if (at >= 0) atomicMax(bias + at, static_cast<uint32_t>(i) + 1u);  // the last one counts
+    };
+    // Its mask, without what lies behind the vocabulary.
+    auto bring_mask = [&](int t) {
+        const int32_t *const from = p.mask ? p.mask + b * p.mask_seq_stride + t * p.mask_row_stride : nullptr;
+        for (int w = tid; w < mine * (kStep / 32); w += kThreads) {
+            const int v = token_of(w * 32);
+            uint32_t m = v < vocab ? (from ? static_cast<uint32_t>(from[v >> 5]) : 0xFFFFFFFFu) : 0u;
+            if (v < vocab && vocab - v < 32) m &= (1u << (vocab - v)) - 1u;
+            mask[w] = m;
         }
-    }
+    };
     __syncthreads();
+    // (waited for before the first exchange: every CTA's shared memory exists before another writes to it)
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    pdl_trigger();
+    pdl_wait();
+    bring(t0);
+    bring_mask(t0);
+
+    const int32_t *const draft = p.draft && p.counted ? p.draft + b * p.draft_stride : nullptr;
+    const float rho = p.r.repetition ? p.r.repetition[b] : 1.f, alpha = p.r.presence ? p.r.presence[b] : 0.f,
+                beta = p.r.frequency ? p.r.frequency[b] : 0.f, tau = p.r.temperature ? p.r.temperature[b] : 1.f;
+    const float *const bias_values = p.biased ? p.r.bias_values + b * p.r.bias_stride : nullptr;
+    auto place = [&](int32_t token) {  // a token's index in its CTA's own
+        return ((token >> (kLogStep + p.log_c)) << kLogStep) + (token & (kStep - 1));
+    };
+    auto owner = [&](int32_t token) { return token >> kLogStep & (C - 1); };
+    auto known = [&](int32_t token) { return token >= 0 && token < vocab; };
+    if (tables) {
+        if (p.counted) {
+            const int32_t *const tokens = p.r.tokens ? p.r.tokens + b * p.r.token_stride : nullptr;
+            const int len = tokens ? min(max(p.r.lens[b], 0), p.r.token_cols) : 0;
+            const int prompt = p.r.prompt_lens ? p.r.prompt_lens[b] : 0;
+            constexpr int kAtOnce = 16;
+            for (int i0 = tid; i0 < len; i0 += kAtOnce * kThreads) {
+                int32_t w[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) w[u] = i0 + u * kThreads < len ? tokens[i0 + u * kThreads] : -1;
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    if (known(w[u]) && owner(w[u]) == rank) mk.occurred(place(w[u]), i0 + u * kThreads < prompt);
+            }
+            if (draft)
+                for (int i = tid; i < t0; i += kThreads)
+                    if (known(draft[i]) && owner(draft[i]) == rank) mk.occurred(place(draft[i]), false);
+        }
+        if (p.biased) {
+            const int32_t *const ids = p.r.bias_ids + b * p.r.bias_stride;
+            for (int i = tid; i < p.r.bias_count; i += kThreads)
+                if (known(ids[i]) && owner(ids[i]) == rank) mk.has_bias(place(ids[i]), static_cast<uint32_t>(i) + 1u);
+        }
+        __syncthreads();
+        // the list: a thread has every 256th eight tokens, and its entries follow one another (an order that does not depend
+        // on timing, as sums over the list then do not either)
+        auto todo = [&](int w) {
+            return (p.counted ? mk.occurrences(w * 8) : 0u) | (p.biased ? reinterpret_cast<const uint8_t *>(mk.listed)[w] : 0u);
+        };
+        int n = 0;
+        for (int w = tid; w < mine * (kStep / 8); w += kThreads) {
+            const uint32_t m = todo(w);
+            reinterpret_cast<uint8_t *>(mk.marks)[w] = static_cast<uint8_t>(m);
+            n += __popc(m);
+        }
+        int up = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, up, o);
+            if (lane >= o) up += y;
+        }
+        if (lane == 31) s.warp_n[warp] = up;
+        __syncthreads();
+        int e = up - n;
+        for (int w = 0; w < warp; ++w) e += s.warp_n[w];
+        if (tid == kThreads - 1) s.n = e + n;
+        for (int w = tid; n > 0; w += kThreads)
+            for (uint32_t m = reinterpret_cast<const uint8_t *>(mk.marks)[w]; m; m &= m - 1, ++e, --n) {
+                const int at = w * 8 + __ffs(m) - 1;
+                if (e < kMaxList) mk.put(e, at, p.counted ? mk.get(mk.counts, at) : 0u);
+            }
+    }
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
     const bool greedy = tau == 0.f;
     float scale = greedy ? 1.f : 1.4426950408889634f / tau;
     if (scale == INFINITY) scale = 3.4028235e38f;  // (so that the best token's 0 * scale stays 0,
     if (scale == 0.f) scale = 1.1754944e-38f;      // and a masked token's -inf * scale -inf)
+    const float2 scale2 = make_float2(scale, scale);
     const bool want_sum = p.probs && !greedy, want_best = p.argmax || (p.probs && greedy);
+    bool arrived = true;  // (a copy that does not arrive in a second: NaN and -1)
     for (int t = t0; t < t1; ++t) {
         const int64_t at_row = static_cast<int64_t>(b) * p.rows + t;
-        const T *const row = static_cast<const T *>(p.logits) + b * p.seq_stride + t * p.row_stride;
-        const int32_t *const mask = p.mask ? p.mask + b * p.mask_seq_stride + t * p.mask_row_stride : nullptr;
         T *const out = p.out ? static_cast<T *>(p.out) + b * p.out_seq_stride + t * p.out_row_stride : nullptr;
-        // (a row that is written in place is written by the pass that reads it last)
-        const bool out_now = out && !p.probs;
-
-        float m = -INFINITY, sum = 0.f, best = -INFINITY;
-        int best_id = 0x7FFFFFFF;
-        for (int64_t at = sl.v0 + warp * (32 * kPer); at < sl.v1; at += kStep) {
-            float x[kPer];
-            sl.load(row, at, lane, x);
-            sl.adjust(mask, at, lane, x);
-            if (want_sum || want_best) {
-                float top = x[0];
-#pragma unroll
-                for (int j = 1; j < kPer; ++j) top = fmaxf(top, x[j]);
-                if (want_best && top > best) {
-                    best = top;
+        if (kVec) {
+            arrived = mbar_wait(smem_u32(&s.full), static_cast<uint32_t>(t - t0) & 1u, &s.abort_flag) && arrived;
+            if (t + 1 < t1 && tid < mine) {  // the next position's logits come to L2 beside this one's passes
+                const int v = token_of(tid * kStep);
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row_at(t + 1) + v),
+                             "r"(static_cast<uint32_t>(min(kStep, vocab - v) * sizeof(T)))
+                             : "memory");
+            }
+        }
+        __syncthreads();  // the list, the mask (and logits that threads have brought) are complete
+        Best q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
+        const int marked = tables ? s.n : 0;
+        // all tokens but those on the list
+        auto walk = [&](auto body) {
+            for (int v = first, at = at0; v < vocab; v += stride, at += kStep) {
+                Raw<T, kVec> r;
+                r.load(logits, at);
+                float2 x[kPer / 2];
+                r.values(r.bits(mask, at) & ~(tables ? r.bits(mk.marks, at) : 0u), x);
+                body(x, v);
+            }
+        };
+        float2 less = make_float2(0.f, 0.f);  // what exponentials are relative to
+        auto pass = [&](auto sum, auto best, auto any) {
+            const bool writes = decltype(any)::value && out && !p.probs;
+            walk([&](float2 (&x)[kPer / 2], int v) {
+                const float top = max3(max3(max3(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), max3(x[2].y, x[3].x, x[3].y), -INFINITY);
+                if (decltype(best)::value && (!decltype(any)::value || want_best) && top > q.v) {
+                    q.v = top;
 #pragma unroll
                     for (int j = kPer - 1; j >= 0; --j)
-                        if (x[j] == top) best_id = static_cast<int>(sl.token(at, lane, j));
+                        if ((j & 1 ? x[j >> 1].y : x[j >> 1].x) == top) q.id = v + (kVec ? j : j * 32);
                 }
-                if (want_sum) {
-                    if (top > m) {
-                        if (m > -INFINITY) sum *= exp2_fast((m - top) * scale);
-                        m = top;
+                if (decltype(sum)::value && (!decltype(any)::value || want_sum)) {
+                    if (top > q.m) {
+                        if (q.m > -INFINITY) q.s *= exp2_fast((q.m - top) * scale);
+                        q.m = top;
+                        less = make_float2(-top, -top);  // (before: nothing yet, exp of -inf or NaN)
                     }
-                    const float base = m == -INFINITY ? 0.f : m;  // (nothing yet: exp of -inf, or NaN)
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) sum += exp2_fast((x[j] - base) * scale);
+                    exponentials(x, less, scale2);
+                    const float2 e = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+                    q.s += e.x + e.y;
+                } else if (writes) {
+                    store8<kVec>(out, v, vocab, x);
                 }
+            });
+        };
+        constexpr std::true_type yes;
+        constexpr std::false_type no;
+        if (want_sum && !want_best)
+            pass(yes, no, no);
+        else if (want_best && !want_sum && !out)
+            pass(no, yes, no);
+        else if (want_sum || want_best || !p.probs)
+            pass(yes, yes, yes);
+        // the tokens on the list under the rules, each by one thread
+        auto marked_tokens = [&](auto body) {
+            auto one = [&](int at, uint32_t entry) {
+                const int v = token_of(at);
+                float x;
+                if constexpr (sizeof(T) == 4) x = logits[at];
+                else x = half_of<T>(reinterpret_cast<const uint16_t *>(logits)[at], 0);
+                if (entry) {
+                    x = x > 0.f ? __fdiv_rn(x, rho) : __fmul_rn(x, rho);
+                    const float c = mk.times(entry);
+                    if (c > 0.f) x = __fsub_rn(__fsub_rn(x, __fmul_rn(beta, c)), alpha);
+                }
+                if (p.biased && mk.bit(mk.listed, at)) x = __fadd_rn(x, bias_values[mk.get(mk.bias, at) - 1]);
+                body(mk.bit(mask, at) ? x : -INFINITY, v);
+            };
+            // (by the bits if the list is too short: one loop for both, a step of which finds the next token)
+            const bool listed = marked <= kMaxList;
+            uint32_t m = 0;
+            int w = tid - kThreads, e = tid;
+            while (true) {
+                int at;
+                if (listed) {
+                    if (e >= marked) break;
+                    at = mk.token(e);
+                } else {
+                    while (m == 0 && (w += kThreads) < mine * (kStep / 8)) m = reinterpret_cast<const uint8_t *>(mk.marks)[w];
+                    if (m == 0) break;
+                    at = w * 8 + __ffs(m) - 1;
+                    m &= m - 1;
+                }
+                one(at, listed ? mk.count(e) : p.counted ? mk.get(mk.counts, at) : 0u);
+                e += kThreads;
             }
-            if (out_now) {
-                if constexpr (kVec) {
-                    const int64_t v = at + lane * kPer;
-                    constexpr int N = 16 / sizeof(T);
-                    if (v < sl.v1) {
-#pragma unroll
-                        for (int i = 0; i < kPer / N; ++i) {
-                            Vec<T> q;
-#pragma unroll
-                            for (int j = 0; j < N; ++j) q.v[j] = from_f<T>(x[i * N + j]);
-                            *reinterpret_cast<Vec<T> *>(out + v + i * N) = q;
+        };
+        if (want_sum || want_best) {
+            if (marked > 0)
+                marked_tokens([&](float x, int v) {
+                    join_best(q.v, q.id, x, x > -INFINITY ? v : 0x7FFFFFFF);
+                    if (want_sum) {
+                        if (x > q.m) {
+                            if (q.m > -INFINITY) q.s *= exp2_fast((q.m - x) * scale);
+                            q.m = x;
                         }
+                        q.s += exp2_fast((x - (q.m == -INFINITY ? 0.f : q.m)) * scale);
+                    }
+                });
+            reduce(q, scale, want_sum, want_best);
+            Best *const here = &s.peer[t & 1][rank * kWarps + warp];
+            if (C > 1) {
+                if (lane < C)
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     mapa_shared(smem_u32(here), static_cast<uint32_t>(lane))),
+                                 "r"(__float_as_uint(q.m)), "r"(__float_as_uint(q.s)), "r"(__float_as_uint(q.v)), "r"(q.id)
+                                 : "memory");
+                __syncwarp();
+                // (the next position writes the other half: who reads this one has not passed that exchange)
+                cluster_sync_all();
+            } else {
+                if (lane == 0) *here = q;
+                __syncthreads();
+            }
+            if (p.probs || (rank == 0 && warp == 0)) {
+                q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
+                for (int u = lane; u < C * kWarps; u += 32) {
+                    const Best a = s.peer[t & 1][u];
+                    if (a.m > q.m) {
+                        q.s *= exp2_fast((q.m - a.m) * scale);
+                        q.m = a.m;
+                    }
+                    q.s += a.m == q.m ? a.s : a.s * exp2_fast((a.m - q.m) * scale);
+                    join_best(q.v, q.id, a.v, a.id);
+                }
+                reduce(q, scale, want_sum, want_best);
+            }
+        }
+        const int id = q.id == 0x7FFFFFFF || !arrived ? -1 : q.id;
+        if (p.argmax && rank == 0 && tid == 0) p.argmax[at_row] = id;
+        float *const probs = p.probs ? p.probs + at_row * p.vocab : nullptr;
+        const float base = q.m == -INFINITY ? 0.f : q.m;
+        // (nothing above -inf: zeros. A sum that is no number makes all of them such.)
+        const float inv = !arrived ? __int_as_float(0x7FFFFFFF) : q.m == -INFINITY && q.s == 0.f ? 0.f : 1.f / q.s;
+        if (probs) {
+            less = make_float2(-base, -base);
+            const float2 inv2 = make_float2(inv, inv);
+            walk([&](float2 (&x)[kPer / 2], int v) {
+                if (out) store8<kVec>(out, v, vocab, x);
+                if (greedy) {
+#pragma unroll
+                    for (int j = 0; j < kPer / 2; ++j) {
+                        x[j].x = v + (kVec ? 2 * j : 64 * j) == id ? 1.f : 0.f;
+                        x[j].y = v + (kVec ? 2 * j + 1 : 64 * j + 32) == id ? 1.f : 0.f;
                     }
                 } else {
+                    exponentials(x, less, scale2);
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const int64_t v = sl.token(at, lane, j);
-                        if (v < sl.v1) out[v] = from_f<T>(x[j]);
-                    }
+                    for (int j = 0; j < kPer / 2; ++j) x[j] = mul2(x[j], inv2);
                 }
-            }
+                store8<kVec>(probs, v, vocab, x);
+            });
         }
-        if (want_sum || want_best) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                join(m, sum, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, sum, o), scale);
-                join_best(best, best_id, __shfl_xor_sync(0xFFFFFFFFu, best, o), __shfl_xor_sync(0xFFFFFFFFu, best_id, o));
-            }
-            if (lane == 0) s.warp[warp] = {m, sum, best, best_id};
+        const bool more = t + 1 < t1;
+        if (marked > 0 && (probs || out)) {  // over what the passes wrote there
             __syncthreads();
-            if (warp == 0) {
-                Best q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
-                if (lane < kWarps) q = s.warp[lane];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    join(q.m, q.s, __shfl_xor_sync(0xFFFFFFFFu, q.m, o), __shfl_xor_sync(0xFFFFFFFFu, q.s, o), scale);
-                    join_best(q.v, q.id, __shfl_xor_sync(0xFFFFFFFFu, q.v, o), __shfl_xor_sync(0xFFFFFFFFu, q.id, o));
-                }
-                if (C > 1) {
-                    if (lane < C) {
-                        const uint32_t to = mapa_shared(smem_u32(&s.peer[t & 1][rank]), static_cast<uint32_t>(lane));
-                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(q.m)),
-                                     "r"(__float_as_uint(q.s)), "r"(__float_as_uint(q.v)), "r"(q.id)
-                                     : "memory");
-                    }
-                } else if (lane == 0) {
-                    s.all = q;
-                }
-                __syncwarp();
-            }
-            Best q;
-            if (C > 1) {
-                // (the next position writes the other half: a CTA that reads this one has not passed that exchange)
-                cluster_sync_all();
-                q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
-                if (lane < C) q = s.peer[t & 1][lane];
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    join(q.m, q.s, __shfl_xor_sync(0xFFFFFFFFu, q.m, o), __shfl_xor_sync(0xFFFFFFFFu, q.s, o), scale);
-                    join_best(q.v, q.id, __shfl_xor_sync(0xFFFFFFFFu, q.v, o), __shfl_xor_sync(0xFFFFFFFFu, q.id, o));
-                }
-                q.m = __shfl_sync(0xFFFFFFFFu, q.m, 0);
-                q.s = __shfl_sync(0xFFFFFFFFu, q.s, 0);
-                q.id = __shfl_sync(0xFFFFFFFFu, q.id, 0);
-            } else {
+            marked_tokens([&](float x, int v) {
+                if (out) out[v] = from_f<T>(x);
+                if (probs) probs[v] = greedy ? (v == id ? 1.f : 0.f) : exp2_fast((x - base) * scale) * inv;
+            });
+        }
+        if (more) {
+            __syncthreads();  // this position's logits and mask have been read
+            bring(t + 1);
+            bring_mask(t + 1);
+            if (draft) {  // the next position follows one more draft
+                const int32_t token = draft[t];
+                const bool here = known(token) && owner(token) == rank;
+                const int at = here ? place(token) : 0;
+                const bool old = here && mk.bit(mk.marks, at);
+                if (old && marked <= kMaxList)
+                    for (int e = tid; e < marked; e += kThreads)
+                        if (mk.token(e) == at) mk.put(e, at, mk.count(e) + 1u);
                 __syncthreads();
-                q = s.all;
-            }
-            const int id = q.id == 0x7FFFFFFF ? -1 : q.id;
-            if (p.argmax && rank == 0 && tid == 0) p.argmax[at_row] = id;
-            if (p.probs) {
-                float *const probs = p.probs + at_row * p.vocab;
-                const float base = q.m == -INFINITY ? 0.f : q.m;
-                const float inv = q.m == -INFINITY && q.s == 0.f ? 0.f : 1.f / q.s;
-                for (int64_t at = sl.v0 + warp * (32 * kPer); at < sl.v1; at += kStep) {
-                    float x[kPer], y[kPer];
-                    sl.load(row, at, lane, x);
-                    sl.adjust(mask, at, lane, x);
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        y[j] = greedy ? (static_cast<int>(sl.token(at, lane, j)) == id ? 1.f : 0.f)
-                                      : exp2_fast((x[j] - base) * scale) * inv;
-                    if constexpr (kVec) {
-                        const int64_t v = at + lane * kPer;
-                        if (v < sl.v1) {
-                            *reinterpret_cast<float4 *>(probs + v) = make_float4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<float4 *>(probs + v + 4) = make_float4(y[4], y[5], y[6], y[7]);
-                            if (out) {
-                                constexpr int N = 16 / sizeof(T);
-#pragma unroll
-                                for (int i = 0; i < kPer / N; ++i) {
-                                    Vec<T> o;
-#pragma unroll
-                                    for (int j = 0; j < N; ++j) o.v[j] = from_f<T>(x[i * N + j]);
-                                    *reinterpret_cast<Vec<T> *>(out + v + i * N) = o;
-                                }
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kPer; ++j) {
-                            const int64_t v = sl.token(at, lane, j);
-                            if (v < sl.v1) {
-                                probs[v] = y[j];
-                                if (out) out[v] = from_f<T>(x[j]);
-                            }
-                        }
-                    }
+                if (here && tid == 0) {
+                    mk.occurred(at, false);  // (for a list that is or gets too short)
+                    if (!old && marked < kMaxList) mk.put(marked, at, 1u);
+                    if (!old) s.n = marked + 1;
+                    mk.marks[at >> 5] |= 1u << (at & 31);
                 }
             }
-        }
-        if (p.counted && draft && t + 1 < t1) {  // the next position follows one more draft
-            __syncthreads();
-            if (tid == 0) {
-                const int at = place(draft[t]);
-                if (at >= 0) ++counts[at];
-            }
-            __syncthreads();
         }
     }
-    if (C > 1) cluster_sync_all();  // no CTA ends while another still writes to it
+    // (after the last exchange nobody writes to another CTA)
 }
 
 dflash_status logits_fail(dflash_status st, const char *fmt, long long a = 0, long long b = 0)
@@ -481,7 +718,7 @@ cudaError_t machine(int *sms, int *smem)
     int optin = 0;
     e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    *smem = optin - static_cast<int>(sizeof(Shared)) - 1024;
+    *smem = optin - static_cast<int>(sizeof(Shared));
     for (int dtype : {static_cast<int>(DFLASH_BF16), static_cast<int>(DFLASH_FP16), static_cast<int>(DFLASH_FP32)})
         for (int vec = 0; vec < 2 && e == cudaSuccess; ++vec) {
             e = cudaFuncSetAttribute(kernel_of(dtype, vec != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, *smem);
@@ -512,7 +749,8 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
         return logits_fail(DFLASH_ERR_UNSUPPORTED, "dtype must be BF16, FP16 or FP32 (got %lld)", dtype);
     if (batch < 0 || rows < 0 || static_cast<int64_t>(batch) * rows >= (int64_t(1) << 31))
         return logits_fail(DFLASH_ERR_INVALID_ARG, "batch and rows must be >= 0, their product below 2^31 (got %lld, %lld)", batch, rows);
-    if (vocab < 1 || vocab >= (int64_t(1) << 31)) return logits_fail(DFLASH_ERR_INVALID_ARG, "vocab must be in [1, 2^31) (got %lld)", vocab);
+    if (vocab < 1) return logits_fail(DFLASH_ERR_INVALID_ARG, "vocab must be at least 1 (got %lld)", vocab);
+    if (vocab > int64_t(1) << 30) return logits_fail(DFLASH_ERR_UNSUPPORTED, "a vocabulary must be at most 2^30 (got %lld)", vocab);
     if (batch == 0 || rows == 0) return DFLASH_OK;
     if (!out && !probs && !argmax) return logits_fail(DFLASH_ERR_INVALID_ARG, "one of out, probs and argmax must be given");
     const int size = dtype == DFLASH_FP32 ? 4 : 2;
@@ -567,25 +805,32 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     p.mask_row_stride = mask_row_stride;
     p.counted = (p.r.repetition || p.r.presence || p.r.frequency) && (p.r.tokens || p.draft);
     p.biased = p.r.bias_count > 0;
-    const int word = 4 * (p.counted + p.biased);
-    // CTAs per cluster: enough that the tables leave room for two CTAs an SM and, with few positions, that all SMs
-    // have work of at least a step
+    // CTAs per cluster: enough that the tables leave room for some CTAs an SM and, with few positions, that all SMs have
+    // work of at least a piece
     const int64_t positions = static_cast<int64_t>(batch) * rows;
-    auto slice_of = [&](int C) { return ((vocab + C - 1) / C + 255) / 256 * 256; };
+    const int64_t entries = (p.counted ? (p.r.tokens ? p.r.token_cols : 0) + static_cast<int64_t>(p.draft ? rows - 1 : 0) : 0) + p.r.bias_count;
+    auto slice_of = [&](int C) { return ((vocab + dfl::kStep - 1) / dfl::kStep + C - 1) / C * dfl::kStep; };
+    auto bytes_of = [&](int64_t slice) {
+        p.wide = entries > 32767 || slice > 65536;
+        p.most = static_cast<int>(entries < slice ? entries : slice);
+        return static_cast<int64_t>(dfl::room_of(static_cast<int>(slice), size, p.most, p.counted, p.biased, p.wide).total) * 4;
+    };
     int C = 1;
-    while (C < dfl::kMaxCluster && (slice_of(C) * word > 100 * 1024 || (positions * C < 2 * sms && slice_of(C) > dfl::kStep))) C *= 2;
+    while (C < dfl::kMaxCluster && (slice_of(C) > int64_t(1) << 24 || bytes_of(slice_of(C)) > 50 * 1024 ||
+                                    (positions * C < 10 * sms && slice_of(C) > (positions * C < 2 * sms ? 1 : 4) * dfl::kStep)))
+        C *= 2;
     const int64_t slice = slice_of(C);
-    if (slice * word > smem_most)
-        return logits_fail(DFLASH_ERR_UNSUPPORTED, "a vocabulary of %lld with tokens or biases needs more shared memory than there is (%lld bytes a CTA)",
-                           vocab, smem_most);
-    // positions per cluster: as many as leave a few waves, since a sequence's tokens are laid out once for them
+    if (slice > int64_t(1) << 24 || bytes_of(slice) > smem_most)
+        return logits_fail(DFLASH_ERR_UNSUPPORTED, "a vocabulary of %lld needs more shared memory than there is (%lld bytes a CTA)", vocab, smem_most);
+    // positions per cluster: a sequence's list is laid out once for them, but two CTAs an SM have work
     int group = 1;
-    if (p.counted || p.biased)
-        while (group < rows && (positions / (2 * group)) * C >= 8 * sms) group *= 2;
+    while ((p.counted || p.biased) && group < rows && static_cast<int64_t>(batch) * ((rows + 2 * group - 1) / (2 * group)) * C >= 2 * sms) group *= 2;
     p.group = group < rows ? group : rows;
     p.groups = (rows + p.group - 1) / p.group;
     p.slice = static_cast<int>(slice);
     p.C = C;
+    while ((1 << p.log_c) < C) ++p.log_c;
+    const size_t smem = static_cast<size_t>(bytes_of(slice));
     const int per = 16 / size;
     const bool vec = !dfl::misaligned(logits, 16) && seq_stride % per == 0 && row_stride % per == 0 && vocab % 8 == 0 &&
                      (!out || (!dfl::misaligned(out, 16) && out_seq_stride % per == 0 && out_row_stride % per == 0)) &&
@@ -593,7 +838,7 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     const int64_t clusters = static_cast<int64_t>(batch) * p.groups;
     if (clusters >= (int64_t(1) << 31)) return logits_fail(DFLASH_ERR_INVALID_ARG, "too many positions");
     e = dfl::launch_ex(dfl::kernel_of(dtype, vec), dim3(static_cast<unsigned>(clusters), 1, C), dim3(dfl::kThreads),
-                       static_cast<size_t>(slice) * word, static_cast<cudaStream_t>(stream), C, p);
+                       smem, static_cast<cudaStream_t>(stream), C, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return logits_fail(DFLASH_ERR_CUDA, "the launch failed (error %lld)", e);
