@@ -2,14 +2,14 @@
 // and the pages of dropped tokens given back.
 //
 // A page's or token's place in the batch follows from running sums over the
-// entries before it. Entries are cut into ranges of 1024; the grid is ranges x
-// parts. Every block sums the entries before its range and scans its own (a few
+// entries before it. Entries are cut into ranges of 32, 256 or 1024 (a block's
+// threads); the grid is ranges x parts. Every block sums the entries before its range and scans its own (a few
 // hundred bytes per hundred entries, from L2), so no block waits for another,
 // and the blocks of a range share its pages, table entries and tokens, found by
 // binary search in the scan. Requests' lengths and the number of free pages
 // change only when every block has read them: the block that finishes last (a
 // counter) writes them. A call is bound by the latency of its dependent reads
-// (row, length, page id).
+// (row, length, page id), so a small batch is one warp's, without barriers.
 #include <stdio.h>
 
 #include "common.cuh"
@@ -22,8 +22,6 @@ dflash_status host_fail(dflash_status st, const char *msg);
 
 namespace {
 
-constexpr int kRange = 1024;  // entries of a range, threads of a block
-constexpr int kWarps = kRange / 32;
 
 struct PagesParams {
     dflash_page_pool pool;
@@ -98,33 +96,51 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane)
     return v;
 }
 
+template <int R>
 struct Shared {
-    long long warp_a[kWarps], warp_b[kWarps];
+    long long warp_a[R / 32], warp_b[R / 32];
     long long before_a, before_b;
-    int first[3][kRange + 1];  // running sums of the range: pages, tokens, table entries
-    int row[kRange], len[kRange], held[kRange];
+    int first[3][R + 1];  // running sums of the range: pages, tokens, table entries
+    int row[R], len[R], held[R];
     unsigned last;
-    int cut;
 };
 
-// Inclusive scans of a and b over the block; s.warp_* hold the warps' sums after it.
-__device__ __forceinline__ void block_scan(Shared &s, long long &a, long long &b)
+template <int R>
+__device__ __forceinline__ void block_sync()
+{
+    if constexpr (R > 32) __syncthreads();
+    else __syncwarp();
+}
+
+template <int R>
+__device__ __forceinline__ int block_count(bool pred)
+{
+    if constexpr (R > 32) return __syncthreads_count(pred);
+    else return __popc(__ballot_sync(0xFFFFFFFFu, pred));
+}
+
+// Inclusive scans of a and b over the block.
+template <int R>
+__device__ __forceinline__ void block_scan(Shared<R> &s, long long &a, long long &b)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     a = warp_scan(a, lane);
     b = warp_scan(b, lane);
-    __syncthreads();  // (the last scan's sums have been read)
-    if (lane == 31) {
-        s.warp_a[warp] = a;
-        s.warp_b[warp] = b;
-    }
-    __syncthreads();
-    const long long wa = warp_scan(s.warp_a[lane], lane), wb = warp_scan(s.warp_b[lane], lane);
-    const long long ea = __shfl_sync(0xFFFFFFFFu, wa, warp > 0 ? warp - 1 : 0);
-    const long long eb = __shfl_sync(0xFFFFFFFFu, wb, warp > 0 ? warp - 1 : 0);
-    if (warp > 0) {
-        a += ea;
-        b += eb;
+    if constexpr (R > 32) {
+        __syncthreads();  // (the last scan's sums have been read)
+        if (lane == 31) {
+            s.warp_a[warp] = a;
+            s.warp_b[warp] = b;
+        }
+        __syncthreads();
+        const bool in = lane < R / 32;
+        const long long wa = warp_scan(in ? s.warp_a[lane] : 0, lane), wb = warp_scan(in ? s.warp_b[lane] : 0, lane);
+        const long long ea = __shfl_sync(0xFFFFFFFFu, wa, warp > 0 ? warp - 1 : 0);
+        const long long eb = __shfl_sync(0xFFFFFFFFu, wb, warp > 0 ? warp - 1 : 0);
+        if (warp > 0) {
+            a += ea;
+            b += eb;
+        }
     }
 }
 
@@ -143,48 +159,50 @@ __device__ __forceinline__ int find(const int *first, int n, int x)
 }
 
 // Pages and tokens of the granted entries before `range`.
-__device__ void sums_before(Shared &s, const PagesParams &p, int range, int free, long long &pages, long long &tokens)
+template <int R>
+__device__ void sums_before(Shared<R> &s, const PagesParams &p, int range, int free, long long &pages, long long &tokens)
 {
     pages = tokens = 0;
     if (range == 0) return;
     long long a = 0, b = 0;
-    for (int i = threadIdx.x; i < range * kRange; i += kRange) {
+    for (int i = threadIdx.x; i < range * R; i += R) {
         const Entry e = entry_of<false>(p, i);
         if (e.valid) a += e.pages, b += e.tokens;
     }
     block_scan(s, a, b);
-    if (threadIdx.x == kRange - 1) s.before_a = a, s.before_b = b;
-    __syncthreads();
+    if (threadIdx.x == R - 1) s.before_a = a, s.before_b = b;
+    block_sync<R>();
     pages = s.before_a;
     tokens = s.before_b;
     if (pages <= free && tokens <= p.tokens) return;
     // the cut lies before this range: the sums up to it
     pages = tokens = 0;
     for (int r = 0; r < range; ++r) {
-        const Entry e = entry_of<false>(p, r * kRange + static_cast<int>(threadIdx.x));
+        const Entry e = entry_of<false>(p, r * R + static_cast<int>(threadIdx.x));
         long long c = e.valid ? e.pages : 0, d = e.valid ? e.tokens : 0;
         block_scan(s, c, d);
         c += pages;
         d += tokens;
         const bool fits = c <= free && d <= p.tokens;
-        const int n = __syncthreads_count(fits);  // (sums never fall: those that fit come first)
+        const int n = block_count<R>(fits);  // (sums never fall: those that fit come first)
         if (static_cast<int>(threadIdx.x) == n - 1) s.before_a = c, s.before_b = d;
-        __syncthreads();
+        block_sync<R>();
         if (n > 0) pages = s.before_a, tokens = s.before_b;
-        __syncthreads();
-        if (n < kRange) break;
+        block_sync<R>();
+        if (n < R) break;
     }
     // what follows the cut is refused: sums that nothing can be added to
     pages |= 1ll << 62;
 }
 
-__global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_constant__ PagesParams p)
+template <int R>
+__global__ void __launch_bounds__(R) pages_extend_kernel(const __grid_constant__ PagesParams p)
 {
-    __shared__ Shared s;
+    __shared__ Shared<R> s;
     pdl_trigger();
     pdl_wait();
     const int t = threadIdx.x, range = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
-    const int b = range * kRange + t, page = p.pool.page_size;
+    const int b = range * R + t, page = p.pool.page_size;
     const int free = min(max(p.pool.counters[0], 0), p.pool.num_pages);
     const Entry e = entry_of<false>(p, b);
     long long pages0, tokens0;
@@ -196,16 +214,16 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
     const bool fits = !cut_before && pages0 + a <= free && tokens0 + c <= p.tokens;
     const bool given = fits && e.valid;
     // the granted entries' sums: those of the last one that fits
-    const int n_fit = __syncthreads_count(fits);
+    const int n_fit = block_count<R>(fits);
     if (t == n_fit - 1) s.before_a = a, s.before_b = c;
     if (t == 0 && n_fit == 0) s.before_a = s.before_b = 0;
-    __syncthreads();
+    block_sync<R>();
     const int my_pages = static_cast<int>(fits ? a : s.before_a), my_tokens = static_cast<int>(fits ? c : s.before_b);
     const int len = e.len + (given ? e.tokens : 0);
     int entries = 0;
     if (p.table && e.row >= 0) entries = min(pages_of(len, page), p.table_cols);
     long long f = entries, none = 0;
-    block_scan(s, f, none);
+    if (p.table) block_scan(s, f, none);
     s.first[0][t + 1] = my_pages;
     s.first[1][t + 1] = my_tokens;
     s.first[2][t + 1] = static_cast<int>(f);
@@ -213,7 +231,10 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
     s.row[t] = e.row;
     s.len[t] = e.len;
     s.held[t] = e.held;
-    __syncthreads();
+    block_sync<R>();
+    // (this block has read the requests' lengths and the free pages: nobody's reads come after the last block's ticket, and
+    // what blocks write is not read by others)
+    if (gridDim.x > 1 && t == 0) s.last = atomicAdd(reinterpret_cast<unsigned *>(p.pool.counters + 1), 1u) == gridDim.x - 1;
     const int64_t base_page = free - 1 - pages0;  // the stack's entry of the range's first page
     const int base_token = static_cast<int>(tokens0);
     if (part == 0 && b < p.batch) {
@@ -226,24 +247,24 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
     }
     if (p.cu && p.batch == 0 && t == 0 && blockIdx.x == 0) p.cu[0] = 0;
 
-    const int stride = p.parts * kRange, at0 = part * kRange + t;
+    const int stride = p.parts * R, at0 = part * R + t;
     auto page_at = [&](int i, int col) -> int {  // page `col` of the range's entry i, new or old
         if (col >= s.held[i]) return p.pool.free_pages[base_page - (s.first[0][i] + col - s.held[i])];
         return p.pool.page_table[s.row[i] * p.pool.table_stride + col];
     };
-    for (int x = at0; x < s.first[0][kRange]; x += stride) {
-        const int i = find(s.first[0], kRange, x);
+    for (int x = at0; x < s.first[0][R]; x += stride) {
+        const int i = find(s.first[0], R, x);
         const int col = s.held[i] + x - s.first[0][i];
         p.pool.page_table[s.row[i] * p.pool.table_stride + col] = p.pool.free_pages[base_page - x];
     }
-    for (int x = at0; x < s.first[2][kRange]; x += stride) {
-        const int i = find(s.first[2], kRange, x);
+    for (int x = at0; x < s.first[2][R]; x += stride) {
+        const int i = find(s.first[2], R, x);
         const int col = x - s.first[2][i];
-        p.table[(range * kRange + i) * p.table_stride + col] = page_at(i, col);
+        p.table[(range * R + i) * p.table_stride + col] = page_at(i, col);
     }
     if (p.positions || p.slots) {
-        for (int x = at0; x < s.first[1][kRange]; x += stride) {
-            const int i = find(s.first[1], kRange, x);
+        for (int x = at0; x < s.first[1][R]; x += stride) {
+            const int i = find(s.first[1], R, x);
             const int at = s.len[i] + x - s.first[1][i];
             if (p.positions) p.positions[base_token + x] = at;
             if (p.slots) p.slots[base_token + x] = static_cast<int64_t>(page_at(i, at / page)) * page + at % page;
@@ -251,19 +272,11 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
     }
 
     // the pool's lengths and free pages, when every block has read them
-    if (gridDim.x > 1) {
-        __threadfence();
-        __syncthreads();
-        if (t == 0) s.last = atomicAdd(reinterpret_cast<unsigned *>(p.pool.counters + 1), 1u) == gridDim.x - 1;
-        __syncthreads();
-        if (!s.last) return;
-        __threadfence();
-    } else {
-        __syncthreads();
-    }
+    block_sync<R>();
+    if (gridDim.x > 1 && !s.last) return;
     long long total = 0, done = 0;
     for (int r = 0; r < p.ranges; ++r) {
-        const Entry q = r == range ? e : entry_of<false>(p, r * kRange + t);
+        const Entry q = r == range ? e : entry_of<false>(p, r * R + t);
         long long g = q.valid ? q.pages : 0, h = q.valid ? q.tokens : 0;
         if (p.ranges > 1) {
             block_scan(s, g, h);
@@ -272,13 +285,13 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
             h = c;
         }
         const bool ok = total + g <= free && done + h <= p.tokens;
-        const int n = __syncthreads_count(ok);
+        const int n = block_count<R>(ok);
         if (t == n - 1) s.before_a = total + g, s.before_b = done + h;
         if (ok && q.valid) p.pool.lens[q.row] = q.len + q.tokens;
-        __syncthreads();
+        block_sync<R>();
         if (n > 0) total = s.before_a, done = s.before_b;
-        __syncthreads();
-        if (n < kRange) break;
+        block_sync<R>();
+        if (n < R) break;
     }
     if (t == 0) {
         p.pool.counters[0] = free - static_cast<int>(total);
@@ -286,50 +299,49 @@ __global__ void __launch_bounds__(kRange) pages_extend_kernel(const __grid_const
     }
 }
 
-__global__ void __launch_bounds__(kRange) pages_trim_kernel(const __grid_constant__ PagesParams p)
+template <int R>
+__global__ void __launch_bounds__(R) pages_trim_kernel(const __grid_constant__ PagesParams p)
 {
-    __shared__ Shared s;
+    __shared__ Shared<R> s;
     pdl_trigger();
     pdl_wait();
     const int t = threadIdx.x, range = blockIdx.x;
     const int free = min(max(p.pool.counters[0], 0), p.pool.num_pages);
-    // pages that the entries before this range give back, and all entries
-    long long before = 0, all = 0;
-    for (int i = t; i < p.ranges * kRange; i += kRange) {
-        const Entry q = entry_of<true>(p, i);
-        all += q.pages;
-        if (i < range * kRange) before += q.pages;
-    }
-    block_scan(s, before, all);
-    if (t == kRange - 1) s.before_a = before, s.before_b = all;
-    __syncthreads();
-    const long long first = s.before_a;
-    const int count = static_cast<int>(min(s.before_b, static_cast<long long>(p.pool.num_pages - free)));
-    const Entry e = entry_of<true>(p, range * kRange + t);
+    const Entry e = entry_of<true>(p, range * R + t);
     long long a = e.pages, none = 0;
     block_scan(s, a, none);
+    // pages that the entries before this range give back, and all entries
+    if (p.ranges > 1) {
+        long long before = 0, all = 0;
+        for (int i = t; i < p.ranges * R; i += R) {
+            const Entry q = entry_of<true>(p, i);
+            all += q.pages;
+            if (i < range * R) before += q.pages;
+        }
+        block_scan(s, before, all);
+        if (t == R - 1) s.before_a = before, s.before_b = all;
+    } else if (t == R - 1) {
+        s.before_a = 0, s.before_b = a;
+    }
+    block_sync<R>();
+    const long long first = s.before_a;
+    const int count = static_cast<int>(min(s.before_b, static_cast<long long>(p.pool.num_pages - free)));
     s.first[0][t + 1] = static_cast<int>(a);
     if (t == 0) s.first[0][0] = 0;
     s.row[t] = e.row;
     s.held[t] = e.held - e.pages;  // what is kept
-    __syncthreads();
-    for (int x = t; x < s.first[0][kRange]; x += kRange) {
-        const int i = find(s.first[0], kRange, x);
+    block_sync<R>();
+    // (this block has read the requests' lengths and the free pages; as above)
+    if (gridDim.x > 1 && t == 0) s.last = atomicAdd(reinterpret_cast<unsigned *>(p.pool.counters + 1), 1u) == gridDim.x - 1;
+    for (int x = t; x < s.first[0][R]; x += R) {
+        const int i = find(s.first[0], R, x);
         const long long at = free + count - 1 - (first + x);  // (a pool that is in order has room for all)
         if (at >= free) p.pool.free_pages[at] = p.pool.page_table[s.row[i] * p.pool.table_stride + s.held[i] + x - s.first[0][i]];
     }
-    if (gridDim.x > 1) {
-        __threadfence();
-        __syncthreads();
-        if (t == 0) s.last = atomicAdd(reinterpret_cast<unsigned *>(p.pool.counters + 1), 1u) == gridDim.x - 1;
-        __syncthreads();
-        if (!s.last) return;
-        __threadfence();
-    } else {
-        __syncthreads();
-    }
+    block_sync<R>();
+    if (gridDim.x > 1 && !s.last) return;
     for (int r = 0; r < p.ranges; ++r) {
-        const Entry q = r == range ? e : entry_of<true>(p, r * kRange + t);
+        const Entry q = r == range ? e : entry_of<true>(p, r * R + t);
         if (q.row >= 0) p.pool.lens[q.row] = q.tokens;
     }
     if (t == 0) {
@@ -406,7 +418,6 @@ extern "C" dflash_status dflash_pages_extend(const dflash_page_pool *pool, const
     p.rows = rows;
     p.counts = new_tokens;
     p.batch = batch;
-    p.ranges = batch > 0 ? (batch + dfl::kRange - 1) / dfl::kRange : 1;
     p.tokens = tokens;
     p.base = -1;
     p.cu = cu_tokens;
@@ -417,15 +428,20 @@ extern "C" dflash_status dflash_pages_extend(const dflash_page_pool *pool, const
     p.positions = positions;
     p.slots = slots;
     p.granted = granted;
-    // parts: a block per 2048 tokens or, of a separate page table, per 4 entries of the batch and 32 of their columns
-    int64_t work = positions || slots ? tokens / 2048 : 0;
-    const int64_t copy = page_table ? static_cast<int64_t>(batch) * table_cols / 8192 : 0;
+    // one warp for a batch of up to 32 with little to write, else blocks of 256 or, over 256 entries, of 1024; and as many
+    // blocks (up to 304) as there are times 512 tokens or, of a separate page table, half filled, 512 entries
+    int64_t work = positions || slots ? tokens : 0;
+    const int64_t copy = page_table ? static_cast<int64_t>(batch) * table_cols / 2 : 0;
     if (copy > work) work = copy;
-    const int64_t most = 128 / p.ranges > 1 ? 128 / p.ranges : 1;
-    work = work / p.ranges + 1;
+    const int R = batch <= 32 && work <= 1024 ? 32 : batch <= 256 ? 256 : 1024;
+    p.ranges = batch > 0 ? (batch + R - 1) / R : 1;
+    const int64_t most = 304 / p.ranges > 1 ? 304 / p.ranges : 1;
+    work = work / 512 / p.ranges + 1;
     p.parts = static_cast<int>(work < most ? work : most);
-    const cudaError_t e = dfl::launch_ex(dfl::pages_extend_kernel, dim3(p.ranges * p.parts), dim3(dfl::kRange), 0,
-                                         static_cast<cudaStream_t>(stream), 1, p);
+    const cudaError_t e = dfl::launch_ex(R == 32    ? dfl::pages_extend_kernel<32>
+                                         : R == 256 ? dfl::pages_extend_kernel<256>
+                                                    : dfl::pages_extend_kernel<1024>,
+                                         dim3(p.ranges * p.parts), dim3(R), 0, static_cast<cudaStream_t>(stream), 1, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return pages_fail(DFLASH_ERR_CUDA, "the launch failed (error %lld)", e);
@@ -445,10 +461,13 @@ extern "C" dflash_status dflash_pages_trim(const dflash_page_pool *pool, const i
     p.counts = counts;
     p.base = base;
     p.batch = batch;
-    p.ranges = (batch + dfl::kRange - 1) / dfl::kRange;
+    const int R = batch <= 32 ? 32 : batch <= 256 ? 256 : 1024;
+    p.ranges = (batch + R - 1) / R;
     p.parts = 1;
-    const cudaError_t e = dfl::launch_ex(dfl::pages_trim_kernel, dim3(p.ranges), dim3(dfl::kRange), 0,
-                                         static_cast<cudaStream_t>(stream), 1, p);
+    const cudaError_t e = dfl::launch_ex(R == 32    ? dfl::pages_trim_kernel<32>
+                                         : R == 256 ? dfl::pages_trim_kernel<256>
+                                                    : dfl::pages_trim_kernel<1024>,
+                                         dim3(p.ranges), dim3(R), 0, static_cast<cudaStream_t>(stream), 1, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return pages_fail(DFLASH_ERR_CUDA, "the launch failed (error %lld)", e);
