@@ -178,6 +178,26 @@ def test_a_long_prompt(pkg):
     both.trim([15990, 3], [0, 2])
 
 
+@pytest.mark.parametrize("requests", [1, 40, 300])
+def test_thousands_of_pages_move_at_once(pkg, requests):
+    """Without positions and slots, a call's blocks share its pages all the same; a trim's as well."""
+    r = random.Random(requests)
+    cols = 12000 // requests + 3
+    m = Model(requests, cols, 12000, 2)
+    pool = pkg.PagePool.empty(requests=requests, cols=cols, num_pages=12000, page_size=2)
+    rows = r.sample(range(requests), requests)
+    new = [2 * cols - 7 + r.randint(0, 3) for _ in rows]
+    for drop in ([r.randint(0, 2 * cols) for _ in rows], [10 ** 6] * requests):
+        m.extend(rows, new, 1 << 30)
+        pool.extend(None, dev(new), rows=dev(rows))
+        m.trim(rows, drop)
+        table = pool.page_table.tolist()
+        pool.trim(dev(drop), rows=dev(rows))
+        assert pool.lens.tolist() == m.lens and pool.counters.tolist() == [len(m.free), 0]
+        assert pool.free_pages[:len(m.free)].tolist() == m.free
+        assert all(table[q][:m.need(m.lens[q])] == m.table[q][:m.need(m.lens[q])] for q in range(requests))
+
+
 def test_accepted_drafts_and_ended_requests(pkg):
     pool = pkg.PagePool.empty(requests=4, cols=8, num_pages=32, page_size=16)
     L = 7
