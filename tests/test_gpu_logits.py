@@ -200,6 +200,46 @@ def test_a_long_history_of_one_token(pkg):
     assert out[0, 0, 3] == -n / 1024 and out[0, 0].abs().sum() == n / 1024 and (out[1] == 0).all()
 
 
+@pytest.mark.parametrize("hist", [30000, 36000])
+@pytest.mark.parametrize("V", [40000, 40001])
+def test_most_of_the_vocabulary_has_occurred(pkg, hist, V):
+    """More tokens than a list holds, with counts in 16 and in 32 bits."""
+    g = gen(hist)
+    logits = torch.randn(2, 3, V, device="cuda", generator=g).to(BF16)
+    r = rules_for(g, 2, V, 1, ALL)
+    r["tokens"] = torch.stack([torch.randperm(V, device="cuda", generator=g)[:hist] for _ in range(2)]).to(torch.int32)
+    r["lens"] = torch.tensor([hist, hist - 11], device="cuda", dtype=torch.int32)
+    r["bias_ids"] = torch.randint(0, V, (2, 9), device="cuda", generator=g, dtype=torch.int32)
+    r["bias_values"] = torch.randn(2, 9, device="cuda", generator=g)
+    check(pkg, logits, r, torch.randint(0, V, (2, 2), device="cuda", generator=g, dtype=torch.int32))
+
+
+def test_drafts_that_fill_a_list(pkg):
+    """Lists that the positions of one sequence fill to 2048 tokens of the first ones (which one CTA has) and beyond."""
+    B, T, V = 40, 6, 65536
+    g = gen(3)
+    logits = torch.randn(B, T, V, device="cuda", generator=g).to(BF16)
+    r = rules_for(g, B, V, 2050, ("repetition", "presence", "frequency"))
+    r["tokens"] = torch.arange(2050, device="cuda", dtype=torch.int32).repeat(B, 1)
+    r["lens"] = 2044 + torch.arange(B, device="cuda", dtype=torch.int32) % 6
+    r["prompt_lens"] = torch.full((B,), 700, device="cuda", dtype=torch.int32)
+    late = torch.tensor([2047, 65535, 2046, 5, 32768, 2045, 2047, 16384, 16385, 900], device="cuda", dtype=torch.int32)
+    draft = late[(torch.arange(B, device="cuda")[:, None] + torch.arange(T - 1, device="cuda")) % len(late)].contiguous()
+    check(pkg, logits, r, draft)
+
+
+@pytest.mark.parametrize("V,dtype,hist", [(262144, FP32, 40000), (1700000, BF16, 0), (1100001, FP16, 0)])
+def test_largest_vocabularies(pkg, V, dtype, hist):
+    g = gen(V)
+    logits = (3 * torch.randn(1, 2, V, device="cuda", generator=g)).to(dtype)
+    r = rules_for(g, 1, V, hist, ALL if hist else ("temperature",))
+    if hist:
+        r["bias_ids"] = torch.randint(0, V, (1, 300), device="cuda", generator=g, dtype=torch.int32)
+        r["bias_values"] = torch.randn(1, 300, device="cuda", generator=g)
+    mask = torch.randint(-2 ** 31, 2 ** 31, (1, 2, -(-V // 32)), device="cuda", generator=g).to(torch.int32)
+    check(pkg, logits, r, torch.full((1, 1), V - 1, device="cuda", dtype=torch.int32), mask)
+
+
 @pytest.mark.parametrize("V", [40, 20000, 32001])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_rows_without_a_choice_and_values_that_are_no_numbers(pkg, V, dtype):
