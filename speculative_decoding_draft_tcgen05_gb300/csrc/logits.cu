@@ -11,10 +11,12 @@
 // occurrences in shared memory, a thread an entry, and left out of the passes
 // over all the others: the first finds the best token and, relative to each
 // thread's running maximum, the sum of the exponentials; the warps of all CTAs
-// exchange those through distributed shared memory, with one cluster barrier;
-// the second writes the probabilities. HBM sees the logits and the outputs
-// once, which is what bounds a large batch; a small one is bound by the chain
-// history -> table -> list -> exchange.
+// send those to all CTAs (st.async, counted by an mbarrier of the receiver: a
+// cluster barrier in its place cost 1.5 us a position, 120 us against 105 for 32
+// sequences of 8); the second writes the probabilities. HBM sees the logits and
+// the outputs once, which is what bounds a large batch (without penalties 3.9
+// TB/s of 238 MB); with them the lists' chains do (105 us against 59), and a
+// small call the chain history -> table -> list -> exchange (9.3 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdio.h>
@@ -323,7 +325,8 @@ __device__ __forceinline__ void exponentials(float2 (&x)[kPer / 2], float2 less,
 
 struct Shared {
     Best peer[2][kMaxCluster * kWarps];
-    uint64_t full;  // a position's logits have arrived
+    uint64_t full;     // a position's logits have arrived
+    uint64_t came[2];  // the warps' results of a position have
     int abort_flag;
     int warp_n[kWarps];
     int n;  // entries of the list
@@ -361,6 +364,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     }
     if (tid == 0) {
         mbar_init(smem_u32(&s.full), 1);
+        mbar_init(smem_u32(&s.came[0]), 1);
+        mbar_init(smem_u32(&s.came[1]), 1);
         s.abort_flag = 0;
         s.n = 0;
         fence_mbar_init();
@@ -378,12 +383,14 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     auto bring = [&](int t) {
         const T *const row = row_at(t);
         if (kVec) {
-            if (tid == 0) {
+            if (warp == 0) {
                 const uint32_t bar = smem_u32(&s.full);
-                uint32_t bytes = 0;
-                for (int i = 0; i < mine; ++i) bytes += static_cast<uint32_t>(min(kStep, vocab - token_of(i * kStep)) * sizeof(T));
-                mbar_arrive_expect_tx(bar, bytes);
-                for (int i = 0; i < mine; ++i) {
+                if (lane == 0) {
+                    const int end = mine > 0 ? token_of((mine - 1) * kStep) + kStep : 0;  // behind the last piece
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>((mine * kStep - max(0, end - vocab)) * sizeof(T)));
+                }
+                __syncwarp();
+                for (int i = lane; i < mine; i += 32) {
                     const int v = token_of(i * kStep);
                     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                      smem_u32(logits + i * kStep)),
@@ -392,15 +399,17 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                 }
             }
         } else {  // rows that do not start on 16 bytes
-            for (int i = 0; i < mine; ++i) {
+            for (int i = 0; i < mine; ++i) {  // (a whole piece without looking at its end: 8 loads under way a thread)
                 const int v = token_of(i * kStep) + tid;
                 T x[kPer];
+                if (v - tid + kStep <= vocab) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (v + j * kThreads < vocab) x[j] = row[v + j * kThreads];
+                    for (int j = 0; j < kPer; ++j) x[j] = row[v + j * kThreads];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (v + j * kThreads < vocab) logits[i * kStep + tid + j * kThreads] = x[j];
+                    for (int j = 0; j < kPer; ++j) logits[i * kStep + tid + j * kThreads] = x[j];
+                } else {
+                    for (int j = 0; v + j * kThreads < vocab; ++j) logits[i * kStep + tid + j * kThreads] = row[v + j * kThreads];
+                }
             }
         }
     };
@@ -416,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     };
     __syncthreads();
     // (waited for before the first exchange: every CTA's shared memory exists before another writes to it)
+    const bool exchange = C > 1 && (p.probs || p.argmax);
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_trigger();
     pdl_wait();
@@ -491,13 +501,38 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     if (scale == 0.f) scale = 1.1754944e-38f;      // and a masked token's -inf * scale -inf)
     const float2 scale2 = make_float2(scale, scale);
     const bool want_sum = p.probs && !greedy, want_best = p.argmax || (p.probs && greedy);
-    bool arrived = true;  // (a copy that does not arrive in a second: NaN and -1)
+    // With the best token alone wanted, a position's exchange passes beside the next one's pass, and who has it knows it: the
+    // last one's goes to rank 0 alone.
+    const bool lazy = exchange && !p.out && !p.probs;
+    bool arrived = true;  // (what does not arrive in a second: NaN and -1)
+    // All warps' results of position t, joined.
+    auto collect = [&](int t, bool read) {
+        if (C > 1) arrived = mbar_wait(smem_u32(&s.came[t & 1]), static_cast<uint32_t>((t - t0) >> 1) & 1u, &s.abort_flag) && arrived;
+        __syncwarp();
+        Best q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
+        if (!read) return q;
+        for (int u = lane; u < C * kWarps; u += 32) {
+            const Best a = s.peer[t & 1][u];
+            if (a.m > q.m) {
+                q.s *= exp2_fast((q.m - a.m) * scale);
+                q.m = a.m;
+            }
+            q.s += a.m == q.m ? a.s : a.s * exp2_fast((a.m - q.m) * scale);
+            join_best(q.v, q.id, a.v, a.id);
+        }
+        reduce(q, scale, want_sum, want_best);
+        return q;
+    };
+    auto best_of = [&](const Best &q) { return q.id == 0x7FFFFFFF || !arrived ? -1 : q.id; };
+    auto store_best = [&](int t, const Best &q) {
+        if (p.argmax && rank == 0 && tid == 0) p.argmax[static_cast<int64_t>(b) * p.rows + t] = best_of(q);
+    };
     for (int t = t0; t < t1; ++t) {
         const int64_t at_row = static_cast<int64_t>(b) * p.rows + t;
         T *const out = p.out ? static_cast<T *>(p.out) + b * p.out_seq_stride + t * p.out_row_stride : nullptr;
         if (kVec) {
             arrived = mbar_wait(smem_u32(&s.full), static_cast<uint32_t>(t - t0) & 1u, &s.abort_flag) && arrived;
-            if (t + 1 < t1 && tid < mine) {  // the next position's logits come to L2 beside this one's passes
+            if (t + 1 < t1 && tid < mine) {  // the next position's logits come to L2 beside this one's passes (mine < 256)
                 const int v = token_of(tid * kStep);
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row_at(t + 1) + v),
                              "r"(static_cast<uint32_t>(min(kStep, vocab - v) * sizeof(T)))
@@ -597,36 +632,32 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                     }
                 });
             reduce(q, scale, want_sum, want_best);
+            if (lazy && t > t0) store_best(t - 1, collect(t - 1, rank == 0 && warp == 0));
             Best *const here = &s.peer[t & 1][rank * kWarps + warp];
             if (C > 1) {
-                if (lane < C)
-                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                // To every CTA. (A position's place is written again two positions on: by then a warp has every other warp's
+                // results of the position between, and those were sent when this one's had been read.)
+                const bool one = lazy && t + 1 == t1;
+                if (tid == 0 && (rank == 0 || !one))
+                    mbar_arrive_expect_tx(smem_u32(&s.came[t & 1]), static_cast<uint32_t>(C * kWarps * sizeof(Best)));
+                if (lane < (one ? 1 : C))
+                    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
                                      mapa_shared(smem_u32(here), static_cast<uint32_t>(lane))),
-                                 "r"(__float_as_uint(q.m)), "r"(__float_as_uint(q.s)), "r"(__float_as_uint(q.v)), "r"(q.id)
+                                 "r"(__float_as_uint(q.m)), "r"(__float_as_uint(q.s)), "r"(__float_as_uint(q.v)), "r"(q.id),
+                                 "r"(mapa_shared(smem_u32(&s.came[t & 1]), static_cast<uint32_t>(lane)))
                                  : "memory");
                 __syncwarp();
-                // (the next position writes the other half: who reads this one has not passed that exchange)
-                cluster_sync_all();
+                if (t + 1 == t1 && (lazy || p.group == 1)) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
             } else {
                 if (lane == 0) *here = q;
                 __syncthreads();
             }
-            if (p.probs || (rank == 0 && warp == 0)) {
-                q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
-                for (int u = lane; u < C * kWarps; u += 32) {
-                    const Best a = s.peer[t & 1][u];
-                    if (a.m > q.m) {
-                        q.s *= exp2_fast((q.m - a.m) * scale);
-                        q.m = a.m;
-                    }
-                    q.s += a.m == q.m ? a.s : a.s * exp2_fast((a.m - q.m) * scale);
-                    join_best(q.v, q.id, a.v, a.id);
-                }
-                reduce(q, scale, want_sum, want_best);
+            if (!lazy) {
+                q = collect(t, p.probs || (rank == 0 && warp == 0));
+                store_best(t, q);
             }
         }
-        const int id = q.id == 0x7FFFFFFF || !arrived ? -1 : q.id;
-        if (p.argmax && rank == 0 && tid == 0) p.argmax[at_row] = id;
+        const int id = best_of(q);
         float *const probs = p.probs ? p.probs + at_row * p.vocab : nullptr;
         const float base = q.m == -INFINITY ? 0.f : q.m;
         // (nothing above -inf: zeros. A sum that is no number makes all of them such.)
@@ -680,7 +711,12 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
             }
         }
     }
-    // (after the last exchange nobody writes to another CTA)
+    // no CTA ends while another may still send to it
+    if (lazy && rank == 0) store_best(t1 - 1, collect(t1 - 1, warp == 0));
+    // (a cluster that ends together leaves room for one of the next call's on as many SMs: with several positions each, 32
+    // sequences of 8 took 115 us otherwise, against 104; with one position each it costs 2 %)
+    if (p.group > 1 && C > 1 && !lazy) cluster_sync_all();
+    else if (exchange) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 dflash_status logits_fail(dflash_status st, const char *fmt, long long a = 0, long long b = 0)
@@ -822,9 +858,10 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     const int64_t slice = slice_of(C);
     if (slice > int64_t(1) << 24 || bytes_of(slice) > smem_most)
         return logits_fail(DFLASH_ERR_UNSUPPORTED, "a vocabulary of %lld needs more shared memory than there is (%lld bytes a CTA)", vocab, smem_most);
-    // positions per cluster: a sequence's list is laid out once for them, but two CTAs an SM have work
+    // positions per cluster: a sequence's list is laid out once for them, but three CTAs an SM have work (24 sequences of 8:
+    // 77 us by 4, 84 by 8; 32: 90 by 4, 85 by 8)
     int group = 1;
-    while ((p.counted || p.biased) && group < rows && static_cast<int64_t>(batch) * ((rows + 2 * group - 1) / (2 * group)) * C >= 2 * sms) group *= 2;
+    while ((p.counted || p.biased) && group < rows && static_cast<int64_t>(batch) * ((rows + 2 * group - 1) / (2 * group)) * C >= 3 * sms) group *= 2;
     p.group = group < rows ? group : rows;
     p.groups = (rows + p.group - 1) / p.group;
     p.slice = static_cast<int>(slice);
