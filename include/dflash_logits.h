@@ -58,8 +58,8 @@ typedef struct {
  *   mask   int32 words, bit v % 32 of word v / 32 set where token v is allowed: words of position t of sequence b at
  *          mask + b * mask_seq_stride + t * mask_row_stride (a stride of 0 shares them)
  * Outputs overlap nothing else. 0 <= batch, rows (0 launches nothing), batch * rows < 2^31; vocab >= 1, and what 16
- * CTAs' shared memory holds of it (UNSUPPORTED above): 262,144 tokens in every case, a million and more of 16-bit
- * logits without penalties and biases. A position whose logits do not arrive on the SM within a second (a fault of the
+ * CTAs' shared memory holds of it (UNSUPPORTED above): 262,144 tokens with up to 8192 biases, a million and more of
+ * 16-bit logits without penalties and biases. A position whose logits do not arrive on the SM within a second (a fault of the
  * machine) gets NaN and -1. No handle, no workspace; launched on the current device.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 dflash_status dflash_logits_adjust(const void *logits, int64_t seq_stride, int64_t row_stride, int32_t batch, int32_t rows,

@@ -41,7 +41,7 @@ constexpr int kLogStep = 11;
 constexpr int kStep = 1 << kLogStep;     // tokens of a CTA in a step
 static_assert(kStep == kThreads * kPer, "a step is a piece");
 constexpr int kMaxCluster = 16;
-constexpr int kMaxList = 2048;           // tokens of a CTA on its list; with more it goes by the bits
+constexpr int kMaxList = 1536;           // tokens of a CTA on its list; with more it goes by the bits
 
 struct LogitsParams {
     const void *logits;
@@ -119,35 +119,46 @@ __device__ __forceinline__ void reduce(Best &q, float scale, bool sum, bool best
 }
 
 // Shared memory in words: a position's logits; the mask's bits; bits of the tokens on the list (marks) and of those with a
-// bias (listed); the list; a table of what has occurred, which the list is made from; places in the list of biases. Entries of
-// a table are 32 bits (wide) or 16: the highest says that the token is in the prompt, the others how often it has occurred
-// behind it. (Two positions' logits, one on its way beside the other, left room for fewer CTAs: 230 us against 115 for 256
-// positions of 151,936 tokens after 8000.)
+// bias (listed); the list; a table of what has occurred, which the list is made from; a hash table of the listed tokens' places
+// in the list of biases. Entries of the table are 32 bits (wide) or 16: the highest says that the token is in the prompt, the
+// others how often it has occurred behind it. What counts is how many CTAs fit an SM. Four do with the tables of 151,936 tokens
+// of 16 bits and 512 biases; a second table in place of the hash left room for three (134 us against 90 for 32 sequences of 8
+// after 2000 with 300 biases), a list of 2048 for two with 32-bit logits, not three (170 us against 130), and a position's
+// logits on their way beside the last one's for two (230 us against 115 for 256 positions after 8000).
 struct Room {
-    int logits, bits, list, counts, bias, total;
+    int logits, bits, list, counts, places, total;
 };
 
-__host__ __device__ inline Room room_of(int slice, int size, int most, bool counted, bool biased, bool wide)
+// Slots of the hash table: a power of two, and no fewer than a CTA's tokens with a bias.
+__host__ __device__ inline int slots_of(int slice, int biases)
+{
+    if (biases == 0) return 0;
+    int n = 4;
+    while (n < biases && n < slice) n *= 2;
+    return n;
+}
+
+__host__ __device__ inline Room room_of(int slice, int size, int most, bool counted, int biases, bool wide)
 {
     Room r = {slice / 4 * size, slice / 32, 0, 0, 0, 0};
     r.total = r.logits + r.bits;
-    if (!counted && !biased) return r;
-    const int table = wide ? slice : slice / 2;
+    if (!counted && biases == 0) return r;
     r.list = ((most < kMaxList ? most : kMaxList) + 3) / 4 * (wide ? 8 : 4);
-    r.counts = counted ? table : 0;
-    r.bias = biased ? table : 0;
-    r.total += 2 * r.bits + r.list + r.bias + r.counts;
+    r.counts = counted ? (wide ? slice : slice / 2) : 0;
+    r.places = slots_of(slice, biases) * (wide ? 2 : 1);
+    r.total += (biases > 0 ? 2 : 1) * r.bits + r.list + r.places + r.counts;
     return r;
 }
 
 // A CTA's tokens on the list. Tokens go by their index in the CTA's own.
 struct Marked {
-    uint32_t *marks, *listed, *list, *counts, *bias;
+    uint32_t *marks, *listed, *list, *counts, *places;
+    uint32_t slots;
     bool wide;
 
-    __device__ __forceinline__ uint32_t get(const uint32_t *table, int at) const
+    __device__ __forceinline__ uint32_t occurrence(int at) const
     {
-        return wide ? table[at] : table[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
+        return wide ? counts[at] : counts[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
     }
     __device__ __forceinline__ bool bit(const uint32_t *bits, int at) const { return bits[at >> 5] >> (at & 31) & 1u; }
 
@@ -166,19 +177,31 @@ struct Marked {
     // how often, of an entry that is not 0
     __device__ __forceinline__ float times(uint32_t entry) const { return static_cast<float>(entry & (wide ? 0x7FFFFFFFu : 0x7FFFu)); }
 
-    __device__ __forceinline__ void has_bias(int at, uint32_t place) const  // the last one counts
+    // Where the search for a token begins (Knuth's multiplicative hashing); it goes on slot by slot.
+    __device__ __forceinline__ uint32_t slot(int at) const { return static_cast<uint32_t>(at) * 0x9E3779B1u >> (__clz(slots) + 1); }
+
+    // A slot is the token and its place by 16 bits each, or (wide) the token, 1 more, and its place.
+    __device__ __forceinline__ void has_bias(int at, uint32_t place) const  // place > 0; the last one counts
     {
         atomicOr(listed + (at >> 5), 1u << (at & 31));
-        if (wide) {
-            atomicMax(bias + at, place);
+        for (uint32_t i = slot(at);; i = (i + 1) & (slots - 1)) {
+            const uint32_t key = wide ? static_cast<uint32_t>(at) + 1u : static_cast<uint32_t>(at) << 16 | place;
+            uint32_t *const word = wide ? places + 2 * i : places + i;
+            const uint32_t was = atomicCAS(word, 0u, key);
+            if (was != 0u && (wide ? was != key : was >> 16 != static_cast<uint32_t>(at))) continue;
+            if (wide) atomicMax(word + 1, place);
+            else if (was != 0u) atomicMax(word, key);
             return;
         }
-        uint32_t *const word = bias + (at >> 1);
-        const int sh = 16 * (at & 1);
-        for (uint32_t old = *word; (old >> sh & 0xFFFFu) < place;) {
-            const uint32_t was = atomicCAS(word, old, (old & ~(0xFFFFu << sh)) | place << sh);
-            if (was == old) break;
-            old = was;
+    }
+    __device__ __forceinline__ uint32_t place(int at) const  // of a listed token
+    {
+        for (uint32_t i = slot(at);; i = (i + 1) & (slots - 1)) {
+            if (wide) {
+                if (places[2 * i] == static_cast<uint32_t>(at) + 1u) return places[2 * i + 1];
+            } else if (places[i] >> 16 == static_cast<uint32_t>(at) && places[i] != 0u) {
+                return places[i] & 0xFFFFu;
+            }
         }
     }
 
@@ -341,16 +364,17 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     const int C = p.C;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const bool tables = p.counted || p.biased;
-    const Room room = room_of(p.slice, sizeof(T), p.most, p.counted, p.biased, p.wide);
+    const Room room = room_of(p.slice, sizeof(T), p.most, p.counted, p.biased ? p.r.bias_count : 0, p.wide);
     uint32_t *const words = reinterpret_cast<uint32_t *>(smem);
     T *const logits = reinterpret_cast<T *>(words);
     uint32_t *const mask = words + room.logits;
     Marked mk;
     mk.marks = mask + room.bits;
     mk.listed = mk.marks + room.bits;
-    mk.list = mk.listed + room.bits;
-    mk.bias = mk.list + room.list;
-    mk.counts = mk.bias + room.bias;
+    mk.list = mk.listed + (p.biased ? room.bits : 0);
+    mk.places = mk.list + room.list;
+    mk.counts = mk.places + room.places;
+    mk.slots = static_cast<uint32_t>(room.places) >> (p.wide ? 1 : 0);
     mk.wide = p.wide;
     if (tables) {
         auto clear = [&](uint32_t *from, int n) {
@@ -359,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         if (p.counted) clear(mk.counts, room.counts);
         if (p.biased) {
             clear(mk.listed, room.bits);
-            clear(mk.bias, room.bias);
+            clear(mk.places, room.places);
         }
     }
     if (tid == 0) {
@@ -490,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         for (int w = tid; n > 0; w += kThreads)
             for (uint32_t m = reinterpret_cast<const uint8_t *>(mk.marks)[w]; m; m &= m - 1, ++e, --n) {
                 const int at = w * 8 + __ffs(m) - 1;
-                if (e < kMaxList) mk.put(e, at, p.counted ? mk.get(mk.counts, at) : 0u);
+                if (e < kMaxList) mk.put(e, at, p.counted ? mk.occurrence(at) : 0u);
             }
     }
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -597,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                     const float c = mk.times(entry);
                     if (c > 0.f) x = __fsub_rn(__fsub_rn(x, __fmul_rn(beta, c)), alpha);
                 }
-                if (p.biased && mk.bit(mk.listed, at)) x = __fadd_rn(x, bias_values[mk.get(mk.bias, at) - 1]);
+                if (p.biased && mk.bit(mk.listed, at)) x = __fadd_rn(x, bias_values[mk.place(at) - 1]);
                 body(mk.bit(mask, at) ? x : -INFINITY, v);
             };
             // (by the bits if the list is too short: one loop for both, a step of which finds the next token)
@@ -615,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                     at = w * 8 + __ffs(m) - 1;
                     m &= m - 1;
                 }
-                one(at, listed ? mk.count(e) : p.counted ? mk.get(mk.counts, at) : 0u);
+                one(at, listed ? mk.count(e) : p.counted ? mk.occurrence(at) : 0u);
                 e += kThreads;
             }
         };
@@ -849,7 +873,7 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     auto bytes_of = [&](int64_t slice) {
         p.wide = entries > 32767 || slice > 65536;
         p.most = static_cast<int>(entries < slice ? entries : slice);
-        return static_cast<int64_t>(dfl::room_of(static_cast<int>(slice), size, p.most, p.counted, p.biased, p.wide).total) * 4;
+        return static_cast<int64_t>(dfl::room_of(static_cast<int>(slice), size, p.most, p.counted, p.r.bias_count, p.wide).total) * 4;
     };
     int C = 1;
     while (C < dfl::kMaxCluster && (slice_of(C) > int64_t(1) << 24 || bytes_of(slice_of(C)) > 50 * 1024 ||
@@ -867,13 +891,15 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     p.slice = static_cast<int>(slice);
     p.C = C;
     while ((1 << p.log_c) < C) ++p.log_c;
-    const size_t smem = static_cast<size_t>(bytes_of(slice));
+    size_t smem = static_cast<size_t>(bytes_of(slice));
     const int per = 16 / size;
     const bool vec = !dfl::misaligned(logits, 16) && seq_stride % per == 0 && row_stride % per == 0 && vocab % 8 == 0 &&
                      (!out || (!dfl::misaligned(out, 16) && out_seq_stride % per == 0 && out_row_stride % per == 0)) &&
                      !dfl::misaligned(probs, 16);
     const int64_t clusters = static_cast<int64_t>(batch) * p.groups;
     if (clusters >= (int64_t(1) << 31)) return logits_fail(DFLASH_ERR_INVALID_ARG, "too many positions");
+    // fewer CTAs than SMs: at most two of them on one (with up to four one block of 8 without penalties took 8.1 us, so 7.4)
+    if (clusters * C <= sms && smem < static_cast<size_t>(smem_most) * 2 / 5) smem = static_cast<size_t>(smem_most) * 2 / 5;
     e = dfl::launch_ex(dfl::kernel_of(dtype, vec), dim3(static_cast<unsigned>(clusters), 1, C), dim3(dfl::kThreads),
                        smem, static_cast<cudaStream_t>(stream), C, p);
     if (e != cudaSuccess) {

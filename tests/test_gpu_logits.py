@@ -228,21 +228,34 @@ def test_drafts_that_fill_a_list(pkg):
     check(pkg, logits, r, draft)
 
 
-def test_drafts_that_fill_one_ctas_list(pkg):
-    """Lists that the positions of one sequence fill to 2048 tokens of one CTA (of up to 8, which take turns at 2048) and beyond."""
+@pytest.mark.parametrize("n", [1536, 2048])
+def test_drafts_that_fill_one_ctas_list(pkg, n):
+    """Lists that the positions of one sequence fill to n tokens of one CTA (of up to 8, which take turns at 2048) and beyond."""
     B, T, V = 40, 6, 65536
     g = gen(3)
     logits = torch.randn(B, T, V, device="cuda", generator=g).to(BF16)
     r = rules_for(g, B, V, 2050, ("repetition", "presence", "frequency"))
     own = torch.arange(65536 // 8, device="cuda", dtype=torch.int32)
     own = (own >> 11 << 14) + (own & 2047)
-    r["tokens"] = own[:2050].repeat(B, 1)
-    r["lens"] = 2044 + torch.arange(B, device="cuda", dtype=torch.int32) % 6
+    r["tokens"] = own[:n + 2].repeat(B, 1)
+    r["lens"] = n - 4 + torch.arange(B, device="cuda", dtype=torch.int32) % 6
     r["prompt_lens"] = torch.full((B,), 700, device="cuda", dtype=torch.int32)
-    late = own[[2047, 8191, 2046, 5, 2048, 2045, 2047, 3000, 3001, 900]].clone()
+    late = own[[n - 1, 8191, n - 2, 5, n, n - 3, n - 1, 3000, 3001, 900]].clone()
     late[3] = 65535  # (another CTA's)
     draft = late[(torch.arange(B, device="cuda")[:, None] + torch.arange(T - 1, device="cuda")) % len(late)].contiguous()
     check(pkg, logits, r, draft)
+
+
+@pytest.mark.parametrize("V,n", [(40, 200), (5000, 6000), (70000, 40000)])
+@pytest.mark.parametrize("hist", [0, 300])
+def test_many_biases(pkg, V, n, hist):
+    """More biases than tokens, each several times; more than 16 bits count."""
+    g = gen(n)
+    logits = torch.randn(2, 2, V, device="cuda", generator=g).to(BF16)
+    r = rules_for(g, 2, V, hist, ALL if hist else ())
+    r["bias_ids"] = torch.randint(-1, V + 1, (2, n), device="cuda", generator=g, dtype=torch.int32)
+    r["bias_values"] = torch.randn(2, n, device="cuda", generator=g)
+    check(pkg, logits, r, torch.randint(0, V, (2, 1), device="cuda", generator=g, dtype=torch.int32) if hist else None)
 
 
 @pytest.mark.parametrize("V,dtype,hist", [(262144, FP32, 40000), (1700000, BF16, 0), (1100001, FP16, 0)])
