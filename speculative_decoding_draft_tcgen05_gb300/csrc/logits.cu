@@ -755,6 +755,18 @@ bool misaligned(const void *p, uintptr_t by)
     return reinterpret_cast<uintptr_t>(p) % by != 0;
 }
 
+// Bytes of a tensor from its first to its last value.
+struct Span {
+    const void *from;
+    int64_t bytes;
+
+    bool meets(const Span &o) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(from), b = reinterpret_cast<uintptr_t>(o.from);
+        return from && o.from && a < b + static_cast<uintptr_t>(o.bytes) && b < a + static_cast<uintptr_t>(bytes);
+    }
+};
+
 using Kernel = void (*)(LogitsParams);
 
 Kernel kernel_of(int dtype, bool vec)
@@ -824,6 +836,14 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
         return logits_fail(DFLASH_ERR_INVALID_ARG, "strides must not be negative, those of out at least vocab");
     if (out == logits && (seq_stride != out_seq_stride || row_stride != out_row_stride))
         return logits_fail(DFLASH_ERR_INVALID_ARG, "out can be the logits only with their strides");
+    // (the logits and out may be slices of one buffer, whose rows pass one another; the others are packed)
+    const int64_t count = static_cast<int64_t>(batch) * rows;
+    const dfl::Span x_span = {logits, ((batch - 1) * seq_stride + (rows - 1) * row_stride + vocab) * size},
+                    out_span = {out, ((batch - 1) * out_seq_stride + (rows - 1) * out_row_stride + vocab) * size},
+                    probs_span = {probs, count * vocab * 4}, argmax_span = {argmax, count * 4};
+    if (probs_span.meets(x_span) || probs_span.meets(out_span) || argmax_span.meets(x_span) || argmax_span.meets(out_span) ||
+        argmax_span.meets(probs_span) || (out != logits && count == 1 && out_span.meets(x_span)))
+        return logits_fail(DFLASH_ERR_INVALID_ARG, "outputs must not overlap the logits or one another (but out may be the logits)");
     static const dflash_logits_rules none = {};
     dfl::LogitsParams p = {};
     p.r = rules ? *rules : none;

@@ -246,12 +246,12 @@ def test_drafts_that_fill_one_ctas_list(pkg, n):
     check(pkg, logits, r, draft)
 
 
-@pytest.mark.parametrize("V,n", [(40, 200), (5000, 6000), (70000, 40000)])
-@pytest.mark.parametrize("hist", [0, 300])
-def test_many_biases(pkg, V, n, hist):
+@pytest.mark.parametrize("V,n,hist,dtype", [(40, 200, 0, BF16), (40, 200, 300, BF16), (5000, 6000, 0, BF16), (5000, 6000, 300, FP16),
+                                            (70000, 40000, 0, BF16), (70000, 40000, 300, BF16), (262144, 8192, 33000, FP32)])
+def test_many_biases(pkg, V, n, hist, dtype):
     """More biases than tokens, each several times; more than 16 bits count."""
     g = gen(n)
-    logits = torch.randn(2, 2, V, device="cuda", generator=g).to(BF16)
+    logits = torch.randn(2, 2, V, device="cuda", generator=g).to(dtype)
     r = rules_for(g, 2, V, hist, ALL if hist else ())
     r["bias_ids"] = torch.randint(-1, V + 1, (2, n), device="cuda", generator=g, dtype=torch.int32)
     r["bias_values"] = torch.randn(2, n, device="cuda", generator=g)

@@ -260,6 +260,17 @@ def test_logits_refusals(lib):
     assert adjust(batch=0, x=None, best=None) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(probs=4096, dtype=3), dict(probs=4600), dict(probs=4032, best=None), dict(best=4604),
+                                dict(out=8192, probs=8700), dict(out=8192, best=8700), dict(probs=8192, best=9212),
+                                dict(batch=1, rows=1, out=4222)])
+def test_logits_refuse_outputs_that_overlap(lib, kw):
+    """Logits at 4096 (2 x 2 x 64 values of 16 bits: to 4607), rows of out likewise, 1024 bytes of probs, 16 of best."""
+    pkg, L = lib
+    c = {**dict(batch=2, rows=2, dtype=0, out=None, probs=None, best=64), **kw}
+    refused(lib, L.dflash_logits_adjust(4096, 128, 64, c["batch"], c["rows"], 64, c["dtype"], None, None, 1, None, 0, 0, c["out"],
+                                        128, 64, c["probs"], c["best"], None), "overlap")
+
+
 def test_pages_refusals(lib):
     pkg, L = lib
 
