@@ -59,14 +59,24 @@ typedef struct {
  *          mask + b * mask_seq_stride + t * mask_row_stride (a stride of 0 shares them)
  * Outputs overlap nothing else. 0 <= batch, rows (0 launches nothing), batch * rows < 2^31; vocab >= 1, and what 16
  * CTAs' shared memory holds of it (UNSUPPORTED above): 262,144 tokens with up to 8192 biases, a million and more of
- * 16-bit logits without penalties and biases. A position whose logits do not arrive on the SM within a second (a fault of the
- * machine) gets NaN and -1. No handle, no workspace; launched on the current device.
+ * 16-bit logits without penalties and biases. Every wait ends within a second.
+ * Where a position's logits have not arrived on an SM by then (a fault of the machine), its argmax is -1 (maybe that of the
+ * position before it too), its probs are all NaN, and its out is NaN at least where that SM's tokens are; so may be the
+ * sequence's positions behind it. No handle, no workspace; launched on
+ * the current device.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 dflash_status dflash_logits_adjust(const void *logits, int64_t seq_stride, int64_t row_stride, int32_t batch, int32_t rows,
                                    int64_t vocab, int32_t dtype, const dflash_logits_rules *rules, const int32_t *draft,
                                    int64_t draft_stride, const int32_t *mask, int64_t mask_seq_stride,
                                    int64_t mask_row_stride, void *out, int64_t out_seq_stride, int64_t out_row_stride,
                                    float *probs, int32_t *argmax, void *stream);
+
+/* Self-test of that: dflash_logits_adjust on packed logits, but copies of the logits do not come for one CTA, `rank` of the
+ * first cluster, from the cluster's position `at` on (a cluster takes positions of the first sequence; without such a CTA or
+ * position, or for rows that threads bring, nothing is lost). Takes some seconds. Errors: as above. */
+dflash_status dflash_selftest_logits_lost(const void *logits, int32_t batch, int32_t rows, int64_t vocab, int32_t dtype,
+                                          const dflash_logits_rules *rules, void *out, float *probs, int32_t *argmax,
+                                          int32_t rank, int32_t at, void *stream);
 
 #ifdef __cplusplus
 }

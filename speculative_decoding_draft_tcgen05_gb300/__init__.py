@@ -530,4 +530,5 @@ from .paged import (DFLASH_BF16, DFLASH_E4M3, DFLASH_FP16, PagedAttention, Paged
                     dflash_paged_init, dflash_paged_sync_status, dflash_qk_norm_rope)
 from .step import (DFLASH_FP32, Linear, LogitsRules, PagePool, dflash_linear_config,  # noqa: E402,F401
                    dflash_linear_destroy, dflash_linear_init, dflash_linear_run, dflash_linear_sync_status,
-                   dflash_logits_adjust, dflash_logits_rules, dflash_page_pool, dflash_pages_extend, dflash_pages_trim)
+                   dflash_logits_adjust, dflash_logits_rules, dflash_page_pool, dflash_pages_extend, dflash_pages_trim,
+                   dflash_selftest_logits_lost)

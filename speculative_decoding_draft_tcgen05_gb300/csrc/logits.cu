@@ -60,6 +60,7 @@ struct LogitsParams {
     const int32_t *mask;
     int64_t mask_seq_stride, mask_row_stride;
     int counted, biased;             // there are tokens (or drafts) that penalties count; there are biases
+    int lost_rank, lost_at;          // a CTA of the first cluster whose copies do not come, from which of its positions on; -1: none
 };
 
 struct alignas(16) Best {
@@ -414,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>((mine * kStep - max(0, end - vocab)) * sizeof(T)));
                 }
                 __syncwarp();
-                for (int i = lane; i < mine; i += 32) {
+                const bool lost = rank == p.lost_rank && blockIdx.x == 0 && t - t0 == p.lost_at;
+                for (int i = lane; i < mine && !lost; i += 32) {
                     const int v = token_of(i * kStep);
                     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                      smem_u32(logits + i * kStep)),
@@ -528,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     // With the best token alone wanted, a position's exchange passes beside the next one's pass, and who has it knows it: the
     // last one's goes to rank 0 alone.
     const bool lazy = exchange && !p.out && !p.probs;
-    bool arrived = true;  // (what does not arrive in a second: NaN and -1)
+    // What does not arrive in a second is given up. A CTA without its logits sends nothing more, so that the cluster's others
+    // give up too where they need what it would have sent.
+    bool arrived = true;
+    int left = t1;  // the positions from here on have been given up
     // All warps' results of position t, joined.
     auto collect = [&](int t, bool read) {
         if (C > 1) arrived = mbar_wait(smem_u32(&s.came[t & 1]), static_cast<uint32_t>((t - t0) >> 1) & 1u, &s.abort_flag) && arrived;
@@ -563,7 +568,14 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                              : "memory");
             }
         }
-        __syncthreads();  // the list, the mask (and logits that threads have brought) are complete
+        // the list, the mask (and logits that threads have brought) are complete
+        if (__syncthreads_or(!arrived)) {
+            // (what has been started lands before the CTA can end)
+            if (kVec && tid == 0) mbar_wait(smem_u32(&s.full), static_cast<uint32_t>(t - t0) & 1u, &s.abort_flag, false);
+            __syncthreads();
+            left = lazy && t > t0 ? t - 1 : t;
+            break;
+        }
         Best q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
         const int marked = tables ? s.n : 0;
         // all tokens but those on the list
@@ -686,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         const float base = q.m == -INFINITY ? 0.f : q.m;
         // (nothing above -inf: zeros. A sum that is no number makes all of them such.)
         const float inv = !arrived ? __int_as_float(0x7FFFFFFF) : q.m == -INFINITY && q.s == 0.f ? 0.f : 1.f / q.s;
+        const float other = arrived ? 0.f : __int_as_float(0x7FFFFFFF);  // of a token that is not the best, with tau = 0
         if (probs) {
             less = make_float2(-base, -base);
             const float2 inv2 = make_float2(inv, inv);
@@ -694,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                 if (greedy) {
 #pragma unroll
                     for (int j = 0; j < kPer / 2; ++j) {
-                        x[j].x = v + (kVec ? 2 * j : 64 * j) == id ? 1.f : 0.f;
-                        x[j].y = v + (kVec ? 2 * j + 1 : 64 * j + 32) == id ? 1.f : 0.f;
+                        x[j].x = v + (kVec ? 2 * j : 64 * j) == id ? 1.f : other;
+                        x[j].y = v + (kVec ? 2 * j + 1 : 64 * j + 32) == id ? 1.f : other;
                     }
                 } else {
                     exponentials(x, less, scale2);
@@ -710,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
             __syncthreads();
             marked_tokens([&](float x, int v) {
                 if (out) out[v] = from_f<T>(x);
-                if (probs) probs[v] = greedy ? (v == id ? 1.f : 0.f) : exp2_fast((x - base) * scale) * inv;
+                if (probs) probs[v] = greedy ? (v == id ? 1.f : other) : exp2_fast((x - base) * scale) * inv;
             });
         }
         if (more) {
@@ -735,11 +748,28 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
             }
         }
     }
+    const bool together = p.group > 1 && C > 1 && !lazy;  // (see below)
+    if (left < t1) {
+        const float none = __int_as_float(0x7FFFFFFF);
+        for (int t = left; t < t1; ++t) {
+            T *const out = p.out ? static_cast<T *>(p.out) + b * p.out_seq_stride + t * p.out_row_stride : nullptr;
+            float *const probs = p.probs ? p.probs + (static_cast<int64_t>(b) * p.rows + t) * p.vocab : nullptr;
+            for (int at = tid; at < mine * kStep; at += kThreads) {
+                const int v = token_of(at);
+                if (v < vocab && out) out[v] = from_f<T>(none);
+                if (v < vocab && probs) probs[v] = none;
+            }
+            if (p.argmax && rank == 0 && tid == 0) p.argmax[static_cast<int64_t>(b) * p.rows + t] = -1;
+        }
+        __syncwarp();
+        if (exchange && !together) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    } else if (lazy && rank == 0) {
+        store_best(t1 - 1, collect(t1 - 1, warp == 0));
+    }
     // no CTA ends while another may still send to it
-    if (lazy && rank == 0) store_best(t1 - 1, collect(t1 - 1, warp == 0));
     // (a cluster that ends together leaves room for one of the next call's on as many SMs: with several positions each, 32
     // sequences of 8 took 115 us otherwise, against 104; with one position each it costs 2 %)
-    if (p.group > 1 && C > 1 && !lazy) cluster_sync_all();
+    if (together) cluster_sync_all();
     else if (exchange) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -810,12 +840,11 @@ cudaError_t machine(int *sms, int *smem)
 
 using dfl::logits_fail;
 
-extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_stride, int64_t row_stride, int32_t batch,
-                                              int32_t rows, int64_t vocab, int32_t dtype, const dflash_logits_rules *rules,
-                                              const int32_t *draft, int64_t draft_stride, const int32_t *mask,
-                                              int64_t mask_seq_stride, int64_t mask_row_stride, void *out,
-                                              int64_t out_seq_stride, int64_t out_row_stride, float *probs, int32_t *argmax,
-                                              void *stream)
+static dflash_status adjust(const void *logits, int64_t seq_stride, int64_t row_stride, int32_t batch, int32_t rows, int64_t vocab,
+                            int32_t dtype, const dflash_logits_rules *rules, const int32_t *draft, int64_t draft_stride,
+                            const int32_t *mask, int64_t mask_seq_stride, int64_t mask_row_stride, void *out,
+                            int64_t out_seq_stride, int64_t out_row_stride, float *probs, int32_t *argmax, int32_t lost_rank,
+                            int32_t lost_at, void *stream)
 {
     if (dtype != DFLASH_BF16 && dtype != DFLASH_FP16 && dtype != DFLASH_FP32)
         return logits_fail(DFLASH_ERR_UNSUPPORTED, "dtype must be BF16, FP16 or FP32 (got %lld)", dtype);
@@ -885,6 +914,8 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
     p.mask_row_stride = mask_row_stride;
     p.counted = (p.r.repetition || p.r.presence || p.r.frequency) && (p.r.tokens || p.draft);
     p.biased = p.r.bias_count > 0;
+    p.lost_rank = lost_rank;
+    p.lost_at = lost_at;
     // CTAs per cluster: enough that the tables leave room for some CTAs an SM and, with few positions, that all SMs have
     // work of at least a piece
     const int64_t positions = static_cast<int64_t>(batch) * rows;
@@ -927,4 +958,24 @@ extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_st
         return logits_fail(DFLASH_ERR_CUDA, "the launch failed (error %lld)", e);
     }
     return DFLASH_OK;
+}
+
+extern "C" dflash_status dflash_logits_adjust(const void *logits, int64_t seq_stride, int64_t row_stride, int32_t batch,
+                                              int32_t rows, int64_t vocab, int32_t dtype, const dflash_logits_rules *rules,
+                                              const int32_t *draft, int64_t draft_stride, const int32_t *mask,
+                                              int64_t mask_seq_stride, int64_t mask_row_stride, void *out,
+                                              int64_t out_seq_stride, int64_t out_row_stride, float *probs, int32_t *argmax,
+                                              void *stream)
+{
+    return adjust(logits, seq_stride, row_stride, batch, rows, vocab, dtype, rules, draft, draft_stride, mask, mask_seq_stride,
+                  mask_row_stride, out, out_seq_stride, out_row_stride, probs, argmax, -1, -1, stream);
+}
+
+extern "C" dflash_status dflash_selftest_logits_lost(const void *logits, int32_t batch, int32_t rows, int64_t vocab, int32_t dtype,
+                                                     const dflash_logits_rules *rules, void *out, float *probs, int32_t *argmax,
+                                                     int32_t rank, int32_t at, void *stream)
+{
+    if (rank < 0 || at < 0) return logits_fail(DFLASH_ERR_INVALID_ARG, "rank and position must be >= 0 (got %lld, %lld)", rank, at);
+    return adjust(logits, rows * vocab, vocab, batch, rows, vocab, dtype, rules, nullptr, 0, nullptr, 0, 0, out, rows * vocab, vocab,
+                  probs, argmax, rank, at, stream);
 }

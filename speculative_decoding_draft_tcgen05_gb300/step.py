@@ -44,7 +44,9 @@ def declare(L):
     L.dflash_linear_init.argtypes = [ctypes.POINTER(dflash_linear_config), P, P, P, ctypes.POINTER(P)]
     L.dflash_linear_sync_status.argtypes = [P, P]
     L.dflash_linear_destroy.argtypes = [P]
-    for f in ("dflash_linear_init", "dflash_linear_sync_status", "dflash_linear_destroy"):
+    I32 = ctypes.c_int32
+    L.dflash_selftest_logits_lost.argtypes = [P, I32, I32, ctypes.c_int64, I32, ctypes.POINTER(dflash_logits_rules), P, P, P, I32, I32, P]
+    for f in ("dflash_linear_init", "dflash_linear_sync_status", "dflash_linear_destroy", "dflash_selftest_logits_lost"):
         getattr(L, f).restype = ctypes.c_int
 
 
@@ -211,6 +213,18 @@ def dflash_logits_adjust(logits, rules=None, *, out=None, probs=None, argmax=Non
     st = (_calls or _load_calls()).logits(logits, rules, out, probs, argmax, draft, mask, stream)
     if st:
         _binding()[1](st, "dflash_logits_adjust")
+
+
+def dflash_selftest_logits_lost(logits, rules=None, *, out=None, probs=None, argmax=None, rank, at, stream=None):
+    """Self-test of the waits of dflash_logits_adjust: the logits of one CTA do not arrive from its position `at` on."""
+    L, check, get_stream = _binding()
+    dev = _one_device(logits=logits, out=out, probs=probs, argmax=argmax)
+    if dev != _torch().cuda.current_device() or any(t is not None and not t.is_contiguous() for t in (logits, out, probs, argmax)):
+        raise ValueError("tensors must be contiguous and on the current device")
+    code = {_torch().bfloat16: DFLASH_BF16, _torch().float16: DFLASH_FP16, _torch().float32: DFLASH_FP32}.get(logits.dtype, -1)
+    at_of = [None if t is None else t.data_ptr() for t in (out, probs, argmax)]
+    check(L.dflash_selftest_logits_lost(logits.data_ptr(), *logits.shape, code, None if rules is None else ctypes.byref(rules.c),
+                                        *at_of, rank, at, get_stream(stream)), "dflash_selftest_logits_lost")
 
 
 # ------------------------------------------------------------ pages

@@ -1,0 +1,68 @@
+"""The operators around a step's attention where calls meet: logits that do not
+arrive, outputs that lie in one buffer with inputs, two calls at once, changing
+row counts, long sums."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32, INT32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from speculative_decoding_draft_tcgen05_gb300 import build
+    build.build()
+    import speculative_decoding_draft_tcgen05_gb300 as p
+    p.lib()
+    return p
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ------------------------------------------------------------ logits that do not arrive
+@pytest.mark.parametrize("want,rank,at", [("argmax", 5, 2), ("argmax", 0, 1), ("argmax", 3, 0), ("probs", 5, 0), ("probs", 5, 2),
+                                          ("greedy", 5, 1), ("out", 5, 1), ("all", 2, 3)])
+def test_logits_that_do_not_arrive(pkg, want, rank, at):
+    """A cluster of 16 CTAs has several positions of a sequence; the logits of one CTA do not come from position `at` on. No
+    position is answered from what the other CTAs have, and no other sequence is touched."""
+    B, T, V = 32, 8, 151936
+    logits = torch.randn(B, T, V, device="cuda", generator=gen(1)).to(BF16)
+    tokens = torch.randint(0, V, (B, 40), device="cuda", generator=gen(2), dtype=INT32)
+    tau = torch.zeros(B, device="cuda") if want == "greedy" else torch.ones(B, device="cuda")
+    rules = pkg.LogitsRules(tokens, torch.full((B,), 40, device="cuda", dtype=INT32), presence=torch.ones(B, device="cuda"), temperature=tau)
+
+    def outputs():
+        return dict(out=torch.zeros_like(logits) if want in ("out", "all") else None,
+                    probs=torch.zeros(B, T, V, device="cuda") if want in ("probs", "greedy", "all") else None,
+                    argmax=torch.zeros(B, T, device="cuda", dtype=INT32) if want in ("argmax", "all") else None)
+    good, bad = outputs(), outputs()
+    pkg.dflash_logits_adjust(logits, rules, **good)
+    pkg.dflash_selftest_logits_lost(logits, rules, rank=rank, at=at, **bad)
+    own = torch.arange(V, device="cuda") // 2048 % 16 == rank
+    for name, y in good.items():
+        if y is None:
+            continue
+        x = bad[name]
+        assert torch.equal(x[1:], y[1:])
+        for t in range(at - 1 if name == "argmax" else at):
+            assert torch.equal(x[0, t], y[0, t])
+        if name == "argmax":
+            assert int(x[0, at]) == -1
+            assert at == 0 or int(x[0, at - 1]) in (-1, int(y[0, at - 1]))
+        elif name == "probs":
+            assert torch.isnan(x[0, at]).all()
+        else:
+            assert torch.isnan(x[0, at, own]).all()
+            assert torch.equal(x[0, at, ~own], y[0, at, ~own]) or torch.isnan(x[0, at]).all()
+        for t in range(at + 1, T):  # given up too, or another cluster's
+            if name == "argmax":
+                assert int(x[0, t]) in (-1, int(y[0, t]))
+            else:
+                assert torch.isnan(x[0, t, own]).all() or torch.equal(x[0, t], y[0, t])
+    pkg.dflash_logits_adjust(logits, rules, **bad)  # the next call is whole again
+    assert all(y is None or torch.equal(bad[name], y) for name, y in good.items())
