@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
                 if (e < kMaxList) mk.put(e, at, p.counted ? mk.occurrence(at) : 0u);
             }
     }
+    __syncwarp();
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
     const bool greedy = tau == 0.f;
@@ -536,7 +537,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     int left = t1;  // the positions from here on have been given up
     // All warps' results of position t, joined.
     auto collect = [&](int t, bool read) {
-        if (C > 1) arrived = mbar_wait(smem_u32(&s.came[t & 1]), static_cast<uint32_t>((t - t0) >> 1) & 1u, &s.abort_flag) && arrived;
+        if (C > 1) {  // (who reads what other CTAs sent acquires it at cluster scope)
+            const uint32_t bar = smem_u32(&s.came[t & 1]), parity = static_cast<uint32_t>((t - t0) >> 1) & 1u;
+            arrived = (read ? mbar_wait_cluster(bar, parity, &s.abort_flag) : mbar_wait(bar, parity, &s.abort_flag)) && arrived;
+        }
         __syncwarp();
         Best q = {-INFINITY, 0.f, -INFINITY, 0x7FFFFFFF};
         if (!read) return q;
@@ -767,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         store_best(t1 - 1, collect(t1 - 1, warp == 0));
     }
     // no CTA ends while another may still send to it
+    __syncwarp();
     // (a cluster that ends together leaves room for one of the next call's on as many SMs: with several positions each, 32
     // sequences of 8 took 115 us otherwise, against 104; with one position each it costs 2 %)
     if (together) cluster_sync_all();
