@@ -57,7 +57,8 @@ typedef struct {
  *   draft  [batch, rows - 1] int32, rows draft_stride apart (NULL with rows = 1, or: no drafts are counted)
  *   mask   int32 words, bit v % 32 of word v / 32 set where token v is allowed: words of position t of sequence b at
  *          mask + b * mask_seq_stride + t * mask_row_stride (a stride of 0 shares them)
- * Outputs overlap nothing else. 0 <= batch, rows (0 launches nothing), batch * rows < 2^31; vocab >= 1, and what 16
+ * Outputs overlap nothing else, or the call is refused; rows of out may pass those of the logits where strides are equal
+ * (slices of one buffer). 0 <= batch, rows (0 launches nothing), batch * rows < 2^31; vocab >= 1, and what 16
  * CTAs' shared memory holds of it (UNSUPPORTED above): 262,144 tokens with up to 8192 biases, a million and more of
  * 16-bit logits without penalties and biases. Every wait ends within a second.
  * Where a position's logits have not arrived on an SM by then (a fault of the machine), its argmax is -1 (maybe that of the

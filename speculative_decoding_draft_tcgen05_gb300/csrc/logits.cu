@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "dflash_logits.h"
 #include "kernels.h"
+#include "spans.h"
 
 namespace dfl {
 
@@ -790,18 +791,6 @@ bool misaligned(const void *p, uintptr_t by)
     return reinterpret_cast<uintptr_t>(p) % by != 0;
 }
 
-// Bytes of a tensor from its first to its last value.
-struct Span {
-    const void *from;
-    int64_t bytes;
-
-    bool meets(const Span &o) const
-    {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(from), b = reinterpret_cast<uintptr_t>(o.from);
-        return from && o.from && a < b + static_cast<uintptr_t>(o.bytes) && b < a + static_cast<uintptr_t>(bytes);
-    }
-};
-
 using Kernel = void (*)(LogitsParams);
 
 Kernel kernel_of(int dtype, bool vec)
@@ -870,14 +859,6 @@ static dflash_status adjust(const void *logits, int64_t seq_stride, int64_t row_
         return logits_fail(DFLASH_ERR_INVALID_ARG, "strides must not be negative, those of out at least vocab");
     if (out == logits && (seq_stride != out_seq_stride || row_stride != out_row_stride))
         return logits_fail(DFLASH_ERR_INVALID_ARG, "out can be the logits only with their strides");
-    // (the logits and out may be slices of one buffer, whose rows pass one another; the others are packed)
-    const int64_t count = static_cast<int64_t>(batch) * rows;
-    const dfl::Span x_span = {logits, ((batch - 1) * seq_stride + (rows - 1) * row_stride + vocab) * size},
-                    out_span = {out, ((batch - 1) * out_seq_stride + (rows - 1) * out_row_stride + vocab) * size},
-                    probs_span = {probs, count * vocab * 4}, argmax_span = {argmax, count * 4};
-    if (probs_span.meets(x_span) || probs_span.meets(out_span) || argmax_span.meets(x_span) || argmax_span.meets(out_span) ||
-        argmax_span.meets(probs_span) || (out != logits && count == 1 && out_span.meets(x_span)))
-        return logits_fail(DFLASH_ERR_INVALID_ARG, "outputs must not overlap the logits or one another (but out may be the logits)");
     static const dflash_logits_rules none = {};
     dfl::LogitsParams p = {};
     p.r = rules ? *rules : none;
@@ -894,6 +875,28 @@ static dflash_status adjust(const void *logits, int64_t seq_stride, int64_t row_
                           static_cast<const void *>(p.r.temperature), static_cast<const void *>(p.r.bias_ids),
                           static_cast<const void *>(p.r.bias_values)})
         if (dfl::misaligned(q, 4)) return logits_fail(DFLASH_ERR_INVALID_ARG, "the rules' arrays must be aligned to their type");
+    // (the logits and out may be slices of one buffer, whose rows pass one another)
+    const int64_t count = static_cast<int64_t>(batch) * rows, vector = static_cast<int64_t>(batch) * 4;
+    const dfl::Rows outputs[] = {{out, vocab * size, rows, out_row_stride * size, batch, out_seq_stride * size},
+                                 {probs, count * vocab * 4},
+                                 {argmax, count * 4}};
+    const dfl::Rows inputs[] = {{logits, vocab * size, rows, row_stride * size, batch, seq_stride * size},
+                                {draft, (rows - 1) * int64_t(4), batch, draft_stride * 4},
+                                {mask, (vocab + 31) / 32 * 4, rows, mask_row_stride * 4, batch, mask_seq_stride * 4},
+                                {p.r.tokens, p.r.token_cols * int64_t(4), batch, p.r.token_stride * 4},
+                                {p.r.bias_ids, p.r.bias_count * int64_t(4), batch, p.r.bias_stride * 4},
+                                {p.r.bias_values, p.r.bias_count * int64_t(4), batch, p.r.bias_stride * 4},
+                                {p.r.lens, vector},
+                                {p.r.prompt_lens, vector},
+                                {p.r.repetition, vector},
+                                {p.r.presence, vector},
+                                {p.r.frequency, vector},
+                                {p.r.temperature, vector}};
+    bool overlap = dfl::folds(outputs[0]) || dfl::meet(outputs[0], outputs[1]) || dfl::meet(outputs[0], outputs[2]) ||
+                   dfl::meet(outputs[1], outputs[2]);
+    for (const dfl::Rows &o : outputs)
+        for (const dfl::Rows &i : inputs) overlap = overlap || ((o.at != i.at || &o != outputs || &i != inputs) && dfl::meet(o, i));
+    if (overlap) return logits_fail(DFLASH_ERR_INVALID_ARG, "outputs must not overlap inputs or one another (but out may be the logits)");
     int sms = 0, smem_most = 0;
     cudaError_t e = dfl::machine(&sms, &smem_most);
     if (e != cudaSuccess) {

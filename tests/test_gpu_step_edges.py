@@ -66,3 +66,30 @@ def test_logits_that_do_not_arrive(pkg, want, rank, at):
                 assert torch.isnan(x[0, t, own]).all() or torch.equal(x[0, t], y[0, t])
     pkg.dflash_logits_adjust(logits, rules, **bad)  # the next call is whole again
     assert all(y is None or torch.equal(bad[name], y) for name, y in good.items())
+
+
+# ------------------------------------------------------------ logits and outputs in one buffer
+@pytest.mark.parametrize("V", [512, 515])
+def test_logits_into_other_slices_of_their_buffer(pkg, V):
+    """Rows that pass one another are answered, rows that share values are refused."""
+    B, T = 3, 4
+    mask = torch.randint(-2 ** 31, 2 ** 31, (B, T, -(-V // 32)), device="cuda", generator=gen(3)).to(INT32)
+
+    def buffer(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen(4)).to(BF16)
+    for x, y in ((b := buffer(B, T, 2, V), b[:, :, 0], b[:, :, 1])[1:], (b := buffer(B, 2 * T, V), b[:, T:], b[:, :T])[1:],
+                 (b := buffer(2 * B, T, V), b[B:], b[:B])[1:], (b := buffer(B, T, 2 * V + 5), b[..., 1:V + 1], b[..., V + 1:2 * V + 1])[1:],
+                 (b := buffer(2 * B, 2 * T, V), b[::2, ::2], b[1::2, 1::2])[1:],
+                 (buffer(B, T, V), buffer(T, B, V).transpose(0, 1))):
+        want = torch.empty(B, T, V, device="cuda", dtype=BF16)
+        pkg.dflash_logits_adjust(x.contiguous(), out=want, mask=mask)
+        before = x.clone()
+        pkg.dflash_logits_adjust(x, out=y, mask=mask)
+        assert torch.equal(y, want) and torch.equal(x, before)
+    b = buffer(B + 1, T + 1, V + 8)
+    for x, y in ((b[:B, :T, :V], b[1:, :T, :V]), (b[:B, :T, :V], b[:B, 1:, :V]), (b[:B, 1:, :V], b[1:, :T, :V]), (b[:B, :T, :V], b[:B, :T, 8:]),
+                 (b[:1, :T, :V], b[:1, 1:, :V])):
+        before = b.clone()
+        with pytest.raises(pkg.DflashError, match="overlap"):
+            pkg.dflash_logits_adjust(x, out=y)
+        assert torch.equal(b, before)
