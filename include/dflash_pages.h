@@ -60,7 +60,8 @@ typedef struct {
  *   granted    [batch] 1, or 0 for a refused entry
  * Rows of positions and slots from cu_tokens[batch] on are left as they were.
  * With rows = NULL, lens and page_table may be the pool's own (the same
- * address; page_table with the same stride); no output overlaps anything else.
+ * address; page_table with the same stride), and new_tokens may be the pool's
+ * lens; nothing else overlaps, or the call is refused.
  * 0 <= batch <= 65536, batch <= requests; 0 <= tokens <= 2^30. Errors: INVALID_ARG, CUDA. */
 dflash_status dflash_pages_extend(const dflash_page_pool *pool, const int32_t *rows, const int32_t *new_tokens,
                                   int32_t batch, int32_t tokens, int32_t *cu_tokens, int32_t *lens, int32_t *page_table,
@@ -74,7 +75,9 @@ dflash_status dflash_pages_extend(const dflash_page_pool *pool, const int32_t *r
  *                           dflash_verify_prefix drop a block's rejected drafts;
  *   everything              with counts = NULL (a request that has ended).
  * Pages that it no longer needs return to the stack, so that an extension that
- * takes them back takes them in the same order. 0 <= batch <= 65536, batch <= requests.
+ * takes them back takes them in the same order. With rows = NULL, counts may
+ * be the pool's lens; nothing else overlaps, or the call is refused.
+ * 0 <= batch <= 65536, batch <= requests.
  * Errors: INVALID_ARG, CUDA. */
 dflash_status dflash_pages_trim(const dflash_page_pool *pool, const int32_t *rows, const int32_t *counts, int32_t base,
                                 int32_t batch, void *stream);

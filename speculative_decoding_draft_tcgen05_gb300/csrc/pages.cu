@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "dflash_pages.h"
 #include "kernels.h"
+#include "spans.h"
 
 namespace dfl {
 
@@ -381,6 +382,29 @@ dflash_status check_pool(const dflash_page_pool *q, int32_t batch, const void *r
     return DFLASH_OK;
 }
 
+// The pool's arrays, the inputs and the n outputs share nothing; but counts may be the pool's lengths without rows, when an
+// entry's number is its own request's length, which is written when every block has read it.
+dflash_status check_overlap(const dflash_page_pool &q, const int32_t *rows, const int32_t *counts, int32_t batch, const Rows *outputs, int n)
+{
+    const Rows pool[] = {{q.lens, q.requests * int64_t(4)},
+                         {q.page_table, q.cols * int64_t(4), q.requests, q.table_stride * 4},
+                         {q.free_pages, q.num_pages * int64_t(4)},
+                         {q.counters, 8}};
+    const Rows inputs[] = {{rows, batch * int64_t(4)}, {rows || counts != q.lens ? counts : nullptr, batch * int64_t(4)}};
+    bool overlap = false;
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j) overlap = overlap || meet(pool[i], pool[j]);
+        for (const Rows &in : inputs) overlap = overlap || meet(pool[i], in);
+    }
+    for (int i = 0; i < n; ++i) {
+        for (int j = 0; j < i; ++j) overlap = overlap || meet(outputs[i], outputs[j]);
+        for (const Rows &in : inputs) overlap = overlap || meet(outputs[i], in);
+        for (const Rows &own : pool) overlap = overlap || meet(outputs[i], own);
+        overlap = overlap || folds(outputs[i]);
+    }
+    return overlap ? pages_fail(DFLASH_ERR_INVALID_ARG, "outputs, inputs and the pool's arrays must not overlap") : DFLASH_OK;
+}
+
 // One warp for a batch of up to 32 with little to do, else blocks of 256 or, over 256 entries, of 1024; and as many blocks
 // (up to 304) as there are times 512 things to do: 32 requests that get 8192 pages each and then end took 6.3 ms by one warp,
 // and take 15 us. Returns a block's threads.
@@ -431,6 +455,14 @@ extern "C" dflash_status dflash_pages_extend(const dflash_page_pool *pool, const
         page_table = nullptr;
     }
     if (batch == 0 && !cu_tokens) return DFLASH_OK;
+    const dfl::Rows outputs[] = {{cu_tokens, (batch + 1) * int64_t(4)},
+                                 {lens, batch * int64_t(4)},
+                                 {page_table, table_cols * int64_t(4), batch, table_stride * 4},
+                                 {positions, tokens * int64_t(4)},
+                                 {slots, tokens * int64_t(8)},
+                                 {granted, batch * int64_t(4)}};
+    st = dfl::check_overlap(*pool, rows, new_tokens, batch, outputs, 6);
+    if (st != DFLASH_OK) return st;
     dfl::PagesParams p;
     p.pool = *pool;
     p.room = room;
@@ -468,6 +500,8 @@ extern "C" dflash_status dflash_pages_trim(const dflash_page_pool *pool, const i
     dflash_status st = dfl::check_pool(pool, batch, rows, counts);
     if (st != DFLASH_OK) return st;
     if (batch == 0) return DFLASH_OK;
+    st = dfl::check_overlap(*pool, rows, counts, batch, nullptr, 0);
+    if (st != DFLASH_OK) return st;
     dfl::PagesParams p = {};
     p.pool = *pool;
     p.rows = rows;

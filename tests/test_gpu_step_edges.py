@@ -93,3 +93,36 @@ def test_logits_into_other_slices_of_their_buffer(pkg, V):
         with pytest.raises(pkg.DflashError, match="overlap"):
             pkg.dflash_logits_adjust(x, out=y)
         assert torch.equal(b, before)
+
+
+# ------------------------------------------------------------ pages and their pool
+@pytest.mark.parametrize("B", [3, 300, 3000])
+def test_counts_that_are_the_pools_lengths(pkg, B):
+    """An entry's number may be its own request's length: as many tokens again, then all of them dropped."""
+    pool = pkg.PagePool.empty(requests=B, cols=6, num_pages=6 * B, page_size=4)
+    start = torch.randint(0, 12, (B,), device="cuda", generator=gen(B), dtype=INT32)
+    pool.extend(None, start)
+    pool.extend(None, pool.lens)
+    assert torch.equal(pool.lens, 2 * start)
+    assert pool.counters.tolist() == [6 * B - int(((2 * start + 3) // 4).sum()), 0]
+    pool.trim(pool.lens)
+    assert not pool.lens.any() and sorted(pool.free_pages.tolist()) == list(range(6 * B))
+    with pytest.raises(pkg.DflashError, match="overlap"):
+        pool.trim(pool.lens, rows=torch.arange(B, device="cuda", dtype=INT32))
+    batch = pkg.PagedBatch(torch.zeros(B, device="cuda", dtype=INT32), pool.lens[1:], torch.zeros(B - 1, 6, device="cuda", dtype=INT32), max_tokens=4)
+    with pytest.raises(pkg.DflashError, match="overlap"):
+        pool.extend(batch, start[1:].clone())
+    assert not pool.lens.any()
+
+
+def test_a_batch_in_the_columns_beside_the_pools(pkg):
+    """The batch's page table may lie in the same rows of a buffer as the pool's."""
+    wide = torch.full((4, 20), -1, device="cuda", dtype=INT32)
+    empty = pkg.PagePool.empty(requests=4, cols=8, num_pages=32, page_size=16)
+    pool = pkg.PagePool(wide[:, :8], empty.lens, empty.free_pages, empty.counters, page_size=16)
+    batch = pkg.PagedBatch(torch.zeros(5, device="cuda", dtype=INT32), torch.zeros(4, device="cuda", dtype=INT32), wide[:, 8:16], max_tokens=100)
+    pool.extend(batch, torch.tensor([100, 0, 17, 1], device="cuda", dtype=INT32))
+    assert wide[0].tolist() == [0, 1, 2, 3, 4, 5, 6, -1, 0, 1, 2, 3, 4, 5, 6, -1, -1, -1, -1, -1]
+    assert wide[2, :3].tolist() == [7, 8, -1] and wide[2, 8:11].tolist() == [7, 8, -1] and (wide[1] == -1).all()
+    with pytest.raises(pkg.DflashError, match="overlap"):
+        pool.extend(pkg.PagedBatch(batch.tensors[0], batch.tensors[1], wide[:, 7:15], max_tokens=1), torch.ones(4, device="cuda", dtype=INT32))

@@ -103,3 +103,47 @@ def test_logits_refuse_outputs_over_inputs(lib, which, output):
         setattr(r, which, at[output])
     refused(lib, L.dflash_logits_adjust(4096, 128, 64, 2, 2, 64, 0, ctypes.addressof(r), draft, 1, mask, 4, 2, given.get("out"), 128, 64,
                                         given.get("probs"), given.get("argmax"), None))
+
+
+# A pool of 4 requests and 8 columns, everything 4096 bytes apart.
+POOL = dict(page_table=1 << 16, table_stride=10, lens=(1 << 16) + 4096, free_pages=(1 << 16) + 8192, counters=(1 << 16) + 12288,
+            requests=4, cols=8, page_size=16, num_pages=32)
+OUT = dict(cu=1 << 20, lens=(1 << 20) + 4096, table=(1 << 20) + 8192, positions=(1 << 20) + 12288, slots=(1 << 20) + 16384,
+           granted=(1 << 20) + 20480)
+
+
+def extend(lib, rows=None, new=1 << 19, stride=8, pool={}, **out):
+    o = {**dict.fromkeys(OUT), **out}
+    q = lib[0].dflash_page_pool(**{**POOL, **pool})
+    return lib[1].dflash_pages_extend(ctypes.addressof(q), rows, new, 3, 8, o["cu"], o["lens"], o["table"], stride, 8, o["positions"],
+                                      o["slots"], o["granted"], None)
+
+
+@pytest.mark.parametrize("name", OUT)
+def test_pages_refuse_outputs_over_the_pool_inputs_and_one_another(lib, name):
+    last = dict(cu=12, lens=8, table=8 * 4 * 2 + 28, positions=28, slots=56, granted=8)[name]
+    for base, size in ((POOL["lens"], 16), (POOL["page_table"], 10 * 4 * 3 + 32), (POOL["free_pages"], 128), (POOL["counters"], 8), (1 << 19, 12)):
+        ends = (base - last // 8 * 8, base + (size - 4) // 8 * 8)
+        for at in (*ends, base) if (base, name) not in ((POOL["lens"], "lens"), (POOL["page_table"], "table")) else ends:
+            refused(lib, extend(lib, **{name: at}))
+    for other in OUT:
+        if other != name:
+            refused(lib, extend(lib, **{**OUT, name: OUT[other]}))
+
+
+def test_pages_refuse_inputs_over_the_pool(lib):
+    for base in (POOL["lens"], POOL["page_table"], POOL["free_pages"], POOL["counters"]):
+        refused(lib, extend(lib, rows=base))
+        refused(lib, extend(lib, new=base + 4))
+        q = lib[0].dflash_page_pool(**POOL)
+        for rows, counts in ((base, None), (1 << 19, base), (None, base + 4)):
+            refused(lib, lib[1].dflash_pages_trim(ctypes.addressof(q), rows, counts, -1, 3, None))
+    refused(lib, extend(lib, rows=1 << 18, new=POOL["lens"]))
+    refused(lib, extend(lib, pool=dict(lens=POOL["free_pages"] + 124)))
+    refused(lib, extend(lib, pool=dict(counters=POOL["page_table"] + 32 + 40 * 3 - 4)))
+
+
+def test_pages_refuse_a_view_of_the_pools_lengths_or_table_from_another_place(lib):
+    refused(lib, extend(lib, lens=POOL["lens"] + 4))
+    refused(lib, extend(lib, table=POOL["page_table"] + 40, stride=10))
+    refused(lib, extend(lib, table=POOL["page_table"] + 4, stride=10))
