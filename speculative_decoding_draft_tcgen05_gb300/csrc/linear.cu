@@ -63,6 +63,7 @@ constexpr int kThreads = 320;  // TMA, products, 8 epilogue warps
 constexpr int kLanes = 128;    // of TMEM: the most weight rows of a CTA
 constexpr int kBox = 64;       // columns of a box: 128 bytes
 constexpr int kMaxSplit = 8;
+constexpr int kPlans = 256;    // that a handle remembers
 constexpr int kMaxSum = 128;   // rows of x of a tile whose results are summed in registers
 
 struct Layout {
@@ -800,7 +801,8 @@ bool fit_stages(Plan &pl, int KB64, const Machine &m)
 
 // A plan's time in microseconds but for a constant: a fit to 3,000 plans of 35 shapes (1 to 12,000 rows, n 128 to
 // 151,936, k 512 to 16,000), by which the chosen plan is 2 % slower than the fastest on average and 12 % at most.
-double cost(const Plan &pl, int64_t rows, int64_t n, int64_t k, int KB64, int64_t items)
+// (Above `most` only some number above it, without the roots.)
+double cost(const Plan &pl, int64_t rows, int64_t n, int64_t k, int KB64, int64_t items, double most)
 {
     const int ctas = pl.pair ? 2 : 1;
     const double rounds = pl.split > 1 ? 1 : static_cast<double>((items + pl.grid - 1) / pl.grid);
@@ -810,6 +812,8 @@ double cost(const Plan &pl, int64_t rows, int64_t n, int64_t k, int KB64, int64_
     // a step: its products, which follow one another, and what the SM takes in for them, in L4
     const double mma = pl.NT * 0.001 > 0.127 ? pl.NT * 0.001 : 0.127;
     const double in = pl.F / 940.0 + xr / 615.0;
+    const double least = rounds * steps * (mma > in ? mma : in);
+    if (least > most) return least;
     const double step = sqrt(sqrt(mma * mma * mma * mma + in * in * in * in));
     const double chain = rounds * steps * step, hbm = static_cast<double>(n) * k * 2 / 9e6;
     // the epilogue of the last tile; with a short k also those that the next tile's products do not cover
@@ -824,26 +828,28 @@ Plan choose(int64_t rows, int64_t n, int64_t k, bool sum, const Machine &m)
 {
     const int KB64 = static_cast<int>((k + kBox - 1) / kBox);
     Plan best = {};
-    double best_t = 0;
+    double best_t = HUGE_VAL;
     const int widest = sum ? kMaxSum : 256;
     const int most = static_cast<int>(rows < widest ? (rows + 15) / 16 * 16 : widest);
     for (int pair = 0; pair < 2; ++pair) {
         const int ctas = pair ? 2 : 1;
         if (pair && rows <= 32) continue;
+        int64_t tiles_f[kLanes / 8 + 1];
+        for (int F = 8; F <= kLanes; F += 8) tiles_f[F / 8] = (n + F * ctas - 1) / (F * ctas);
         for (int split = 1; split * ctas <= kMaxSplit; ++split) {
             const int slots = m.clusters[pair][split * ctas];
             if (slots < 1 || split > KB64) continue;
             for (int NT = most; NT >= 16; NT -= 16) {
                 if (NT < most && rows <= 64) break;       // (more rows per weight cost nothing there)
                 if (rows > 512 && NT < 64) break;
+                const int64_t tiles_t = (rows + NT - 1) / NT;
                 for (int F = kLanes; F >= (rows <= 256 ? 16 : kLanes); F -= 8) {
                     Plan pl = {pair, F, NT, split, 1, 0, 0};
-                    const int64_t items = (n + F * ctas - 1) / (F * ctas) * ((rows + NT - 1) / NT);
+                    const int64_t items = tiles_f[F / 8] * tiles_t;
                     if (split > 1 && items > slots) break;
-                    if (!fit_stages(pl, KB64, m)) continue;
                     pl.grid = static_cast<int>(items < slots ? items : slots);
-                    const double t = cost(pl, rows, n, k, KB64, items);
-                    if (best_t == 0 || t < best_t) best = pl, best_t = t;
+                    const double t = cost(pl, rows, n, k, KB64, items, best_t);
+                    if (t < best_t && fit_stages(pl, KB64, m)) best = pl, best_t = t;
                 }
             }
         }
@@ -939,9 +945,9 @@ struct dflash_linear_ctx {
     const void *W = nullptr, *bias = nullptr;
     CUtensorMap tm_w[dfl::kLanes / 8];  // by F / 8 - 1
     int *err = nullptr;
-    // the last call's rows and plan (rows << 32 | F / 8 << 16 | NT / 16 << 8 | split << 4 | pair): a step calls its layers
-    // with the same rows again, and looking through the plans takes some microseconds
-    std::atomic<uint64_t> plan{0};
+    // plans that have been chosen, by the low bits of the rows (rows << 32 | F / 8 << 16 | NT / 16 << 8 | split << 4 | pair): a
+    // server's steps come back to their row counts, and looking through the plans takes 0.5 to 25 us
+    std::atomic<uint64_t> plans[dfl::kPlans] = {};
 };
 
 namespace dfl {
@@ -949,7 +955,8 @@ namespace {
 
 Plan plan_for(dflash_linear_ctx *h, int64_t rows)
 {
-    const uint64_t last = h->plan.load(std::memory_order_relaxed);
+    std::atomic<uint64_t> &place = h->plans[rows % kPlans];
+    const uint64_t last = place.load(std::memory_order_relaxed);
     const int64_t n = h->cfg.n, k = h->cfg.k;
     if (last >> 32 == static_cast<uint64_t>(rows)) {
         Plan pl = {static_cast<int>(last & 15), static_cast<int>(last >> 16 & 255) * 8, static_cast<int>(last >> 8 & 255) * 16,
@@ -962,9 +969,9 @@ Plan plan_for(dflash_linear_ctx *h, int64_t rows)
     }
     const Plan pl = choose(rows, n, k, h->cfg.out_dtype == DFLASH_FP32, h->m);
     if (pl.grid > 0)
-        h->plan.store(static_cast<uint64_t>(rows) << 32 | static_cast<uint64_t>(pl.F / 8) << 16 | static_cast<uint64_t>(pl.NT / 16) << 8 |
-                          static_cast<uint64_t>(pl.split) << 4 | static_cast<uint64_t>(pl.pair),
-                      std::memory_order_relaxed);
+        place.store(static_cast<uint64_t>(rows) << 32 | static_cast<uint64_t>(pl.F / 8) << 16 | static_cast<uint64_t>(pl.NT / 16) << 8 |
+                        static_cast<uint64_t>(pl.split) << 4 | static_cast<uint64_t>(pl.pair),
+                    std::memory_order_relaxed);
     return pl;
 }
 
