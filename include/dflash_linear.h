@@ -57,6 +57,10 @@ dflash_status dflash_linear_init(const dflash_linear_config *cfg, const void *W,
  * >= n and the alignment of their type; rows that start on whole 16 bytes are
  * the fast ones. residual may be y itself (same address and stride, in place);
  * y overlaps nothing else. Products accumulate in fp32 and y is rounded once.
+ * The tensor cores' sums truncate: where all products have one sign, an fp32 y
+ * is too small by up to 1.1e-6 of itself (bf16) or 3.3e-6 (fp16), with both
+ * signs it is nearer; a 16-bit y, before its rounding, by k / 512 times as much
+ * for k up to 65536 and by 3e-5 above. Calls give the same bits each time.
  * Calls with one handle may overlap on the GPU. Current device: the handle's.
  * Errors: INVALID_ARG, CUDA. */
 dflash_status dflash_linear_run(dflash_linear_handle h, const void *x, int64_t x_stride, int64_t rows,

@@ -16,9 +16,17 @@
 // accumulators in TMEM, so that a tile's epilogue runs beside the next one's
 // products.
 //
-// The tensor cores' fp32 accumulator truncates: over k = 2560 its error is
-// 2.7e-6 of the result (2-norm). Results in 16 bits do not notice; for results
-// in 32 bits the accumulator is read every 512 columns and summed in registers.
+// The tensor cores' fp32 accumulator truncates, at every 16 columns its sum and
+// what lies more than some 25 bits below it of their products. Values of one
+// sign come out too low: by 7e-7 of the result every 512 columns that one
+// accumulator takes for bf16, 2.6e-6 for fp16, whose products have more bits;
+// of values of both signs two thirds and a quarter of that are left (2-norm).
+// So results in 32 bits read the accumulator out every 512 columns and sum in
+// registers. Results in 16 bits are rounded by up to 3.9e-3 (bf16) or 4.9e-4
+// (fp16): up to 65536 columns may stay in one accumulator (off by some 3.3e-4
+// at that length for fp16 of one sign, 9e-5 for bf16). Tiles whose sums fit
+// registers are half as large (256 rows, n = 5120, k = 53248 take 103 us, 153
+// with them), so only sums longer than that are read out, every 4096.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -65,6 +73,7 @@ constexpr int kBox = 64;       // columns of a box: 128 bytes
 constexpr int kMaxSplit = 8;
 constexpr int kPlans = 256;    // that a handle remembers
 constexpr int kMaxSum = 128;   // rows of x of a tile whose results are summed in registers
+constexpr int64_t kLong = 65536;  // columns, above which results in 16 bits are summed there too
 
 struct Layout {
     uint32_t w, stage, bars, extra, total;
@@ -370,8 +379,8 @@ struct RowStore {
 
 // kPair: two CTAs compute a tile of 2 F weight rows (cta_group::2 products issued by the even CTA): each holds F weight
 // rows and half of the tile's rows of x, and has the results of its weight rows. A cluster of p.split CTAs or pairs
-// shares the stages of one tile.
-template <bool kPair, typename T, typename Y>
+// shares the stages of one tile. kSum: the accumulator is read out every p.seg stages and summed in registers.
+template <bool kPair, typename T, typename Y, bool kSum>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -559,8 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         // ---------------------------------------------------------------- epilogue: a thread has a weight row's results;
         // the two warps of a lane quadrant take turns at 32 of a tile's rows of x
         const int g = (warp - 2) >> 2, q = warp & 3, f = q * 32 + lane;
-        // results in 32 bits are summed in registers over the accumulators
-        constexpr bool kSum = std::is_same_v<Y, float>;
         constexpr int kSteps = kMaxSum / (2 * kRows);  // of a warp, at most
         float *const turn = reinterpret_cast<float *>(gbase + lay.extra + (warp - 2) * kTurn);
         const uint32_t mail = base + (p.apart ? lay.extra : 0u);  // where the parts of a split tile arrive
@@ -759,6 +766,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
 }
 
+// Results in 16 bits of up to kLong columns do not notice the accumulator's truncation (see the top).
+bool sums(const dflash_linear_config &c)
+{
+    return c.out_dtype == DFLASH_FP32 || c.k > kLong;
+}
+
 // How a call is cut: tiles of NT rows by F weight rows of a CTA, or of both CTAs of a pair, `split` of which share k.
 struct Plan {
     int pair, F, NT, split, boxes, stages, grid;  // grid: clusters
@@ -876,28 +889,28 @@ cudaLaunchConfig_t config(int teams, int size, int smem, cudaStream_t s, cudaLau
     return cfg;
 }
 
-template <typename T, typename Y>
+template <typename T, typename Y, bool kSum>
 cudaError_t launch(const Plan &pl, const LinearParams &p, cudaStream_t s)
 {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config(pl.grid, (pl.pair ? 2 : 1) * pl.split, smem_of(pl), s, attr);
-    return pl.pair ? cudaLaunchKernelEx(&cfg, linear_kernel<true, T, Y>, p) : cudaLaunchKernelEx(&cfg, linear_kernel<false, T, Y>, p);
+    return pl.pair ? cudaLaunchKernelEx(&cfg, linear_kernel<true, T, Y, kSum>, p) : cudaLaunchKernelEx(&cfg, linear_kernel<false, T, Y, kSum>, p);
 }
 
-template <typename T, typename Y>
+template <typename T, typename Y, bool kSum>
 cudaError_t prepare(Machine &m)
 {
     cudaLaunchAttribute attr[2];
-    cudaError_t e = set_max_dynamic_smem(linear_kernel<true, T, Y>, m.smem);
-    if (e == cudaSuccess) e = set_max_dynamic_smem(linear_kernel<false, T, Y>, m.smem);
+    cudaError_t e = set_max_dynamic_smem(linear_kernel<true, T, Y, kSum>, m.smem);
+    if (e == cudaSuccess) e = set_max_dynamic_smem(linear_kernel<false, T, Y, kSum>, m.smem);
     if (e != cudaSuccess) return e;
     m.clusters[0][1] = m.sms;
     for (int pair = 0; pair < 2; ++pair)
         for (int size = 2; size <= kMaxSplit; size += pair + 1) {
             const cudaLaunchConfig_t cfg = config(1, size, m.smem, nullptr, attr);
             int *const to = &m.clusters[pair][size];
-            e = pair ? cudaOccupancyMaxActiveClusters(to, linear_kernel<true, T, Y>, &cfg)
-                     : cudaOccupancyMaxActiveClusters(to, linear_kernel<false, T, Y>, &cfg);
+            e = pair ? cudaOccupancyMaxActiveClusters(to, linear_kernel<true, T, Y, kSum>, &cfg)
+                     : cudaOccupancyMaxActiveClusters(to, linear_kernel<false, T, Y, kSum>, &cfg);
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 *to = 0;  // (such a cluster is not used)
@@ -967,7 +980,7 @@ Plan plan_for(dflash_linear_ctx *h, int64_t rows)
         pl.grid = static_cast<int>(items < slots ? items : slots);
         return pl;
     }
-    const Plan pl = choose(rows, n, k, h->cfg.out_dtype == DFLASH_FP32, h->m);
+    const Plan pl = choose(rows, n, k, sums(h->cfg), h->m);
     if (pl.grid > 0)
         place.store(static_cast<uint64_t>(rows) << 32 | static_cast<uint64_t>(pl.F / 8) << 16 | static_cast<uint64_t>(pl.NT / 16) << 8 |
                         static_cast<uint64_t>(pl.split) << 4 | static_cast<uint64_t>(pl.pair),
@@ -1018,9 +1031,14 @@ extern "C" dflash_status dflash_linear_init(const dflash_linear_config *cfg, con
     }
     c->m.smem = smem;
     const bool half = cfg->dtype == DFLASH_FP16, wide = cfg->out_dtype == DFLASH_FP32;
-    cudaError_t e = half ? (wide ? dfl::prepare<__half, float>(c->m) : dfl::prepare<__half, __half>(c->m))
-                         : (wide ? dfl::prepare<__nv_bfloat16, float>(c->m)
-                                 : dfl::prepare<__nv_bfloat16, __nv_bfloat16>(c->m));
+    const bool sum = dfl::sums(*cfg);
+    using B16 = __nv_bfloat16;
+    cudaError_t e = half ? (wide  ? dfl::prepare<__half, float, true>(c->m)
+                            : sum ? dfl::prepare<__half, __half, true>(c->m)
+                                  : dfl::prepare<__half, __half, false>(c->m))
+                         : (wide  ? dfl::prepare<B16, float, true>(c->m)
+                            : sum ? dfl::prepare<B16, B16, true>(c->m)
+                                  : dfl::prepare<B16, B16, false>(c->m));
     dflash_status st = DFLASH_OK;
     if (e == cudaSuccess) {
         for (int i = 0; st == DFLASH_OK && i < dfl::kLanes / 8; ++i)
@@ -1095,8 +1113,8 @@ extern "C" dflash_status dflash_linear_run(dflash_linear_handle h, const void *x
     p.boxes = pl.boxes;
     p.stages = pl.stages;
     p.KB = static_cast<int>((k + dfl::kBox * pl.boxes - 1) / (dfl::kBox * pl.boxes));
-    // (results in 32 bits: an accumulator takes 512 columns)
-    p.seg = h->cfg.out_dtype == DFLASH_FP32 ? 8 / pl.boxes : p.KB;
+    // (columns of an accumulator: 512 for results in 32 bits, 4096 for long sums in 16)
+    p.seg = !dfl::sums(h->cfg) ? p.KB : (size == 4 ? 8 : 64) / pl.boxes;
     p.F = pl.F;
     const int F = pl.pair ? 2 * pl.F : pl.F;
     p.tiles_f = static_cast<int>((n + F - 1) / F);
@@ -1114,10 +1132,14 @@ extern "C" dflash_status dflash_linear_run(dflash_linear_handle h, const void *x
     p.ahead = residual && pl.split == 1 && !dfl::misaligned(residual, 16) && (rows == 1 || residual_stride * size % 16 == 0);
     p.err = h->err;
     const auto s = static_cast<cudaStream_t>(stream);
-    const bool half = h->cfg.dtype == DFLASH_FP16, wide = size == 4;
-    const cudaError_t e = half ? (wide ? dfl::launch<__half, float>(pl, p, s) : dfl::launch<__half, __half>(pl, p, s))
-                               : (wide ? dfl::launch<__nv_bfloat16, float>(pl, p, s)
-                                       : dfl::launch<__nv_bfloat16, __nv_bfloat16>(pl, p, s));
+    const bool half = h->cfg.dtype == DFLASH_FP16, wide = size == 4, sum = dfl::sums(h->cfg);
+    using B16 = __nv_bfloat16;
+    const cudaError_t e = half ? (wide  ? dfl::launch<__half, float, true>(pl, p, s)
+                                  : sum ? dfl::launch<__half, __half, true>(pl, p, s)
+                                        : dfl::launch<__half, __half, false>(pl, p, s))
+                               : (wide  ? dfl::launch<B16, float, true>(pl, p, s)
+                                  : sum ? dfl::launch<B16, B16, true>(pl, p, s)
+                                        : dfl::launch<B16, B16, false>(pl, p, s));
     if (e != cudaSuccess) {
         cudaGetLastError();
         return linear_fail(DFLASH_ERR_CUDA, "the product's launch failed (error %lld)", e);

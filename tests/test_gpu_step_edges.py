@@ -160,3 +160,23 @@ def test_changing_row_counts_cost_no_search(pkg):
         host([0, 1])
         same, changing = host([0, 0]), host([0, 1])
         assert changing < same + 15e-6, (same, changing)
+
+
+# ------------------------------------------------------------ long sums of the matrix product
+def signed(g, sign, *shape, dtype):
+    v = torch.rand(*shape, device="cuda", generator=g) if sign == "one sign" else torch.randn(*shape, device="cuda", generator=g) / 2
+    return (v * 2.0 ** -4).to(dtype)
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 200, 65544), (16, 129, 262144), (300, 128, 262144), (70, 513, 70000)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_long_sums_of_one_sign(pkg, rows, n, k, dtype):
+    """Results in 16 bits are within their rounding however long the sum: 256 steps of an accumulator of 4096 columns drop at most
+    (1 + .. + 256) / 256 = 128.5 times what one drops (2^-23 of the sum so far, and 2^-25 of it for each of 16 products), and 2^-23 for each sum of the pieces of a part."""
+    g = gen(k + rows)
+    x, w, bias, residual = (signed(g, "one sign", *shape, dtype=dtype) for shape in ((rows, k), (n, k), (n,), (rows, n)))
+    z = (x.double() @ w.double().T + bias.double()).clamp(min=0) + residual.double()
+    with pkg.Linear(w, bias, activation="relu") as layer:
+        y = layer(x, residual=residual).double()
+    off = ((y - z).abs() / z).max()
+    assert float(off) <= torch.finfo(dtype).eps / 2 * 1.001 + 128.5 * (2 ** -23 + 16 * 2 ** -25) + (k / 4096 + 12) * 2 ** -23
