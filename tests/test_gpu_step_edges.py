@@ -168,6 +168,25 @@ def signed(g, sign, *shape, dtype):
     return (v * 2.0 ** -4).to(dtype)
 
 
+@pytest.mark.parametrize("rows", [8, 300])
+@pytest.mark.parametrize("k", [16384, 32760])
+@pytest.mark.parametrize("dtype,sign", [(BF16, "one sign"), (BF16, "both signs"), (FP16, "one sign"), (FP16, "both signs")])
+def test_fp32_results_are_summed_in_short_pieces(pkg, rows, k, dtype, sign):
+    """The accumulator of up to 512 columns takes 32 steps of 16 products. A step drops less than 2^-23 of the sum so far, and of
+    each product what lies 2^-25 below the sum: nothing of a bf16 one (16 bits, at most 2^9 below the sum of 512), up to 2^-25 of
+    the sum of an fp16 one (22 bits). Over the steps of one sign that is at most (1 + .. + 32) / 32 = 16.5 times as much, of both
+    signs (sums that grow like the root) 21.6 times the sum's own part while the products' parts cancel; half of it on
+    average, and 2^-23 for the sums of the pieces. One accumulator for 2048 columns, an eighth of k, would be off by more than that."""
+    g = gen(k + rows)
+    x, w = signed(g, sign, rows, k, dtype=dtype), signed(g, sign, 520, k, dtype=dtype)
+    z = x.double() @ w.double().T
+    with pkg.Linear(w, out_dtype=FP32) as layer:
+        off = float((layer(x).double() - z).norm() / z.norm())
+    step = 2.0 ** -23 if sign == "both signs" or dtype is BF16 else 2.0 ** -23 + 16 * 2.0 ** -25
+    bound = (21.6 if sign == "both signs" else 16.5) * step / 2 + 2.0 ** -23
+    assert off <= bound, (off, bound)
+
+
 @pytest.mark.parametrize("rows,n,k", [(1, 200, 65544), (16, 129, 262144), (300, 128, 262144), (70, 513, 70000)])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 def test_long_sums_of_one_sign(pkg, rows, n, k, dtype):
