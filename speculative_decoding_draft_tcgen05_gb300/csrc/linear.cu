@@ -72,6 +72,11 @@ constexpr int kLanes = 128;    // of TMEM: the most weight rows of a CTA
 constexpr int kBox = 64;       // columns of a box: 128 bytes
 constexpr int kMaxSplit = 8;
 constexpr int kPlans = 256;    // that a handle remembers
+// The least shared memory of a CTA in a cluster: more than half an SM's. CTAs of a cluster wait for one another with tensor
+// memory in their hands, so two clusters must never hold parts of the same two SMs and wait for the rest; one such CTA to an
+// SM rules that out. (Their registers do so today, against this kernel and the library's others with tensor memory: 320
+// threads of 151 take 48,640 of 65,536.)
+constexpr int kAlone = 117 * 1024;
 constexpr int kMaxSum = 128;   // rows of x of a tile whose results are summed in registers
 constexpr int64_t kLong = 65536;  // columns, above which results in 16 bits are summed there too
 
@@ -893,7 +898,8 @@ template <typename T, typename Y, bool kSum>
 cudaError_t launch(const Plan &pl, const LinearParams &p, cudaStream_t s)
 {
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config(pl.grid, (pl.pair ? 2 : 1) * pl.split, smem_of(pl), s, attr);
+    const int size = (pl.pair ? 2 : 1) * pl.split, smem = smem_of(pl);
+    const cudaLaunchConfig_t cfg = config(pl.grid, size, size > 1 && smem < kAlone ? kAlone : smem, s, attr);
     return pl.pair ? cudaLaunchKernelEx(&cfg, linear_kernel<true, T, Y, kSum>, p) : cudaLaunchKernelEx(&cfg, linear_kernel<false, T, Y, kSum>, p);
 }
 

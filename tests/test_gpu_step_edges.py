@@ -199,3 +199,46 @@ def test_long_sums_of_one_sign(pkg, rows, n, k, dtype):
         y = layer(x, residual=residual).double()
     off = ((y - z).abs() / z).max()
     assert float(off) <= torch.finfo(dtype).eps / 2 * 1.001 + 128.5 * (2 ** -23 + 16 * 2 ** -25) + (k / 4096 + 12) * 2 ** -23
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 1, 8), (3, 129, 16384), (8, 520, 70000), (65, 300, 4096), (300, 513, 2568), (700, 128, 33000), (4097, 640, 328)])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (FP16, FP16), (BF16, FP32), (FP16, FP32)])
+def test_whole_numbers_are_exact(pkg, rows, n, k, dtype, out):
+    """Sums of products of -1, 0 and 1 fit any accumulator, so that a column that is lost or taken twice shows."""
+    g = gen(rows + k)
+    x, w = (torch.randint(-1, 2, shape, device="cuda", generator=g).to(dtype) for shape in ((rows, k), (n, k)))
+    with pkg.Linear(w, out_dtype=out) as layer:
+        assert torch.equal(layer(x), (x.double() @ w.double().T).to(out))
+
+
+# ------------------------------------------------------------ calls at the same time
+def test_clusters_of_several_calls_at_the_same_time(pkg):
+    """Pairs, clusters that share k, single CTAs and the logits' clusters of 16 on four streams: each as if alone."""
+    g = gen(9)
+
+    def product(rows, n, k, **kw):
+        x, w = torch.randn(rows, k, device="cuda", generator=g).to(BF16), (torch.randn(n, k, device="cuda", generator=g) / 50).to(BF16)
+        layer = pkg.Linear(w, **kw)
+        y = torch.empty(rows, n, device="cuda", dtype=kw.get("out_dtype") or BF16)
+        return (lambda stream: layer(x, y, stream=stream)), y, layer
+    logits = torch.randn(2, 8, 151936, device="cuda", generator=g).to(BF16)
+    tokens = torch.randint(0, 151936, (2, 500), device="cuda", generator=g, dtype=INT32)
+    rules = pkg.LogitsRules(tokens, torch.full((2,), 500, device="cuda", dtype=INT32), repetition=torch.full((2,), 1.3, device="cuda"))
+    probs = torch.empty(2, 8, 151936, device="cuda")
+    work = [product(300, 5120, 2560), product(256, 2560, 2560), product(8, 2560, 2560), product(200, 128, 640, out_dtype=FP32),
+            (lambda stream: pkg.dflash_logits_adjust(logits, rules, probs=probs, stream=stream), probs, None), product(2000, 1280, 640, activation="silu"),
+            product(40, 20000, 512), product(16, 64, 4096)]
+    want = []
+    for call, y, _ in work:
+        call(None)
+        want.append(y.clone())
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for turn in range(30):
+        for i, (call, _, _) in enumerate(work):
+            call(streams[i % 4])
+    torch.cuda.synchronize()
+    for (_, y, layer), z in zip(work, want):
+        assert torch.equal(y, z)
+        if layer is not None:
+            layer.sync_status()
