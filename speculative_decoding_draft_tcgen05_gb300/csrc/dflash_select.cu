@@ -68,6 +68,19 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
+// Encodes a tensor map. The driver's call wants a current context, which a thread that has not used the GPU does not have yet:
+// selecting its device makes it one.
+template <typename... Args>
+CUresult encode(EncodeTiledFn fn, Args... args)
+{
+    CUresult r = fn(args...);
+    int dev = 0;
+    if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = fn(args...);
+    return r;
+}
+
 // bf16 [rows, cols] row-major, tiles of 64 columns x box_rows rows, 128B swizzle,
 // rows past the end read as zero.
 dflash_status make_tmap(CUtensorMap *tm, const void *ptr, int64_t rows, int64_t cols, int box_rows)
@@ -78,8 +91,8 @@ dflash_status make_tmap(CUtensorMap *tm, const void *ptr, int64_t rows, int64_t 
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(dfl::kLmTileK), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    CUresult r = encode(fn, tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a [%lld, %lld] tensor", static_cast<int>(r),
@@ -112,7 +125,7 @@ dflash_status host_make_tmap_rows(CUtensorMap *tm, const void *ptr, int64_t rows
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
     cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+    CUresult r = encode(fn, tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -140,7 +153,7 @@ dflash_status host_make_tmap_pages(CUtensorMap *tm, const void *ptr, int bytes, 
                              static_cast<cuuint64_t>(page_stride) * bytes};
     cuuint32_t box[4] = {static_cast<cuuint32_t>(bytes == 2 ? 64 : head_dim), static_cast<cuuint32_t>(box_rows), 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = fn(tm, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+    CUresult r = encode(fn, tm, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                     const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

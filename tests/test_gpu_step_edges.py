@@ -1,6 +1,7 @@
 """The operators around a step's attention where calls meet: logits that do not
 arrive, outputs that lie in one buffer with inputs, two calls at once, changing
 row counts, long sums."""
+import threading
 import time
 
 import pytest
@@ -242,3 +243,59 @@ def test_clusters_of_several_calls_at_the_same_time(pkg):
         assert torch.equal(y, z)
         if layer is not None:
             layer.sync_status()
+
+
+def in_threads(*calls):
+    """Runs every call in a thread of its own, all at once; raises what the first of them raised."""
+    raised = []
+
+    def one(call):
+        try:
+            call()
+        except BaseException as e:
+            raised.append(e)
+    threads = [threading.Thread(target=one, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if raised:
+        raise raised[0]
+
+
+def test_a_threads_first_use_of_the_gpu(pkg):
+    """A thread that has not used the GPU calls operators that make tensor maps."""
+    w, x = torch.randn(128, 64, device="cuda").to(BF16), torch.randn(40, 64, device="cuda").to(BF16)
+    y = torch.zeros(40, 128, device="cuda", dtype=BF16)
+    cache = pkg.PagedCache(*(torch.randn(8, 16, 2, 64, device="cuda").to(BF16) for _ in range(2)))
+    batch = pkg.PagedBatch(torch.tensor([0, 40], device="cuda", dtype=INT32), torch.tensor([100], device="cuda", dtype=INT32),
+                           torch.arange(8, device="cuda", dtype=INT32).view(1, 8), max_tokens=40)
+    q = torch.randn(40, 4, 64, device="cuda").to(BF16)
+    a = torch.zeros_like(q)
+    with pkg.Linear(w) as layer, pkg.PagedAttention(heads=4, kv_heads=2, head_dim=64, page_size=16, dtype=BF16, max_batch=1) as attention:
+        torch.cuda.synchronize()
+        in_threads(lambda: layer(x, y), lambda: attention.attend(cache, batch, q, a))
+        torch.cuda.synchronize()
+        assert torch.equal(y, layer(x)) and torch.equal(a, attention.attend(cache, batch, q))
+
+
+def test_one_handle_by_two_threads(pkg):
+    """Two threads call one handle with row counts of their own, each on its stream."""
+    w = (torch.randn(640, 1280, device="cuda", generator=gen(1)) / 36).to(BF16)
+    x = torch.randn(520, 1280, device="cuda", generator=gen(2)).to(BF16)
+    counts = ((1, 257, 33, 513, 5), (256, 1, 512, 7, 261))
+    with pkg.Linear(w) as layer:
+        want = {n: layer(x[:n]) for c in counts for n in c}
+        torch.cuda.synchronize()
+        wrong = []
+
+        def calls(mine):
+            stream = torch.cuda.Stream()
+            outs = []
+            for _ in range(40):
+                for n in mine:
+                    outs.append((n, layer(x[:n], torch.empty(n, 640, device="cuda", dtype=BF16), stream=stream)))
+            stream.synchronize()
+            wrong.extend(n for n, y in outs if not torch.equal(y, want[n]))
+        in_threads(*(lambda c=c: calls(c) for c in counts))
+        assert not wrong
