@@ -299,3 +299,66 @@ def test_one_handle_by_two_threads(pkg):
             wrong.extend(n for n, y in outs if not torch.equal(y, want[n]))
         in_threads(*(lambda c=c: calls(c) for c in counts))
         assert not wrong
+
+
+# ------------------------------------------------------------ the ends of the sizes
+@pytest.mark.parametrize("n,k", [(1, 1), (5, 1), (130, 3), (1, 7), (64, 65)])
+@pytest.mark.parametrize("rows", [1, 9, 70])
+def test_products_of_few_columns(pkg, rows, n, k):
+    """Rows of x and W that start on 16 bytes, with fewer columns than that or an odd number of them."""
+    x, w = (torch.randint(-4, 5, (m, 72), device="cuda", generator=gen(m)).to(BF16)[:, :k] for m in (rows, n))
+    for out in (BF16, FP32):
+        with pkg.Linear(w, out_dtype=out) as layer:
+            assert torch.equal(layer(x), (x.double() @ w.double().T).to(out))
+
+
+def test_results_beyond_31_bits(pkg):
+    rows, n = 47000, 46000  # 2.16e9 values
+    x, w = (torch.randint(-2, 3, (m, 64), device="cuda", generator=gen(m)).to(BF16) for m in (rows, n))
+    with pkg.Linear(w) as layer:
+        y = layer(x)
+        for part in (slice(0, 300), slice(rows // 2 - 1, rows // 2 + 200), slice(rows - 500, rows)):
+            assert torch.equal(y[part], (x[part].double() @ w.double().T).to(BF16))
+        z = torch.ones_like(y)
+        layer(x, z, residual=z)
+        for part in (slice(0, 300), slice(rows - 500, rows)):
+            assert torch.equal(z[part], ((x[part].double() @ w.double().T) + 1).to(BF16))
+
+
+def test_logits_beyond_31_bits(pkg):
+    B, V = 14200, 151936  # 2.16e9 values
+    logits = torch.zeros(B, 1, V, device="cuda", dtype=BF16)
+    at = torch.randint(0, V, (B,), device="cuda", generator=gen(1))
+    logits[torch.arange(B, device="cuda"), 0, at] = 1
+    best = torch.empty(B, 1, device="cuda", dtype=INT32)
+    tokens = at.to(INT32).view(B, 1)
+    pkg.dflash_logits_adjust(logits, argmax=best)
+    assert torch.equal(best.view(-1), at.to(INT32))
+    rules = pkg.LogitsRules(tokens, torch.ones(B, device="cuda", dtype=INT32), presence=torch.full((B,), 3.0, device="cuda"))
+    pkg.dflash_logits_adjust(logits, rules, out=logits, argmax=best)  # in place: the one token falls to -2
+    assert torch.equal(best.view(-1), (at == 0).to(INT32))
+    assert (logits[torch.arange(B, device="cuda"), 0, at] == -2).all() and not logits[-1, 0, : int(at[-1])].any()
+
+
+def test_the_largest_batch_of_pages(pkg):
+    B, page = 65536, 3
+    pool = pkg.PagePool.empty(requests=B + 7, cols=4, num_pages=3 * B, page_size=page)
+    rows = torch.randperm(B + 7, device="cuda", generator=gen(1))[:B].to(INT32)
+    new = torch.randint(0, 2 * page + 1, (B,), device="cuda", generator=gen(2), dtype=INT32)
+    total = int(new.sum())
+    positions, slots = torch.full((total,), -1, device="cuda", dtype=INT32), torch.full((total,), -1, device="cuda", dtype=torch.int64)
+    batch = pkg.PagedBatch(torch.zeros(B + 1, device="cuda", dtype=INT32), torch.zeros(B, device="cuda", dtype=INT32),
+                           torch.full((B, 4), -1, device="cuda", dtype=INT32), max_tokens=2 * page)
+    granted = torch.zeros(B, device="cuda", dtype=INT32)
+    pool.extend(batch, new, rows=rows, positions=positions, slots=slots, granted=granted)
+    take = (new + page - 1) // page
+    cu = torch.cumsum(new, 0)
+    assert granted.all() and torch.equal(batch.tensors[0][1:], cu.to(INT32)) and torch.equal(pool.lens[rows.long()], new)
+    of = torch.repeat_interleave(torch.arange(B, device="cuda"), new.long())
+    at = torch.arange(total, device="cuda") - (cu - new)[of]
+    first = torch.cumsum(take, 0) - take  # (pages are taken from 0 on)
+    assert torch.equal(positions.long(), at) and torch.equal(slots, (first[of] + at // page) * page + at % page)
+    assert pool.counters.tolist() == [3 * B - int(take.sum()), 0]
+    pool.trim(new, rows=rows)
+    assert not pool.lens.any() and pool.counters.tolist() == [3 * B, 0]
+    assert torch.equal(pool.free_pages, torch.arange(3 * B - 1, -1, -1, device="cuda", dtype=INT32))
