@@ -6,15 +6,16 @@
 // boxes of 64 columns.
 //
 // Few rows are bound by the stream of W, each weight read once. One SM takes in
-// some 60 GB/s from HBM whatever it has in flight, so all of them have to
-// stream: a CTA takes as few weight rows (F, a multiple of 8) as gives every SM
-// its share, and a cluster of up to 8 CTAs can split a tile's k; they join their
-// sums through distributed shared memory in the order of their ranks, so that
-// results do not depend on timing. The products' other lanes then hold what
-// happens to lie behind the tile, and nobody reads them. Many rows are bound by
-// the tensor cores: persistent CTA pairs on tiles of 256 x NT with two
-// accumulators in TMEM, so that a tile's epilogue runs beside the next one's
-// products.
+// some 60 GB/s from HBM whatever it has in flight, so many of them have to
+// stream: a CTA takes fewer weight rows than 128 (F, a multiple of 8), or a
+// cluster of up to 8 CTAs splits a tile's k, as far as the cost of a CTA and of
+// the join allows (8 rows, 2560 x 2560: 100 CTAs of 128 weight rows and a fifth
+// of k). The CTAs of a cluster join their sums through distributed shared
+// memory in the order of their ranks, so that results do not depend on timing.
+// The products' other lanes then hold what happens to lie behind the tile, and
+// nobody reads them. Many rows are bound by the tensor cores: persistent CTA
+// pairs on tiles of 256 x NT with two accumulators in TMEM, so that a tile's
+// epilogue runs beside the next one's products.
 //
 // The tensor cores' fp32 accumulator truncates, at every 16 columns its sum and
 // what lies more than some 25 bits below it of their products. Values of one
@@ -465,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         __syncwarp();
         pol_w = p.tiles_t == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
         pol_x = p.tiles_t == 1 ? l2_policy_evict_last() : l2_policy_evict_normal();
-        // W is constant from the handle's creation on: its first loads overlap the previous kernel on the stream
+        // W is constant from the handle's creation on: its first loads overlap the previous kernel on the stream, on SMs
+        // that have room beside it
         if constexpr (!kPair)
             for (int i = 0; i < pre; ++i) load_w(i, first_feature(tf0), kb0 + i);
     }
@@ -799,7 +801,7 @@ bool fit_stages(Plan &pl, int KB64, const Machine &m)
 {
     const int need = (KB64 + pl.split - 1) / pl.split;
     const int box = static_cast<int>(layout(pl.F, pl.NT, 1, 1, pl.pair, pl.split, 0, 0).stage);
-    // stages of up to 4 boxes and 32 KB: fewer barriers, and longer pieces of W's rows
+    // stages of up to 4 boxes and 40 KB: fewer barriers, and longer pieces of W's rows
     pl.boxes = 1;
     while (pl.boxes < 4 && 2 * pl.boxes * box <= 40 * 1024 && 4 * pl.boxes <= need) pl.boxes *= 2;
     const int KB = (KB64 + pl.boxes - 1) / pl.boxes;
@@ -818,7 +820,8 @@ bool fit_stages(Plan &pl, int KB64, const Machine &m)
 }
 
 // A plan's time in microseconds but for a constant: a fit to 3,000 plans of 35 shapes (1 to 12,000 rows, n 128 to
-// 151,936, k 512 to 16,000), by which the chosen plan is 2 % slower than the fastest on average and 12 % at most.
+// 151,936, k 512 to 16,000), by which the chosen plan is 2 % slower than the fastest on average and 12 % at most. (The
+// constants are what the fit gave; its timings were not kept.)
 // (Above `most` only some number above it, without the roots.)
 double cost(const Plan &pl, int64_t rows, int64_t n, int64_t k, int KB64, int64_t items, double most)
 {

@@ -12,11 +12,11 @@
 // over all the others: the first finds the best token and, relative to each
 // thread's running maximum, the sum of the exponentials; the warps of all CTAs
 // send those to all CTAs (st.async, counted by an mbarrier of the receiver: a
-// cluster barrier in its place cost 1.5 us a position, 120 us against 105 for 32
+// cluster barrier in its place cost 1.5 us a position, 120 us against 106 for 32
 // sequences of 8); the second writes the probabilities. HBM sees the logits and
 // the outputs once, which is what bounds a large batch (without penalties 3.9
-// TB/s of 238 MB); with them the lists' chains do (105 us against 59), and a
-// small call the chain history -> table -> list -> exchange (9.3 us).
+// TB/s of 238 MB); with them the lists' chains do (106 us against 60), and a
+// small call the chain history -> table -> list -> exchange (9.5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdio.h>

@@ -6,8 +6,8 @@ cache (``include/dflash_pages.h``).
 The functions have the names of the C entry points and only marshal arguments.
 ``Linear`` owns a layer's handle; ``LogitsRules`` and ``PagePool`` hold the C
 structures of what stays the same from call to call. Tensors that they hold are
-read by later calls: what changes in them is seen, but they must not be freed
-or moved.
+read by later calls: what changes in the tensors of rules and pools is seen, a
+layer's weights must stay as they are, and none may be freed or moved.
 """
 from __future__ import annotations
 
@@ -131,7 +131,8 @@ def dflash_linear_destroy(handle):
 
 
 class Linear:
-    """Owns a layer's handle and keeps its weights alive (convenience only)."""
+    """Owns a layer's handle and keeps its weights alive (convenience only). The weights must not change: a call may begin
+    to read them before what was launched ahead of it has ended."""
 
     def __init__(self, weight, bias=None, *, activation=None, out_dtype=None, stream=None):
         self.h = None
