@@ -41,8 +41,9 @@ typedef struct {
     int32_t requests, cols, page_size, num_pages;
 } dflash_page_pool;
 
-/* Entry b of the batch is request rows[b] (distinct; NULL: b itself), which
- * gets new_tokens[b] >= 0 tokens behind those that it has. Entries are served
+/* Entry b of the batch is request rows[b] (NULL: b itself; distinct among the
+ * entries with new tokens, so that others may pad a batch), which gets
+ * new_tokens[b] >= 0 tokens behind those that it has. Entries are served
  * in order while pages and `tokens` last: entry b is refused, and gets nothing,
  * if the entries up to and including it need more than the free pages or have
  * more than `tokens` new tokens together (so are all after it that follow in
@@ -68,8 +69,8 @@ dflash_status dflash_pages_extend(const dflash_page_pool *pool, const int32_t *r
                                   int64_t table_stride, int32_t table_cols, int32_t *positions, int64_t *slots,
                                   int32_t *granted, void *stream);
 
-/* Request rows[b] (distinct; NULL: b itself) loses its last d tokens, at most
- * those that it has (none with d <= 0, or for a row out of range):
+/* Request rows[b] (NULL: b itself; distinct among those that lose something)
+ * loses its last d tokens, at most those that it has (none with d <= 0, or for a row out of range):
  *   d = counts[b]           with base < 0;
  *   d = base - counts[b]    with base >= 0: base = L and the accept lengths of
  *                           dflash_verify_prefix drop a block's rejected drafts;

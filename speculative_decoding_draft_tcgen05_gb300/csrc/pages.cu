@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(R) pages_extend_kernel(const __grid_constant__
         const bool ok = total + g <= free && done + h <= p.tokens;
         const int n = block_count<R>(ok);
         if (t == n - 1) s.before_a = total + g, s.before_b = done + h;
-        if (ok && q.valid) p.pool.lens[q.row] = q.len + q.tokens;
+        if (ok && q.valid && q.tokens > 0) p.pool.lens[q.row] = q.len + q.tokens;  // (an entry that pads the batch may name any request)
         block_sync<R>();
         if (n > 0) total = s.before_a, done = s.before_b;
         block_sync<R>();
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(R) pages_trim_kernel(const __grid_constant__ P
     if (gridDim.x > 1 && !s.last) return;
     for (int r = 0; r < p.ranges; ++r) {
         const Entry q = r == range ? e : entry_of<true>(p, r * R + t);
-        if (q.row >= 0) p.pool.lens[q.row] = q.tokens;
+        if (q.row >= 0 && q.tokens != q.len) p.pool.lens[q.row] = q.tokens;
     }
     if (t == 0) {
         p.pool.counters[0] = free + count;

@@ -131,6 +131,23 @@ def test_a_batch_in_the_columns_beside_the_pools(pkg):
         pool.extend(pkg.PagedBatch(batch.tensors[0], batch.tensors[1], wide[:, 7:15], max_tokens=1), torch.ones(4, device="cuda", dtype=INT32))
 
 
+@pytest.mark.parametrize("B", [5, 200, 2500])
+def test_a_batch_padded_with_a_request_that_it_has(pkg, B):
+    """Entries without new tokens, and those that lose none, may name the request of another entry: it keeps what that one does."""
+    pool = pkg.PagePool.empty(requests=B, cols=4, num_pages=4 * B, page_size=16)
+    pool.extend(None, torch.full((B,), 20, device="cuda", dtype=INT32))
+    for real in (0, B // 2, B - 1):  # one entry does something, before, between or behind those that pad
+        rows = torch.full((B,), 3, device="cuda", dtype=INT32)
+        counts = torch.zeros(B, device="cuda", dtype=INT32)
+        counts[real] = 17
+        positions = torch.full((17,), -1, device="cuda", dtype=INT32)
+        for _ in range(20):
+            pool.extend(None, counts, rows=rows, positions=positions)
+            assert int(pool.lens[3]) == 37 and positions.tolist() == list(range(20, 37)) and pool.counters.tolist() == [2 * B - 1, 0]
+            pool.trim(counts, rows=rows)
+            assert int(pool.lens[3]) == 20 and pool.counters.tolist() == [2 * B, 0]
+
+
 # ------------------------------------------------------------ row counts that change from call to call
 def test_a_handle_with_changing_row_counts(pkg):
     """Results are those of a handle that has seen no other row count (rows 5, 261, 517, .. share a remembered plan's place)."""
