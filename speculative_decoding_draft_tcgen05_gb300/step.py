@@ -218,11 +218,20 @@ def dflash_logits_adjust(logits, rules=None, *, out=None, probs=None, argmax=Non
 
 def dflash_selftest_logits_lost(logits, rules=None, *, out=None, probs=None, argmax=None, rank, at, stream=None):
     """Self-test of the waits of dflash_logits_adjust: the logits of one CTA do not arrive from its position `at` on."""
-    L, check, get_stream = _binding()
+    torch = _torch()
+    if logits.dim() != 3:
+        raise ValueError(f"logits must have 3 dimensions, got {tuple(logits.shape)}")
+    for name, t, shape, dtype in (("logits", logits, logits.shape, logits.dtype), ("out", out, logits.shape, logits.dtype),
+                                  ("probs", probs, logits.shape, torch.float32), ("argmax", argmax, logits.shape[:2], torch.int32)):
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.shape != shape or t.dtype is not dtype):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if rules is not None and rules.spec[1] not in (-1, logits.shape[0]):
+        raise ValueError(f"the rules are for {rules.spec[1]} sequences, the logits for {logits.shape[0]}")
     dev = _one_device(logits=logits, out=out, probs=probs, argmax=argmax)
-    if dev != _torch().cuda.current_device() or any(t is not None and not t.is_contiguous() for t in (logits, out, probs, argmax)):
-        raise ValueError("tensors must be contiguous and on the current device")
-    code = {_torch().bfloat16: DFLASH_BF16, _torch().float16: DFLASH_FP16, _torch().float32: DFLASH_FP32}.get(logits.dtype, -1)
+    if dev != torch.cuda.current_device() or (rules is not None and rules.spec[2] not in (-1, dev)):
+        raise ValueError("the tensors must be on the current device")
+    L, check, get_stream = _binding()
+    code = {torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_FP16, torch.float32: DFLASH_FP32}.get(logits.dtype, -1)
     at_of = [None if t is None else t.data_ptr() for t in (out, probs, argmax)]
     check(L.dflash_selftest_logits_lost(logits.data_ptr(), *logits.shape, code, None if rules is None else ctypes.byref(rules.c),
                                         *at_of, rank, at, get_stream(stream)), "dflash_selftest_logits_lost")

@@ -71,6 +71,20 @@ def test_logits_that_do_not_arrive(pkg, want, rank, at):
     assert all(y is None or torch.equal(bad[name], y) for name, y in good.items())
 
 
+def test_the_self_test_refuses_what_does_not_fit(pkg):
+    logits, best = torch.zeros(2, 3, 64, device="cuda"), torch.zeros(2, 3, device="cuda", dtype=INT32)
+    lose = pkg.dflash_selftest_logits_lost
+    for x, kw in ((logits[0], {}), (logits[:, ::2], {}), (logits.cpu(), {}), (logits, dict(argmax=best[:1])), (logits, dict(argmax=best.long())),
+                  (logits, dict(out=logits.half())), (logits, dict(probs=torch.zeros(2, 3, 65, device="cuda"))),
+                  (logits, dict(argmax=best, rules=pkg.LogitsRules(temperature=torch.ones(1, device="cuda"))))):
+        with pytest.raises(ValueError):
+            lose(x, rank=0, at=0, **kw)
+    with pytest.raises(pkg.DflashError, match="rank"):
+        lose(logits, argmax=best, rank=-1, at=0)
+    lose(logits, argmax=best, rank=3, at=0)  # (no such CTA: nothing is lost)
+    assert not best.any()
+
+
 # ------------------------------------------------------------ logits and outputs in one buffer
 @pytest.mark.parametrize("V", [512, 515])
 def test_logits_into_other_slices_of_their_buffer(pkg, V):
